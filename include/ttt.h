@@ -382,6 +382,138 @@ int ttt_mlp_fwd_ex(const void* K, const void* Q, const void* V,
                    void* workspace, size_t workspace_bytes,
                    void* stream, int plan);
 
+/* ------------------------------------------------------------------------ */
+/* Gated linear recurrence                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* The recurrence of a gated sequence layer, one scalar state per channel:
+ *   h_t = exp(g_t) h_{t-1} + x_t,   z_t = h_t,   t = 0 .. T-1,
+ * over [B, H, T, d] like the scan above, every (batch, head, feature) a channel of
+ * its own.  g_t is the logarithm of the gate: it carries gates close to 1 in bf16,
+ * where the gate itself could not.
+ *   - g_t <= 0 is required.  Values above 0 are not checked; the results are then
+ *     unspecified (no access depends on them).
+ *   - g_t = -inf forgets: h_t = x_t whatever h_{t-1} is, infinite and NaN included.
+ *     Documents packed in one row start anew that way.
+ *   - g_t = 0 with x_t = 0 carries the state through (padding of a shorter sequence:
+ *     h_out is then the state at its own end).
+ * Arithmetic is fp32 whatever the I/O type; every output is the same bits on every
+ * call.
+ *   X, G    : [B, H, T, d] in io_dtype.
+ *   h0      : [B, H, d] fp32 state before the first token, or NULL for zero.
+ *   Z       : [B, H, T, d] in io_dtype (output; must not overlap an input).
+ *   h_out   : [B, H, d] fp32 state after the last token (may alias h0), or NULL.
+ *   d >= 1 (any), T >= 1; all pointers 16-byte aligned.
+ *   workspace : at least ttt_gated_workspace_bytes(...) bytes, 256-byte aligned (NULL
+ *           where that is 0).  Calls that may overlap in time need one each, graph
+ *           replays included; its contents need not be kept between calls. */
+int ttt_gated_fwd(const void* X, const void* G, const float* h0, void* Z, float* h_out,
+                  int B, int H, int T, int d, int io_dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_gated_fwd and ttt_gated_bwd need for this shape (0 for few
+ * tokens, and for shapes they refuse). */
+size_t ttt_gated_workspace_bytes(int B, int H, int T, int d, int io_dtype);
+
+/* Streaming continuation (decode): n more tokens of every sequence, the state updated
+ * in place.  The same as ttt_gated_fwd from h0 = h to h_out = h; no workspace, so n is
+ * meant to be small (any n >= 1 is right).
+ *   X, G, Z : [B, H, n, d] in io_dtype;  h : [B, H, d] fp32. */
+int ttt_gated_step(const void* X, const void* G, float* h, void* Z,
+                   int B, int H, int n, int d, int io_dtype, void* stream);
+
+/* Backward pass (vector-Jacobian product) of ttt_gated_fwd: the gradients of
+ * L = <dZ, Z> + <dh_T, h_out>.  With lambda_T = dh_T,
+ *   lambda_t = dz_t + exp(g_{t+1}) lambda_{t+1}   (g_T taken as 0),
+ *   dx_t = lambda_t,   dg_t = exp(g_t) lambda_t h_{t-1},   dh0 = exp(g_0) lambda_0,
+ * where a gate of g_t = -inf gives dg_t = 0 and passes nothing back.
+ *   G       : as given to ttt_gated_fwd.
+ *   Z       : what ttt_gated_fwd returned (h_{t-1} is read from it, in io_dtype).
+ *   h0      : as given to ttt_gated_fwd (NULL for zero).
+ *   dZ      : [B, H, T, d] in io_dtype;  dh_T : [B, H, d] fp32 or NULL for zero.
+ *   dX, dG  : [B, H, T, d] in io_dtype (outputs).
+ *   dh0     : [B, H, d] fp32 (output), or NULL.
+ * Outputs must not overlap inputs or each other.  Workspace as ttt_gated_fwd. */
+int ttt_gated_bwd(const void* G, const void* Z, const float* h0, const void* dZ,
+                  const float* dh_T, void* dX, void* dG, float* dh0,
+                  int B, int H, int T, int d, int io_dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Root-mean-square norm with the residual's addition                        */
+/* ------------------------------------------------------------------------ */
+
+/* Over each of `rows` rows of D features:
+ *   r = x + residual,   y = r / sqrt(mean(r^2) + eps) * weight.
+ * The sum, the mean and y are formed in fp32 from the unrounded r (sums of squares past
+ * fp32's range give the k = 0 of an infinite mean).
+ *   X        : [rows, D] in io_dtype.
+ *   residual : [rows, D] in io_dtype, or NULL (r = x).
+ *   weight   : [D] fp32, or NULL for ones.
+ *   Y        : [rows, D] in io_dtype (output; may alias X).
+ *   R        : [rows, D] in io_dtype (output: r, the residual of what follows; may alias
+ *              residual or X, but not Y), or NULL to leave it out.
+ *   eps      : > 0, finite.  rows >= 0 (0 does nothing), D >= 1; X, residual, Y and R
+ *              16-byte aligned, weight 4-byte. */
+int ttt_rmsnorm_fwd(const void* X, const void* residual, const float* weight, float eps,
+                    void* Y, void* R, long long rows, int D, int io_dtype, void* stream);
+
+/* The same with y in 8-bit floating point (OCP e4m3: largest value 448) and one scale
+ * per row: scale = max|y| / 448, Y8 = y / scale rounded to nearest even.  A row of zeros
+ * has scale 0 and Y8 0; a row whose r has a NaN or an infinity in it has a NaN scale, and
+ * its Y8 is NaN throughout.
+ *   Y8 : [rows, D] bytes (16-byte aligned);  scale : [rows] fp32. */
+int ttt_rmsnorm_q8_fwd(const void* X, const void* residual, const float* weight, float eps,
+                       void* Y8, float* scale, void* R, long long rows, int D, int io_dtype,
+                       void* stream);
+
+/* Backward pass of ttt_rmsnorm_fwd.  With k = 1 / sqrt(mean(r^2) + eps), n = k r and
+ * u = dy * weight:
+ *   dx = k (u - n mean(u n)) + dr,   dweight = sum over the rows of dy n.
+ * dx is the gradient for x and for the residual alike.
+ *   R        : [rows, D] in io_dtype, r as the forward pass stored it (X where there was
+ *              no residual).
+ *   dY       : [rows, D] in io_dtype.
+ *   dR       : [rows, D] in io_dtype, the gradient that reaches r by itself, or NULL.
+ *   dX       : [rows, D] in io_dtype (output; may alias dY or dR).
+ *   dweight  : [D] fp32 (output), or NULL.
+ *   workspace: at least ttt_rmsnorm_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ *              (may be NULL when dweight is NULL).
+ * The rows' terms of dweight are added in a fixed order: the same bits on every call. */
+int ttt_rmsnorm_bwd(const void* R, const float* weight, const void* dY, const void* dR,
+                    float eps, void* dX, float* dweight, long long rows, int D, int io_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_rmsnorm_bwd needs for this shape (0 for shapes it refuses). */
+size_t ttt_rmsnorm_bwd_workspace_bytes(long long rows, int D, int io_dtype);
+
+/* ------------------------------------------------------------------------ */
+/* Gradient norm over many tensors, and clipping                             */
+/* ------------------------------------------------------------------------ */
+
+/* norm = sqrt(sum of the squares of every element of every tensor), in fp64, and
+ *   outs[i] = grads[i] * min(1, max_norm / (norm + eps)).
+ * A norm that is not finite scales as the formula says (NaN: everything NaN; inf: finite
+ * elements 0): the caller looks at *norm.
+ *   n        : number of tensors, >= 0.  The four arrays are HOST arrays of n entries,
+ *              read before the call returns.
+ *   grads    : device pointers, contiguous, aligned to their element.
+ *   outs     : device pointers; outs[i] may be grads[i] (in place), else it overlaps no
+ *              tensor of the call; or NULL for the norm alone.  No two outputs overlap
+ *              (TTT_ERR_INVALID_ARG), so a gradient that is listed twice is refused.
+ *   sizes    : elements of each (0 allowed);  dtypes : ttt_dtype of each.
+ *   max_norm : >= 0 (inf allowed);  eps : > 0, finite.
+ *   norm     : DEVICE fp32 [1] (output).
+ *   workspace: at least ttt_clip_workspace_bytes() bytes, 256-byte aligned; one for each
+ *              call that may overlap in time.
+ * Sums run in a fixed order: the same bits on every call. */
+int ttt_clip_grad_norm(int n, const void* const* grads, void* const* outs,
+                       const long long* sizes, const int* dtypes, float max_norm, float eps,
+                       float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_clip_grad_norm needs, whatever the tensors. */
+size_t ttt_clip_workspace_bytes(void);
+
 /* Static string for a ttt_status value (or "unknown status"). */
 const char* ttt_status_string(int status);
 

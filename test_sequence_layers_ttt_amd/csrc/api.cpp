@@ -10,13 +10,12 @@
 #include <mutex>
 
 #include "ttt.h"
+#include "host_checks.h"
 #include "launch.h"
 
 using namespace ttt;
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool dims_ok(int B, int H, int T, int d, int chunk)
 {
@@ -74,8 +73,6 @@ int mlp_plan(int B, int H, int T, int d, int chunk, int io_dtype, int plan)
     }
     return mfma ? TTT_PLAN_MFMA : TTT_PLAN_GENERIC;
 }
-
-int launch_status(hipError_t e) { return e == hipSuccess ? TTT_OK : TTT_ERR_LAUNCH; }
 
 // Workspace of ttt_linear_fwd_noalloc: one static array per GPU, held until the
 // process ends.  Host code never passes `scratch` itself to a kernel (on the host

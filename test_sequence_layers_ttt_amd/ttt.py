@@ -28,6 +28,9 @@ EXPORTS = ("ttt_linear_workspace_bytes", "ttt_linear_workspace_bytes_ex",
            "ttt_linear_noalloc_scratch_bytes",
            "ttt_mlp_workspace_bytes", "ttt_mlp_workspace_bytes_ex", "ttt_mlp_select_plan",
            "ttt_mlp_fwd", "ttt_mlp_fwd_ex",
+           "ttt_gated_workspace_bytes", "ttt_gated_fwd", "ttt_gated_step", "ttt_gated_bwd",
+           "ttt_rmsnorm_fwd", "ttt_rmsnorm_q8_fwd", "ttt_rmsnorm_bwd",
+           "ttt_rmsnorm_bwd_workspace_bytes", "ttt_clip_grad_norm", "ttt_clip_workspace_bytes",
            "ttt_status_string", "ttt_plan_name")
 
 
@@ -96,6 +99,27 @@ def lib() -> ctypes.CDLL:
         L.ttt_mlp_fwd_ex.argtypes = [vp, vp, vp, vp, f, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                      i, i, i, i, i, i, vp, sz, vp, i]
         L.ttt_mlp_fwd_ex.restype = i
+        ll = ctypes.c_longlong
+        L.ttt_gated_workspace_bytes.argtypes = [i] * 5
+        L.ttt_gated_workspace_bytes.restype = sz
+        L.ttt_gated_fwd.argtypes = [vp] * 5 + [i] * 5 + [vp, sz, vp]
+        L.ttt_gated_fwd.restype = i
+        L.ttt_gated_step.argtypes = [vp] * 4 + [i] * 5 + [vp]
+        L.ttt_gated_step.restype = i
+        L.ttt_gated_bwd.argtypes = [vp] * 8 + [i] * 5 + [vp, sz, vp]
+        L.ttt_gated_bwd.restype = i
+        L.ttt_rmsnorm_fwd.argtypes = [vp, vp, vp, f, vp, vp, ll, i, i, vp]
+        L.ttt_rmsnorm_fwd.restype = i
+        L.ttt_rmsnorm_q8_fwd.argtypes = [vp, vp, vp, f, vp, vp, vp, ll, i, i, vp]
+        L.ttt_rmsnorm_q8_fwd.restype = i
+        L.ttt_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, f, vp, vp, ll, i, i, vp, sz, vp]
+        L.ttt_rmsnorm_bwd.restype = i
+        L.ttt_rmsnorm_bwd_workspace_bytes.argtypes = [ll, i, i]
+        L.ttt_rmsnorm_bwd_workspace_bytes.restype = sz
+        L.ttt_clip_grad_norm.argtypes = [i, vp, vp, vp, vp, f, f, vp, vp, sz, vp]
+        L.ttt_clip_grad_norm.restype = i
+        L.ttt_clip_workspace_bytes.argtypes = []
+        L.ttt_clip_workspace_bytes.restype = sz
         L.ttt_status_string.argtypes = [i]
         L.ttt_status_string.restype = ctypes.c_char_p
         L.ttt_plan_name.argtypes = [i]
@@ -455,3 +479,286 @@ def mlp_fwd(K, Q, V, eta, W1, b1, W2, b2, chunk: int, eta_scalar: float = 0.0, *
     if rc != OK:
         raise TTTError(rc, "ttt_mlp_fwd")
     return Z, W1_out, b1_out, W2_out, b2_out
+
+
+# ---- operators around the scan: gated recurrence, RMS norm, gradient clipping ----
+
+def _match(t, name, shape, dtype, device):
+    """_check for the operators below: also on one device."""
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _first(t, name):
+    """Checks the tensor that the others are held to; returns its ttt_dtype."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return _io_dtype(t)
+
+
+class _On:
+    """The device and stream a call runs on: the tensors' device is made current, and
+    what the call allocates belongs to its stream (so a workspace that it drops is
+    not handed out to another stream while the call still runs)."""
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self):
+        import torch
+        if self.stream is not None:
+            guard = torch.cuda.stream(self.stream)   # sets its device too
+            if self.stream.device != self.device:
+                raise ValueError("the stream belongs to %s, the tensors to %s"
+                                 % (self.stream.device, self.device))
+        elif torch.cuda.current_device() != self.device.index:
+            guard = torch.cuda.device(self.device)
+        else:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        guard.__enter__()
+        self.guards = (guard,)
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
+
+
+def gated_workspace_bytes(B, H, T, d, io_dtype) -> int:
+    return int(lib().ttt_gated_workspace_bytes(B, H, T, d, io_dtype))
+
+
+def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None) -> Tuple:
+    """Gated linear recurrence h_t = exp(G_t) h_{t-1} + X_t over [B, H, T, d] fp32 or
+    bf16 (G <= 0; -inf starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
+    (Z, h_T): the states in the I/O type, and the last one in fp32."""
+    import torch
+    B, H, T, d = X.shape
+    io, dev = _first(X, "X"), X.device
+    _match(G, "G", X.shape, X.dtype, dev)
+    if h0 is not None:
+        _match(h0, "h0", (B, H, d), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if Z is None:
+            Z = torch.empty_like(X)
+        else:
+            _match(Z, "Z", X.shape, X.dtype, dev)
+        if h_out is None:
+            h_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+        else:
+            _match(h_out, "h_out", (B, H, d), torch.float32, dev)
+        L = lib()
+        ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), dev, workspace)
+        rc = L.ttt_gated_fwd(X.data_ptr(), G.data_ptr(), _ptr(h0), Z.data_ptr(),
+                             h_out.data_ptr(), B, H, T, d, io, _ptr(ws),
+                             0 if ws is None else ws.numel(), st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_gated_fwd")
+    return Z, h_out
+
+
+def gated_step(X, G, h, *, Z=None, stream=None):
+    """Continue gated recurrences by the n tokens of X, G [B, H, n, d] from the state h
+    [B, H, d] fp32, which is updated in place.  Returns Z."""
+    import torch
+    B, H, n, d = X.shape
+    io, dev = _first(X, "X"), X.device
+    _match(G, "G", X.shape, X.dtype, dev)
+    _match(h, "h", (B, H, d), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if Z is None:
+            Z = torch.empty_like(X)
+        else:
+            _match(Z, "Z", X.shape, X.dtype, dev)
+        rc = lib().ttt_gated_step(X.data_ptr(), G.data_ptr(), h.data_ptr(), Z.data_ptr(),
+                                  B, H, n, d, io, st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_gated_step")
+    return Z
+
+
+def gated_bwd(G, Z, dZ, h0=None, dh_T=None, *, dX=None, dG=None, dh0=None, workspace=None,
+              stream=None) -> Tuple:
+    """Gradients of <dZ, Z> + <dh_T, h_T> through Z, h_T = gated_fwd(X, G, h0).  Z is the
+    forward call's; h0 and dh_T: [B, H, d] fp32 or None (zero).  Returns (dX, dG, dh0)."""
+    import torch
+    B, H, T, d = G.shape
+    io, dev = _first(G, "G"), G.device
+    _match(Z, "Z", G.shape, G.dtype, dev)
+    _match(dZ, "dZ", G.shape, G.dtype, dev)
+    for t, name in ((h0, "h0"), (dh_T, "dh_T"), (dh0, "dh0")):
+        if t is not None:
+            _match(t, name, (B, H, d), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if dX is None:
+            dX = torch.empty_like(G)
+        else:
+            _match(dX, "dX", G.shape, G.dtype, dev)
+        if dG is None:
+            dG = torch.empty_like(G)
+        else:
+            _match(dG, "dG", G.shape, G.dtype, dev)
+        if dh0 is None:
+            dh0 = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+        L = lib()
+        ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), dev, workspace)
+        rc = L.ttt_gated_bwd(G.data_ptr(), Z.data_ptr(), _ptr(h0), dZ.data_ptr(), _ptr(dh_T),
+                             dX.data_ptr(), dG.data_ptr(), dh0.data_ptr(), B, H, T, d, io,
+                             _ptr(ws), 0 if ws is None else ws.numel(), st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_gated_bwd")
+    return dX, dG, dh0
+
+
+def _rms_args(X, weight, residual):
+    import torch
+    if X.dim() == 0:
+        raise ValueError("X needs a feature axis")
+    io, dev, D = _first(X, "X"), X.device, X.shape[-1]
+    if weight is not None:
+        _match(weight, "weight", (D,), torch.float32, dev)
+    if residual is not None:
+        _match(residual, "residual", X.shape, X.dtype, dev)
+    return io, dev, D, X.numel() // D if D else 0
+
+
+def rmsnorm_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y=None, R=None,
+                stream=None) -> Tuple:
+    """RMS norm over the last axis with the residual's addition: r = X + residual,
+    y = r / sqrt(mean(r^2) + eps) * weight.  X, residual: [..., D] fp32 or bf16; weight:
+    [D] fp32 or None.  Returns (Y, R): R is r, or None without a residual (unless a
+    tensor for it is given)."""
+    import torch
+    io, dev, D, rows = _rms_args(X, weight, residual)
+    with _On(dev, stream) as st:
+        if Y is None:
+            Y = torch.empty_like(X)
+        else:
+            _match(Y, "Y", X.shape, X.dtype, dev)
+        if R is not None:
+            _match(R, "R", X.shape, X.dtype, dev)
+        elif residual is not None:
+            R = torch.empty_like(X)
+        rc = lib().ttt_rmsnorm_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps,
+                                   Y.data_ptr(), _ptr(R), rows, D, io, st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_rmsnorm_fwd")
+    return Y, R
+
+
+def rmsnorm_q8_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y8=None, scale=None,
+                   R=None, stream=None) -> Tuple:
+    """rmsnorm_fwd with y in 8-bit floating point (torch.float8_e4m3fn) and one fp32 scale
+    per row: y = Y8 * scale.  Returns (Y8, scale, R)."""
+    import torch
+    io, dev, D, rows = _rms_args(X, weight, residual)
+    with _On(dev, stream) as st:
+        if Y8 is None:
+            Y8 = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=dev)
+        else:
+            _match(Y8, "Y8", X.shape, torch.float8_e4m3fn, dev)
+        if scale is None:
+            scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=dev)
+        else:
+            _match(scale, "scale", X.shape[:-1], torch.float32, dev)
+        if R is not None:
+            _match(R, "R", X.shape, X.dtype, dev)
+        elif residual is not None:
+            R = torch.empty_like(X)
+        rc = lib().ttt_rmsnorm_q8_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps,
+                                      Y8.data_ptr(), scale.data_ptr(), _ptr(R), rows, D, io, st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_rmsnorm_q8_fwd")
+    return Y8, scale, R
+
+
+def rmsnorm_bwd_workspace_bytes(rows, D, io_dtype) -> int:
+    return int(lib().ttt_rmsnorm_bwd_workspace_bytes(rows, D, io_dtype))
+
+
+def rmsnorm_bwd(R, weight, dY, dR=None, eps: float = 1e-6, *, dX=None, dweight=None,
+                want_dweight: bool = True, workspace=None, stream=None) -> Tuple:
+    """Gradients through rmsnorm_fwd.  R: the r it returned (X where there was no
+    residual); dR: the gradient that reaches r by itself, or None.  Returns (dX, dweight):
+    dX is the gradient for X and for the residual, dweight [D] fp32 (None when
+    want_dweight is False)."""
+    import torch
+    io, dev, D, rows = _rms_args(R, weight, None)
+    _match(dY, "dY", R.shape, R.dtype, dev)
+    if dR is not None:
+        _match(dR, "dR", R.shape, R.dtype, dev)
+    with _On(dev, stream) as st:
+        if dX is None:
+            dX = torch.empty_like(R)
+        else:
+            _match(dX, "dX", R.shape, R.dtype, dev)
+        if dweight is not None:
+            _match(dweight, "dweight", (D,), torch.float32, dev)
+        elif want_dweight:
+            dweight = torch.empty(D, dtype=torch.float32, device=dev)
+        L = lib()
+        ws = None
+        if dweight is not None:
+            ws = _workspace(L.ttt_rmsnorm_bwd_workspace_bytes(rows, D, io), dev, workspace)
+        rc = L.ttt_rmsnorm_bwd(R.data_ptr(), _ptr(weight), dY.data_ptr(), _ptr(dR), eps,
+                               dX.data_ptr(), _ptr(dweight), rows, D, io, _ptr(ws),
+                               0 if ws is None else ws.numel(), st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_rmsnorm_bwd")
+    return dX, dweight
+
+
+def clip_workspace_bytes() -> int:
+    return int(lib().ttt_clip_workspace_bytes())
+
+
+def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm=None,
+                   workspace=None, stream=None) -> Tuple:
+    """The 2-norm over all tensors of the list `grads` (fp32 or bf16, any contiguous
+    shapes, one device), and each of them times min(1, max_norm / (norm + eps)).  outs:
+    the list of tensors to write, which may be grads itself (in place); None makes new
+    ones.  Returns (outs, norm): norm is a [1] fp32 device tensor."""
+    import torch
+    n = len(grads)
+    if n == 0 and norm is None:
+        raise ValueError("no gradients, and no tensor for the norm")
+    dev = grads[0].device if n else norm.device
+    dtypes = (ctypes.c_int * n)()
+    sizes = (ctypes.c_longlong * n)()
+    gp = (ctypes.c_void_p * n)()
+    op = (ctypes.c_void_p * n)()
+    for k, g in enumerate(grads):
+        dtypes[k] = _first(g, "grads[%d]" % k)
+        if g.device != dev:
+            raise ValueError("grads[%d] is on %s, expected %s" % (k, g.device, dev))
+        sizes[k] = g.numel()
+        gp[k] = g.data_ptr()
+    if norm is not None:
+        _match(norm, "norm", (1,), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if outs is None:
+            outs = [torch.empty_like(g) for g in grads]
+        if len(outs) != n:
+            raise ValueError("%d outputs for %d gradients" % (len(outs), n))
+        for k, (o, g) in enumerate(zip(outs, grads)):
+            if o is not g:
+                _match(o, "outs[%d]" % k, g.shape, g.dtype, dev)
+            op[k] = o.data_ptr()
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=dev)
+        L = lib()
+        ws = _workspace(L.ttt_clip_workspace_bytes(), dev, workspace)
+        rc = L.ttt_clip_grad_norm(n, gp, op, sizes, dtypes, max_norm, eps, norm.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), st)
+    if rc != OK:
+        raise TTTError(rc, "ttt_clip_grad_norm")
+    return outs, norm
