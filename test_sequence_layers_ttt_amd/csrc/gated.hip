@@ -1,96 +1,636 @@
-// Gated linear recurrence: h_t = exp(g_t) h_{t-1} + x_t per channel, and its backward
-// pass.  Simplest form: one thread per (row, feature), serial over the tokens.
+// Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel, and its backward pass.
+//
+// The step h -> exp(g) h + x is affine, and affine maps compose: a run of tokens is the
+// pair (sum of its g, B) with h_end = exp(sum g) h_start + B.  The gates' product is kept
+// as the sum of the g: -inf then marks a run with a reset in it, exactly, where a product
+// that underflowed would look the same.
+//
+// A tile is all that one workgroup holds in registers: `rows` runs of L tokens over the
+// channels of one block, each thread a run of L tokens of V neighbouring channels (16
+// bytes).  Every input is read once:
+//   1. each thread reduces its run to its pair;
+//   2. the pairs of the tile's runs are scanned in LDS (threads as channel x part);
+//   3. the tile publishes its pair, takes the state before it from the tiles before, and
+//      publishes the state after it;
+//   4. each thread runs its tokens again from its own start state and writes them.
+// Step 3 is a chain along the sequence.  Tiles take their place in it by a ticket, so a
+// tile only ever waits for tiles that run already.  The words they pass on are 32 or 64
+// bits wide, written whole and read until they are there (an unwritten word is all ones,
+// which no published value is): no fence, no flag.  The state that enters a tile is
+// always carried left to right, one tile's pair after another, so it has the same bits
+// however many of the tiles before had published their state.
+//
+// The backward pass is the same chain from the other end: lambda_t = dz_t + exp(g_{t+1})
+// lambda_{t+1}; then dx_t = lambda_t and dg_t = exp(g_t) lambda_t h_{t-1}.
 #include <stdint.h>
 
-#include <cmath>
+#include <algorithm>
 
-#include "device_common.h"
 #include "block_launch.h"
+#include "device_common.h"
+#include "mfma_common.h"
 
 namespace ttt {
 namespace {
 
-// exp(g) h, with a gate of -inf passing nothing on (infinities and NaN included)
-__device__ __forceinline__ float decay(float g, float h)
-{
-    return g == -INFINITY ? 0.f : expf(g) * h;
-}
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kShut = -__builtin_inff();   // the summed g of a run with a reset in it
+constexpr int kThreads = 256;
+constexpr int kWindow = 8;                   // tiles looked back over at once
+constexpr int kMostPolls = 1 << 22;          // seconds: only a workspace in use twice gets there
 
-template <typename TIO>
-__global__ __launch_bounds__(256) void gated_fwd_kernel(const TIO* __restrict__ X,
-                                                        const TIO* __restrict__ G, const float* h0,
-                                                        TIO* __restrict__ Z, float* h_out,
-                                                        long long channels, int T, int d)
-{
-    const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (c >= channels) return;
-    const size_t row = c / d, f = c - row * d;
-    float h = h0 ? h0[c] : 0.f;
-    size_t i = row * T * d + f;
-    for (int t = 0; t < T; ++t, i += d) {
-        h = decay(io<TIO>::load(G, i), h) + io<TIO>::load(X, i);
-        io<TIO>::store(Z, i, h);
+// V elements of the I/O type at any element-aligned address, as raw words
+template <typename TIO, int V>
+struct Raw {
+    static constexpr int BYTES = V * (int)sizeof(TIO);
+    static constexpr int WORDS = (BYTES + 3) / 4;
+    struct __attribute__((packed, aligned(sizeof(TIO)))) Mem { TIO e[V]; };
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const TIO* p)
+    {
+        const Mem m = *reinterpret_cast<const Mem*>(p);
+        if constexpr (BYTES < 4) w[0] = m.e[0];
+        else __builtin_memcpy(w, &m, BYTES);
     }
-    if (h_out) h_out[c] = h;
+    __device__ __forceinline__ void store(TIO* p) const
+    {
+        Mem m;
+        if constexpr (BYTES < 4) m.e[0] = (TIO)w[0];
+        else __builtin_memcpy(&m, w, BYTES);
+        *reinterpret_cast<Mem*>(p) = m;
+    }
+    // the elements from `skip` on
+    __device__ __forceinline__ void store_from(TIO* p, int skip) const
+    {
+        if (skip == 0) return store(p);
+        Mem m;
+        if constexpr (BYTES < 4) m.e[0] = (TIO)w[0];
+        else __builtin_memcpy(&m, w, BYTES);
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+            if (i >= skip) p[i] = m.e[i];
+    }
+    // hides that the words are the ones a first pass has used: the second computes its
+    // gates again instead of keeping the first one's in registers
+    __device__ __forceinline__ void again()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int i) const
+    {
+        if constexpr (sizeof(TIO) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+    }
+    __device__ __forceinline__ void put(const float (&v)[V])
+    {
+        if constexpr (sizeof(TIO) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+        } else if constexpr (V == 1) {
+            w[0] = f32_to_bf16_bits(v[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+                w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
+        }
+    }
+};
+
+// one token: g2 = g log2(e)
+__device__ __forceinline__ float token(float g2, float x, float h)
+{
+    return fmaf(__builtin_amdgcn_exp2f(g2), g2 == kShut ? 0.f : h, x);
 }
 
-template <typename TIO>
-__global__ __launch_bounds__(256) void gated_bwd_kernel(
+// one run: (S, B) with S the summed g2.  The factor of an open run is kept above 0, so that an
+// infinite state stays one.
+__device__ __forceinline__ float run(float S, float B, float h)
+{
+    return S == kShut ? B : fmaf(fmaxf(__builtin_amdgcn_exp2f(S), 1.2e-38f), h, B);
+}
+
+// how the channels of a row lie over workgroups and threads (host and device)
+struct Layout {
+    int V;        // channels of a thread
+    int lanes;    // threads over the channels of a block
+    int rows;     // runs of a tile
+    int blocks;   // channel blocks of a row
+    int parts;    // parts that the scan over the runs is split into
+    int per;      // runs of a part
+    int width;    // lanes * V: channel slots of a block
+};
+
+Layout layout_of(int d, bool bf16)
+{
+    Layout y;
+    y.V = bf16 ? 8 : 4;
+    while (y.V > d) y.V >>= 1;
+    const int groups = (d + y.V - 1) / y.V, most = kThreads / y.V;
+    y.blocks = (groups + most - 1) / most;
+    y.lanes = (groups + y.blocks - 1) / y.blocks;
+    y.rows = kThreads / y.lanes;
+    y.width = y.lanes * y.V;
+    y.parts = std::min(kThreads / y.width, y.rows);
+    y.per = (y.rows + y.parts - 1) / y.parts;
+    return y;
+}
+
+constexpr int kRunFwd = 8, kRunBwd = 8;      // tokens of a thread's run
+
+// Workspace of a chain: tickets [sequences], then per (sequence, tile) the states after
+// it [width] and its pairs [width] as 64-bit words.  A sequence here is one channel block
+// of one row.
+struct Chain {
+    unsigned* ticket;
+    unsigned* state;
+    unsigned long long* pair;
+};
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t chain_bytes(long long seqs, long long tiles, int width, Chain* c, void* ws)
+{
+    const size_t t = up256(4 * (size_t)seqs), n = (size_t)seqs * tiles * width;
+    if (c) {
+        unsigned char* p = (unsigned char*)ws;
+        c->ticket = (unsigned*)p;
+        c->state = (unsigned*)(p + t);
+        c->pair = (unsigned long long*)(p + t + up256(4 * n));
+    }
+    return t + up256(4 * n) + up256(8 * n);
+}
+
+// tickets to 0, everything else to all ones
+__global__ __launch_bounds__(kThreads) void gated_clear_kernel(uint4* p, size_t zeros, size_t n)
+{
+    for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n;
+         i += (size_t)gridDim.x * kThreads) {
+        const unsigned v = i < zeros ? 0u : 0xffffffffu;
+        p[i] = make_uint4(v, v, v, v);
+    }
+}
+
+__device__ __forceinline__ unsigned word_of(float v)   // never all ones
+{
+    return v != v ? 0x7fc00000u : __float_as_uint(v);
+}
+
+__device__ __forceinline__ unsigned get32(const unsigned* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ unsigned long long get64(const unsigned long long* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that enters tile j > 0 of one channel: `state` and `pair` point at tile 0's words of
+// the channel, `width` apart from tile to tile.
+__device__ __forceinline__ float look_back(const unsigned* state, const unsigned long long* pair,
+                                           int j, int width)
+{
+    for (int poll = 0; poll < kMostPolls; ++poll) {
+        unsigned s[kWindow];
+        unsigned long long p[kWindow];
+#pragma unroll
+        for (int k = 0; k < kWindow; ++k) {
+            const size_t at = (size_t)max(j - 1 - k, 0) * width;
+            s[k] = get32(state + at);
+            p[k] = get64(pair + at);
+        }
+        // the nearest tile with a state, and pairs all the way from it
+        int from = -1;
+        bool open = true;
+#pragma unroll
+        for (int k = 0; k < kWindow; ++k) {
+            open = open && j - 1 - k >= 0;
+            if (open && s[k] != 0xffffffffu) {
+                from = k;
+                open = false;
+            }
+            open = open && p[k] != ~0ull;
+        }
+        if (from >= 0) {
+            float h = 0.f;
+#pragma unroll
+            for (int k = kWindow - 1; k >= 0; --k) {
+                if (k == from) h = __uint_as_float(s[k]);
+                else if (k < from)
+                    h = run(__uint_as_float((unsigned)p[k]), __uint_as_float((unsigned)(p[k] >> 32)), h);
+            }
+            return h;
+        }
+        __builtin_amdgcn_s_sleep(2);
+    }
+    return __builtin_nanf("");
+}
+
+struct Tile {
+    int seq, j;        // sequence (row, channel block) and place of the tile in it
+    int row;           // of the input
+    int r, lane;       // this thread's run and channel group
+    int c0;            // its first channel
+    int skip;          // how many of them the group before has as well
+    bool on;           // it has any
+
+    // channel of a slot of the block, or -1
+    __device__ __forceinline__ int channel(const Layout& y, int d, int slot) const
+    {
+        const int g = (seq - row * y.blocks) * y.lanes + slot / y.V;
+        return g * y.V < d ? min(g * y.V, d - y.V) + slot % y.V : -1;
+    }
+};
+
+// A workgroup's tile; j < 0: there is none left (a workspace in use twice).
+__device__ __forceinline__ Tile take_tile(const Layout& y, int d, int tiles, int seqs,
+                                          const Chain& chain, int* lds)
+{
+    Tile t;
+    t.seq = blockIdx.x % seqs;
+    t.j = 0;
+    if (tiles > 1) {
+        if (threadIdx.x == 0)
+            *lds = (int)__hip_atomic_fetch_add(chain.ticket + t.seq, 1u, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        t.j = *lds;
+        if ((unsigned)t.j >= (unsigned)tiles) t.j = -1;
+    }
+    t.row = t.seq / y.blocks;
+    t.r = threadIdx.x / y.lanes;
+    t.lane = threadIdx.x - t.r * y.lanes;
+    const int group = (t.seq - t.row * y.blocks) * y.lanes + t.lane;
+    // The last group of a row whose width V does not divide starts early enough to be whole: the
+    // channels it shares with the group before are computed by both, to the same bits.
+    t.c0 = min(group * y.V, d - y.V);
+    t.skip = group * y.V - t.c0;
+    t.on = t.r < y.rows && group * y.V < d;
+    return t;
+}
+
+// The start state of each thread's run, from its pairs (S, B) and the states that enter the
+// sequence (`first` of the row's channels, or nullptr for zero).
+template <int V>
+__device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int d, int tiles,
+                                             const Chain& chain, const float* first,
+                                             const float (&S)[V], const float (&B)[V],
+                                             float (&h)[V])
+{
+    __shared__ float sS[kThreads * V], sB[kThreads * V], pS[kThreads], pB[kThreads];
+    const int w = y.width, tid = threadIdx.x;
+    if (t.r < y.rows) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sS[t.r * w + t.lane * V + i] = t.on ? S[i] : 0.f;
+            sB[t.r * w + t.lane * V + i] = t.on ? B[i] : 0.f;
+        }
+    }
+    __syncthreads();
+    // threads as (part, channel): each part's runs in turn, exclusive pairs left in place
+    const int part = tid / w, c = tid - part * w;
+    const bool scans = part < y.parts;
+    if (scans) {
+        float s = 0.f, b = 0.f;
+        const int end = min((part + 1) * y.per, y.rows);
+        for (int r = part * y.per; r < end; ++r) {
+            const float ts = sS[r * w + c], tb = sB[r * w + c];
+            sS[r * w + c] = s;
+            sB[r * w + c] = b;
+            b = run(ts, tb, b);
+            s = ts == kShut ? kShut : s + ts;
+        }
+        pS[tid] = s;
+        pB[tid] = b;
+    }
+    __syncthreads();
+    if (part == 0) {
+        // the tile's pair, then the state before it, then every part's start
+        float s = 0.f, b = 0.f, h = 0.f;
+        const size_t at0 = (size_t)t.seq * tiles * w + c, at = at0 + (size_t)max(t.j, 0) * w;
+        for (int p = 0; p < y.parts; ++p) {
+            const float ts = pS[p * w + c], tb = pB[p * w + c];
+            b = run(ts, tb, b);
+            s = ts == kShut ? kShut : s + ts;
+        }
+        if (t.j > 0) {
+            if (t.j + 1 < tiles)
+                __hip_atomic_store(chain.pair + at,
+                                   (unsigned long long)word_of(b) << 32 | word_of(s),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            h = look_back(chain.state + at0, chain.pair + at0, t.j, w);
+        } else if (first) {
+            const int ch = t.channel(y, d, c);
+            if (ch >= 0) h = first[ch];
+        }
+        if (t.j + 1 < tiles)
+            __hip_atomic_store(chain.state + at, word_of(run(s, b, h)), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        for (int p = 0; p < y.parts; ++p) {
+            const float ts = pS[p * w + c], tb = pB[p * w + c];
+            pB[p * w + c] = h;
+            h = run(ts, tb, h);
+        }
+    }
+    __syncthreads();
+    if (t.on) {
+        const int p = t.r / y.per;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int k = t.r * w + t.lane * V + i;
+            h[i] = run(sS[k], sB[k], pB[p * w + t.lane * V + i]);
+        }
+    }
+}
+
+// own: the states are updated in place, so a channel is written by one group alone (the
+// other group's copy may have started from what was written).
+template <typename TIO, int V>
+__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(
+    const TIO* __restrict__ X, const TIO* __restrict__ G, const float* h0, TIO* __restrict__ Z,
+    float* h_out, int T, int d, int tiles, int seqs, Layout y, Chain chain, bool own)
+{
+    constexpr int L = kRunFwd;
+    __shared__ int ticket;
+    const Tile t = take_tile(y, d, tiles, seqs, chain, &ticket);
+    if (t.j < 0) return;
+    const long long t0 = ((long long)t.j * y.rows + t.r) * L;
+    const int n = t.on ? (int)min(max(T - t0, 0ll), (long long)L) : 0;
+    const size_t at = ((size_t)t.row * T + t0) * d + t.c0;
+
+    Raw<TIO, V> x[L], g[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        x[l].zero();
+        g[l].zero();
+        if (l < n) {
+            g[l].load(G + at + (size_t)l * d);
+            x[l].load(X + at + (size_t)l * d);
+        }
+    }
+    float S[V], B[V], h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) S[i] = B[i] = 0.f;
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float g2 = g[l].at(i) * kLog2e;
+            B[i] = token(g2, x[l].at(i), B[i]);
+            S[i] = g2 == kShut ? kShut : S[i] + g2;
+        }
+    start_states<V>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, S, B, h);
+    const int skip = own ? t.skip : 0;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        if (l >= n) break;
+        g[l].again();
+        x[l].again();
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = token(g[l].at(i) * kLog2e, x[l].at(i), h[i]);
+        Raw<TIO, V> z;
+        z.put(h);
+        z.store_from(Z + at + (size_t)l * d, skip);
+    }
+    if (h_out && n > 0 && t0 + n == T) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i >= skip) h_out[(size_t)t.row * d + t.c0 + i] = h[i];
+    }
+}
+
+template <typename TIO, int V>
+__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(
     const TIO* __restrict__ G, const TIO* __restrict__ Z, const float* __restrict__ h0,
     const TIO* __restrict__ dZ, const float* __restrict__ dh_T, TIO* __restrict__ dX,
-    TIO* __restrict__ dG, float* __restrict__ dh0, long long channels, int T, int d)
+    TIO* __restrict__ dG, float* __restrict__ dh0, int T, int d, int tiles, int seqs, Layout y,
+    Chain chain)
 {
-    const long long c = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (c >= channels) return;
-    const size_t row = c / d, f = c - row * d, base = row * T * d + f;
-    float carry = dh_T ? dh_T[c] : 0.f;   // exp(g_{t+1}) lambda_{t+1}
-    for (int t = T - 1; t >= 0; --t) {
-        const size_t i = base + (size_t)t * d;
-        const float lam = io<TIO>::load(dZ, i) + carry;
-        const float before = t > 0 ? io<TIO>::load(Z, i - d) : (h0 ? h0[c] : 0.f);
-        const float g = io<TIO>::load(G, i);
-        carry = decay(g, lam);
-        io<TIO>::store(dX, i, lam);
-        io<TIO>::store(dG, i, g == -INFINITY ? 0.f : carry * before);
+    constexpr int L = kRunBwd;
+    __shared__ int ticket;
+    const Tile t = take_tile(y, d, tiles, seqs, chain, &ticket);
+    if (t.j < 0) return;
+    // this run's tokens, from the last one down: T - 1 - p0, ...
+    const long long p0 = ((long long)t.j * y.rows + t.r) * L;
+    const int n = t.on ? (int)min(max(T - p0, 0ll), (long long)L) : 0;
+    const size_t at = ((size_t)t.row * T + (T - 1 - p0)) * d + t.c0;
+    const bool first_token = n > 0 && p0 + n == T;   // the run ends with token 0
+
+    Raw<TIO, V> dz[L], g[L + 1], z[L];               // g[l]: the gate after token l's
+    g[0].zero();
+    if (n > 0 && p0 > 0) g[0].load(G + at + d);
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        dz[l].zero();
+        g[l + 1].zero();
+        z[l].zero();
+        if (l < n) {
+            dz[l].load(dZ + at - (size_t)l * d);
+            g[l + 1].load(G + at - (size_t)l * d);
+            if (p0 + l + 1 < T) z[l].load(Z + at - (size_t)(l + 1) * d);
+        }
     }
-    if (dh0) dh0[c] = carry;
+    float S[V], B[V], lam[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) S[i] = B[i] = 0.f;
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float g2 = g[l].at(i) * kLog2e;
+            B[i] = token(g2, dz[l].at(i), B[i]);
+            S[i] = g2 == kShut ? kShut : S[i] + g2;
+        }
+    start_states<V>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, S, B, lam);
+    g[0].again();
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        if (l >= n) break;
+        g[l + 1].again();
+        dz[l].again();
+        float dg[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            lam[i] = token(g[l].at(i) * kLog2e, dz[l].at(i), lam[i]);
+            float before = z[l].at(i);
+            if (first_token && l == n - 1) before = h0 ? h0[(size_t)t.row * d + t.c0 + i] : 0.f;
+            const float g2 = g[l + 1].at(i) * kLog2e;
+            const float back = token(g2, 0.f, lam[i]);
+            dg[i] = g2 == kShut ? 0.f : back * before;
+            if (dh0 && first_token && l == n - 1) dh0[(size_t)t.row * d + t.c0 + i] = back;
+        }
+        Raw<TIO, V> o;
+        o.put(lam);
+        o.store(dX + at - (size_t)l * d);
+        o.put(dg);
+        o.store(dG + at - (size_t)l * d);
+    }
 }
 
-unsigned blocks(long long channels) { return (unsigned)((channels + 255) / 256); }
+// Few tokens: a thread runs V channels through all of them, 8 tokens' loads at a time.
+template <typename TIO, int V>
+__global__ __launch_bounds__(kThreads) void gated_step_kernel(
+    const TIO* __restrict__ X, const TIO* __restrict__ G, const float* h0, TIO* __restrict__ Z,
+    float* h_out, int T, int d, int groups, long long n, bool own)
+{
+    constexpr int L = 8;
+    const long long k = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (k >= n) return;
+    const long long row = k / groups;
+    const int group = (int)(k - row * groups), c0 = min(group * V, d - V);
+    const int skip = own ? group * V - c0 : 0;
+    float h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = h0 ? h0[row * d + c0 + i] : 0.f;
+    size_t at = (size_t)row * T * d + c0;
+    for (int t0 = 0; t0 < T; t0 += L, at += (size_t)L * d) {
+        Raw<TIO, V> x[L], g[L];
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            if (t0 + l < T) {
+                g[l].load(G + at + (size_t)l * d);
+                x[l].load(X + at + (size_t)l * d);
+            }
+        }
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            if (t0 + l >= T) break;
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = token(g[l].at(i) * kLog2e, x[l].at(i), h[i]);
+            Raw<TIO, V> z;
+            z.put(h);
+            z.store_from(Z + at + (size_t)l * d, skip);
+        }
+    }
+    if (h_out) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i >= skip) h_out[row * d + c0 + i] = h[i];
+    }
+}
+
+long long tiles_of(const Layout& y, int T, int L) { return (T + (long long)y.rows * L - 1) / ((long long)y.rows * L); }
+
+// Sets up the chain of a call: the number of workgroups, or 0 where they would be too many.
+unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int& tiles, int& seqs,
+                 hipStream_t s)
+{
+    const long long nt = tiles_of(y, T, L), ns = (long long)BH * y.blocks;
+    if (nt * ns > 0x7fffffffll) return 0;
+    tiles = (int)nt;
+    seqs = (int)ns;
+    c = Chain{};
+    if (nt > 1) {
+        const size_t bytes = chain_bytes(ns, nt, y.width, &c, ws);
+        const size_t n = (bytes + 15) / 16, zeros = up256(4 * (size_t)ns) / 16;
+        hipLaunchKernelGGL(gated_clear_kernel,
+                           dim3((unsigned)std::min<size_t>(2048, (n + kThreads - 1) / kThreads)),
+                           dim3(kThreads), 0, s, (uint4*)ws, zeros, n);
+    }
+    return (unsigned)(nt * ns);
+}
+
+template <typename TIO, int V>
+hipError_t fwd_v(const GatedArgs& a, const Layout& y, hipStream_t s)
+{
+    Chain c;
+    int tiles, seqs;
+    const unsigned grid = prepare(y, a.BH, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
+    if (!grid) return hipErrorInvalidValue;
+    const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
+    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V>), dim3(grid), dim3(kThreads), 0, s,
+                       (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d, tiles,
+                       seqs, y, c, own);
+    return hipGetLastError();
+}
+
+template <typename TIO, int V>
+hipError_t step_v(const GatedArgs& a, hipStream_t s)
+{
+    const int groups = (a.d + V - 1) / V;
+    const long long n = (long long)a.BH * groups, grid = (n + kThreads - 1) / kThreads;
+    if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+    const bool own = a.h0 && a.h0 == a.h_out;
+    hipLaunchKernelGGL((gated_step_kernel<TIO, V>), dim3((unsigned)grid), dim3(kThreads), 0, s,
+                       (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d,
+                       groups, n, own);
+    return hipGetLastError();
+}
+
+template <typename TIO, int V>
+hipError_t bwd_v(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
+{
+    Chain c;
+    int tiles, seqs;
+    const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
+    if (!grid) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V>), dim3(grid), dim3(kThreads), 0, s,
+                       (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
+                       (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
+    return hipGetLastError();
+}
+
+// f(integral V) for the layout's V
+#define GATED_BY_WIDTH(V, call)                                                          \
+    switch (V) {                                                                         \
+    case 1: { constexpr int W = 1; return call; }                                        \
+    case 2: { constexpr int W = 2; return call; }                                        \
+    case 4: { constexpr int W = 4; return call; }                                        \
+    default: break;                                                                      \
+    }
 
 }  // namespace
 
-size_t gated_workspace(int, int, int, bool) { return 0; }
+size_t gated_workspace(int BH, int T, int d, bool bf16)
+{
+    const Layout y = layout_of(d, bf16);
+    size_t n = 0;
+    for (int L : {kRunFwd, kRunBwd}) {
+        const long long tiles = tiles_of(y, T, L);
+        if (tiles > 1)
+            n = std::max(n, chain_bytes((long long)BH * y.blocks, tiles, y.width, nullptr, nullptr));
+    }
+    return n;
+}
+
+hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s)
+{
+    const int V = layout_of(a.d, a.bf16).V;
+    if (a.bf16) {
+        GATED_BY_WIDTH(V, (step_v<uint16_t, W>(a, s)))
+        return step_v<uint16_t, 8>(a, s);
+    }
+    GATED_BY_WIDTH(V, (step_v<float, W>(a, s)))
+    return hipErrorInvalidValue;
+}
 
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s)
 {
-    const long long n = (long long)a.BH * a.d;
-    if (a.bf16)
-        hipLaunchKernelGGL(gated_fwd_kernel<uint16_t>, dim3(blocks(n)), dim3(256), 0, s,
-                           (const uint16_t*)a.X, (const uint16_t*)a.G, a.h0, (uint16_t*)a.Z,
-                           a.h_out, n, a.T, a.d);
-    else
-        hipLaunchKernelGGL(gated_fwd_kernel<float>, dim3(blocks(n)), dim3(256), 0, s,
-                           (const float*)a.X, (const float*)a.G, a.h0, (float*)a.Z, a.h_out, n,
-                           a.T, a.d);
-    return hipGetLastError();
+    if (a.T <= kRunFwd) return launch_gated_step(a, s);
+    const Layout y = layout_of(a.d, a.bf16);
+    if (a.bf16) {
+        GATED_BY_WIDTH(y.V, (fwd_v<uint16_t, W>(a, y, s)))
+        return fwd_v<uint16_t, 8>(a, y, s);
+    }
+    GATED_BY_WIDTH(y.V, (fwd_v<float, W>(a, y, s)))
+    return hipErrorInvalidValue;
 }
-
-hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s) { return launch_gated_fwd(a, s); }
 
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s)
 {
-    const long long n = (long long)a.BH * a.d;
-    if (a.bf16)
-        hipLaunchKernelGGL(gated_bwd_kernel<uint16_t>, dim3(blocks(n)), dim3(256), 0, s,
-                           (const uint16_t*)a.G, (const uint16_t*)a.Z, a.h0,
-                           (const uint16_t*)a.dZ, a.dh_T, (uint16_t*)a.dX, (uint16_t*)a.dG, a.dh0,
-                           n, a.T, a.d);
-    else
-        hipLaunchKernelGGL(gated_bwd_kernel<float>, dim3(blocks(n)), dim3(256), 0, s,
-                           (const float*)a.G, (const float*)a.Z, a.h0, (const float*)a.dZ, a.dh_T,
-                           (float*)a.dX, (float*)a.dG, a.dh0, n, a.T, a.d);
-    return hipGetLastError();
+    const Layout y = layout_of(a.d, a.bf16);
+    if (a.bf16) {
+        GATED_BY_WIDTH(y.V, (bwd_v<uint16_t, W>(a, y, s)))
+        return bwd_v<uint16_t, 8>(a, y, s);
+    }
+    GATED_BY_WIDTH(y.V, (bwd_v<float, W>(a, y, s)))
+    return hipErrorInvalidValue;
 }
 
 }  // namespace ttt
