@@ -1,161 +1,564 @@
-// Root-mean-square norm with the residual's addition: forward in the I/O type or in
-// e4m3 with one scale per row, and the backward pass.  Simplest form: one workgroup per
-// row, the row read again for each pass over it.
+// Root-mean-square norm with the residual's addition: forward in the I/O type or in e4m3
+// with one scale per row, and the backward pass.
+//
+// A row of D features is held in registers by TPR threads, K vectors of 16 bytes each, so
+// every input is read once and every output written once: HBM bounds it.  Rows of up to
+// 64 K vectors stay within one wave (sums by lane exchanges, no LDS, no barrier); longer
+// ones take a workgroup.  A last vector that would pass the row's end starts early enough
+// to be whole: what it shares with the one before is left out of the sums and written
+// twice, with the same bits.  (All of a row's loads come before its first store, so
+// outputs may stand at their inputs' places.)
+//
+// dweight sums over the rows: each thread adds up its own columns over its workgroup's
+// rows, the workgroup's threads of one column are added in LDS, and a second kernel adds
+// the workgroups' planes, all in a fixed order.
 #include <stdint.h>
 
-#include "device_common.h"
+#include <algorithm>
+
 #include "block_launch.h"
+#include "device_common.h"
+#include "mfma_common.h"
 
 namespace ttt {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
 
-// sum over the 256 threads, the same bits in every thread
-__device__ __forceinline__ float block_sum(float x, float* lds)
+typedef uint32_t quad __attribute__((ext_vector_type(4)));
+typedef quad quad_any __attribute__((aligned(2)));
+
+template <typename TIO> constexpr int kVec = 16 / (int)sizeof(TIO);
+
+// 16 bytes of the I/O type at any element-aligned address
+template <typename TIO>
+__device__ __forceinline__ quad load16(const TIO* p)
 {
-    for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return lds[0] + lds[1] + lds[2] + lds[3];
+    return __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(p));
+}
+
+template <typename TIO>
+__device__ __forceinline__ void store16(TIO* p, quad q)
+{
+    __builtin_nontemporal_store(q, reinterpret_cast<quad_any*>(p));
+}
+
+template <typename TIO>
+__device__ __forceinline__ void widen(quad q, float (&v)[kVec<TIO>])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(TIO) == 4) {
+            v[i] = __uint_as_float(q[i]);
+        } else {
+            v[2 * i] = __uint_as_float(q[i] << 16);
+            v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+        }
+    }
+}
+
+template <typename TIO>
+__device__ __forceinline__ quad narrow(const float (&v)[kVec<TIO>])
+{
+    quad q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(TIO) == 4) q[i] = __float_as_uint(v[i]);
+        else q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    return q;
 }
 
 // max with NaN winning
-__device__ __forceinline__ float nan_max(float a, float b) { return a != a ? a : b != b ? b : fmaxf(a, b); }
-
-__device__ __forceinline__ float block_max(float x, float* lds)
+__device__ __forceinline__ float nan_max(float a, float b)
 {
-    for (int o = 32; o; o >>= 1) x = nan_max(x, __shfl_xor(x, o));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return nan_max(nan_max(lds[0], lds[1]), nan_max(lds[2], lds[3]));
+    return a != a ? a : b != b ? b : fmaxf(a, b);
 }
 
-// y / scale as e4m3: a zero scale (a row of zeros) gives 0, a NaN stays one
-__device__ __forceinline__ uint8_t to_e4m3(float y, float scale)
+// sum (or max) over the TPR threads of a row, the same bits in each; `lds` holds a float
+// per wave where a row takes several
+template <int TPR, bool MAX>
+__device__ __forceinline__ float over_row(float x, float* lds)
 {
-    float v = scale == 0.f ? 0.f : y / scale;
-    v = v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;
-    return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false);
+    constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const float other = __shfl_xor(x, o);
+        x = MAX ? nan_max(x, other) : x + other;
+    }
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = lds[0];
+#pragma unroll
+        for (int i = 1; i < TPR / 64; ++i) x = MAX ? nan_max(x, lds[i]) : x + lds[i];
+    }
+    return x;
 }
+
+// two sums at once
+template <int TPR>
+__device__ __forceinline__ void sums_over_row(float& x, float& y, float* lds)
+{
+    constexpr int W = TPR < 64 ? TPR : 64, N = TPR / 64;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const float ox = __shfl_xor(x, o), oy = __shfl_xor(y, o);
+        x += ox;
+        y += oy;
+    }
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            lds[threadIdx.x >> 6] = x;
+            lds[N + (threadIdx.x >> 6)] = y;
+        }
+        __syncthreads();
+        x = lds[0];
+        y = lds[N];
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            x += lds[i];
+            y += lds[N + i];
+        }
+    }
+}
+
+// y / scale rounded to e4m3, four at a time.  A scale of 0 (a row of zeros) gives 0; NaN stays.
+__device__ __forceinline__ float clamp448(float v)
+{
+    return v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;
+}
+
+__device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(a), clamp448(b), 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(clamp448(c), clamp448(d), r, true);
+}
+
+// y / scale to a rounding, given 1 / scale to one: the quotient's remainder put right
+__device__ __forceinline__ float quotient(float y, float scale, float inv)
+{
+    const float q = y * inv;
+    return fmaf(fmaf(-q, scale, y), inv, q);
+}
+
+// threads of a workgroup
+template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
+// rows a thread has under way at once
+template <int K> constexpr int kRows = K == 1 ? 4 : K == 2 ? 2 : 1;
+
+template <typename TIO, int TPR, int K, bool Q8>
+__global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
+    const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, void* Y,
+    float* scale, TIO* R, long long rows, int D)
+{
+    constexpr int V = kVec<TIO>, U = kRows<K>, GROUPS = kBlock<TPR> / TPR;
+    __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int vectors = (D + V - 1) / V;
+    int col[K], dup[K];        // first column of each vector, and how many the one before has
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int v = lane + k * TPR;
+        col[k] = min(v * V, D - V);
+        dup[k] = v < vectors ? v * V - col[k] : V;
+    }
+    const float inv_d = 1.f / D;
+    for (long long r0 = ((long long)blockIdx.x * GROUPS + group) * U; r0 - group * U < rows;
+         r0 += (long long)gridDim.x * GROUPS * U) {
+        quad x[U][K], z[U][K];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                x[u][k] = z[u][k] = quad{0, 0, 0, 0};
+                if (r0 + u < rows && dup[k] < V) {
+                    const size_t at = (size_t)(r0 + u) * D + col[k];
+                    x[u][k] = load16(X + at);
+                    if (residual) z[u][k] = load16(residual + at);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float r[K][V], ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float a[V];
+                widen<TIO>(x[u][k], r[k]);
+                if (residual) {
+                    widen<TIO>(z[u][k], a);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) r[k][i] += a[i];
+                }
+                if (dup[k] == 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) ss = fmaf(r[k][i], r[k][i], ss);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) ss = i >= dup[k] ? fmaf(r[k][i], r[k][i], ss) : ss;
+                }
+            }
+            const float mean = over_row<TPR, false>(ss, lds) * inv_d;
+            const float rate = rsqrtf(mean + eps);
+            const bool live = r0 + u < rows;
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const size_t at = (size_t)(r0 + u) * D + col[k];
+                if (R && live && dup[k] < V) store16(R + at, narrow<TIO>(r[k]));
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    r[k][i] *= rate;
+                    if (weight && dup[k] < V) r[k][i] *= weight[col[k] + i];
+                    if constexpr (Q8) m = dup[k] < V ? nan_max(m, fabsf(r[k][i])) : m;
+                }
+                if constexpr (!Q8)
+                    if (live && dup[k] < V) store16((TIO*)Y + at, narrow<TIO>(r[k]));
+            }
+            if constexpr (Q8) {
+                const float sc = over_row<TPR, true>(m, lds) / kE4m3Max;
+                if (live && lane == 0) scale[r0 + u] = sc;
+                const bool tiny = sc < 1e-30f;       // whose reciprocal may leave fp32's range
+                const float inv = 1.f / sc;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (!live || dup[k] == V) continue;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        r[k][i] = tiny ? (sc == 0.f ? 0.f : r[k][i] / sc) : quotient(r[k][i], sc, inv);
+                    unsigned q[V / 4];
+#pragma unroll
+                    for (int i = 0; i < V / 4; ++i)
+                        q[i] = pack_e4m3(r[k][4 * i], r[k][4 * i + 1], r[k][4 * i + 2], r[k][4 * i + 3]);
+                    __builtin_memcpy((uint8_t*)Y + (size_t)(r0 + u) * D + col[k], q, V);
+                }
+            }
+        }
+    }
+}
+
+// Rows too long (or too short) for the registers' layout: a workgroup per row, the row read again
+// for every pass.
+__device__ __forceinline__ float block_sum(float x, float* lds) { return over_row<256, false>(x, lds); }
 
 template <typename TIO, bool Q8>
-__global__ __launch_bounds__(256) void rms_fwd_kernel(const TIO* X, const TIO* residual,
-                                                      const float* __restrict__ weight, float eps,
-                                                      void* Y, float* scale, TIO* R, int D)
+__global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const TIO* residual,
+                                                           const float* __restrict__ weight,
+                                                           float eps, void* Y, float* scale, TIO* R,
+                                                           long long rows, int D)
 {
     __shared__ float lds[4];
-    const size_t base = (size_t)blockIdx.x * D;
-    auto r_at = [&](int i) {
-        return io<TIO>::load(X, base + i) + (residual ? io<TIO>::load(residual, base + i) : 0.f);
-    };
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const float r = r_at(i);
-        ss = fmaf(r, r, ss);
-    }
-    const float k = rsqrtf(block_sum(ss, lds) / D + eps);
-    float sc = 0.f;
-    if constexpr (Q8) {
-        float m = 0.f;
-        for (int i = threadIdx.x; i < D; i += 256)
-            m = nan_max(m, fabsf(r_at(i) * k * (weight ? weight[i] : 1.f)));
-        sc = block_max(m, lds) / kE4m3Max;
-        if (threadIdx.x == 0) scale[blockIdx.x] = sc;
-    }
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const float r = r_at(i);
-        const float y = r * k * (weight ? weight[i] : 1.f);
-        if constexpr (Q8) ((uint8_t*)Y)[base + i] = to_e4m3(y, sc);
-        else io<TIO>::store((TIO*)Y, base + i, y);
-        if (R) io<TIO>::store(R, base + i, r);
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        const size_t base = (size_t)row * D;
+        auto r_at = [&](int i) {
+            const float x = io<TIO>::load(X, base + i);
+            return residual ? x + io<TIO>::load(residual, base + i) : x;
+        };
+        float ss = 0.f;
+        for (int i = threadIdx.x; i < D; i += 256) {
+            const float r = r_at(i);
+            ss = fmaf(r, r, ss);
+        }
+        const float rate = rsqrtf(block_sum(ss, lds) / D + eps);
+        float sc = 0.f;
+        if constexpr (Q8) {
+            float m = 0.f;
+            for (int i = threadIdx.x; i < D; i += 256)
+                m = nan_max(m, fabsf(r_at(i) * rate * (weight ? weight[i] : 1.f)));
+            sc = over_row<256, true>(m, lds) / kE4m3Max;
+            if (threadIdx.x == 0) scale[row] = sc;
+        }
+        for (int i = threadIdx.x; i < D; i += 256) {
+            const float r = r_at(i);
+            const float y = r * rate * (weight ? weight[i] : 1.f);
+            if constexpr (Q8)
+                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(sc == 0.f ? 0.f : y / sc, 0.f, 0.f, 0.f);
+            else
+                io<TIO>::store((TIO*)Y, base + i, y);
+            if (R) io<TIO>::store(R, base + i, r);
+        }
     }
 }
 
-template <typename TIO>
-__global__ __launch_bounds__(256) void rms_bwd_kernel(const TIO* __restrict__ R,
-                                                      const float* __restrict__ weight,
-                                                      const TIO* dY, const TIO* dR, float eps,
-                                                      TIO* dX, int D)
+template <typename TIO, int TPR, int K>
+__global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
+    const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
+    float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
 {
-    __shared__ float lds[4];
-    const size_t base = (size_t)blockIdx.x * D;
-    float ss = 0.f, su = 0.f;
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const float r = io<TIO>::load(R, base + i);
-        ss = fmaf(r, r, ss);
-        su = fmaf(io<TIO>::load(dY, base + i) * (weight ? weight[i] : 1.f), r, su);
+    constexpr int V = kVec<TIO>, GROUPS = kBlock<TPR> / TPR;
+    __shared__ float lds[TPR > 64 ? 2 * (TPR / 64) : 1];
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int vectors = (D + V - 1) / V;
+    int col[K], dup[K];
+    float w[K][V], dw[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int v = lane + k * TPR;
+        col[k] = min(v * V, D - V);
+        dup[k] = v < vectors ? v * V - col[k] : V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            w[k][i] = weight && dup[k] < V ? weight[col[k] + i] : 1.f;
+            dw[k][i] = 0.f;
+        }
     }
-    const float k = rsqrtf(block_sum(ss, lds) / D + eps);
-    const float m = block_sum(su, lds) * k / D;
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const float n = io<TIO>::load(R, base + i) * k;
-        const float u = io<TIO>::load(dY, base + i) * (weight ? weight[i] : 1.f);
-        io<TIO>::store(dX, base + i, k * (u - n * m) + (dR ? io<TIO>::load(dR, base + i) : 0.f));
+    const float inv_d = 1.f / D;
+    for (long long row = (long long)blockIdx.x * GROUPS + group; row - group < rows;
+         row += (long long)gridDim.x * GROUPS) {
+        const bool live = row < rows;
+        quad r[K], y[K], e[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            r[k] = y[k] = e[k] = quad{0, 0, 0, 0};
+            if (live && dup[k] < V) {
+                const size_t at = (size_t)row * D + col[k];
+                r[k] = load16(R + at);
+                y[k] = load16(dY + at);
+                if (dR) e[k] = load16(dR + at);
+            }
+        }
+        float ss = 0.f, su = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float rv[V], yv[V];
+            widen<TIO>(r[k], rv);
+            widen<TIO>(y[k], yv);
+            if (dup[k] == 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ss = fmaf(rv[i], rv[i], ss);
+                    su = fmaf(yv[i] * w[k][i], rv[i], su);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ss = i >= dup[k] ? fmaf(rv[i], rv[i], ss) : ss;
+                    su = i >= dup[k] ? fmaf(yv[i] * w[k][i], rv[i], su) : su;
+                }
+            }
+        }
+        sums_over_row<TPR>(ss, su, lds);
+        const float rate = rsqrtf(ss * inv_d + eps);
+        const float m = su * rate * inv_d;               // mean(u n)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            // (widened again from the words: the first pass's values would take as many
+            // registers as all the rest)
+            asm volatile("" : "+v"(r[k]), "+v"(y[k]));
+            float rv[V], yv[V], ev[V];
+            widen<TIO>(r[k], rv);
+            widen<TIO>(y[k], yv);
+            widen<TIO>(e[k], ev);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float n = rv[i] * rate;
+                dw[k][i] = live ? fmaf(yv[i], n, dw[k][i]) : dw[k][i];
+                rv[i] = fmaf(rate, yv[i] * w[k][i] - n * m, ev[i]);
+            }
+            if (live && dup[k] < V) store16(dX + (size_t)row * D + col[k], narrow<TIO>(rv));
+        }
+    }
+    if (!plane) return;
+    float* out = plane + (size_t)blockIdx.x * D;
+    if constexpr (GROUPS > 1) {
+        // the groups' sums of each column slot, added in the groups' order
+        constexpr int SLOTS = TPR * K * V;
+        __shared__ float part[GROUPS * SLOTS];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) part[group * SLOTS + (k * TPR + lane) * V + i] = dw[k][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < SLOTS; c += kBlock<TPR>) {
+            const int v = c / V, i = c % V, c0 = min(v * V, D - V);
+            if (v >= vectors || i < v * V - c0) continue;
+            float sum = part[c];
+#pragma unroll 4
+            for (int g = 1; g < GROUPS; ++g) sum += part[g * SLOTS + c];
+            out[c0 + i] = sum;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i >= dup[k]) out[col[k] + i] = dw[k][i];
     }
 }
 
-// row rates 1 / sqrt(mean(r^2) + eps), for the columns' sums
+// the same, a workgroup per row at a time, for the rows of rms_fwd_loop_kernel: each thread keeps
+// its columns' sums in the plane
 template <typename TIO>
-__global__ __launch_bounds__(256) void rms_rate_kernel(const TIO* __restrict__ R, float eps,
-                                                       float* __restrict__ rate, int D)
+__global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
+    const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
+    float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
 {
     __shared__ float lds[4];
-    const size_t base = (size_t)blockIdx.x * D;
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const float r = io<TIO>::load(R, base + i);
-        ss = fmaf(r, r, ss);
+    if (plane)
+        for (int i = threadIdx.x; i < D; i += 256) plane[(size_t)blockIdx.x * D + i] = 0.f;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        const size_t base = (size_t)row * D;
+        float ss = 0.f, su = 0.f;
+        for (int i = threadIdx.x; i < D; i += 256) {
+            const float r = io<TIO>::load(R, base + i);
+            ss = fmaf(r, r, ss);
+            su = fmaf(io<TIO>::load(dY, base + i) * (weight ? weight[i] : 1.f), r, su);
+        }
+        const float rate = rsqrtf(block_sum(ss, lds) / D + eps);
+        const float m = block_sum(su, lds) * rate / D;
+        for (int i = threadIdx.x; i < D; i += 256) {
+            const float n = io<TIO>::load(R, base + i) * rate, dy = io<TIO>::load(dY, base + i);
+            if (plane) plane[(size_t)blockIdx.x * D + i] += dy * n;
+            const float u = dy * (weight ? weight[i] : 1.f);
+            io<TIO>::store(dX, base + i,
+                           fmaf(rate, u - n * m, dR ? io<TIO>::load(dR, base + i) : 0.f));
+        }
     }
-    const float k = rsqrtf(block_sum(ss, lds) / D + eps);
-    if (threadIdx.x == 0) rate[blockIdx.x] = k;
 }
 
-template <typename TIO>
-__global__ __launch_bounds__(256) void rms_dw_kernel(const TIO* __restrict__ R,
-                                                     const TIO* __restrict__ dY,
-                                                     const float* __restrict__ rate,
-                                                     float* __restrict__ dweight, long long rows,
-                                                     int D)
+// dweight: 32 columns a workgroup, the planes dealt out to 32 threads of each column
+__global__ __launch_bounds__(1024) void rms_planes_kernel(const float* __restrict__ plane,
+                                                          float* __restrict__ dweight, int planes,
+                                                          int D)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= D) return;
+    __shared__ float part[32][33];
+    const int c = threadIdx.x & 31, p = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
     float s = 0.f;
-    for (long long r = 0; r < rows; ++r)
-        s = fmaf(io<TIO>::load(dY, r * D + i), io<TIO>::load(R, r * D + i) * rate[r], s);
-    dweight[i] = s;
+    if (i < D) {
+#pragma unroll 8
+        for (int k = p; k < planes; k += 32) s += plane[(size_t)k * D + i];
+    }
+    part[p][c] = s;
+    __syncthreads();
+    if (p == 0 && i < D) {
+#pragma unroll
+        for (int k = 1; k < 32; ++k) s += part[k][c];
+        dweight[i] = s;
+    }
 }
+
+// how a row lies in registers: threads and vectors of each; 0 threads: not at all
+struct Shape { int tpr, k; };
+
+Shape shape_of(int D, int vec)
+{
+    const int n = (D + vec - 1) / vec;
+    if (D < vec || n > 2048) return {0, 0};
+    if (n <= 64) return {n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1};
+    if (n <= 256) return {64, n <= 128 ? 2 : 4};
+    if (n <= 1024) return {256, n <= 512 ? 2 : 4};
+    return {1024, 2};
+}
+
+// The backward pass holds three inputs and two rows of fp32 (weight, dweight): fewer vectors a
+// thread.
+Shape bwd_shape_of(int D, int vec)
+{
+    const int n = (D + vec - 1) / vec;
+    if (n <= 64 || n > 2048 || D < vec) return shape_of(D, vec);
+    if (n <= 128) return {64, 2};
+    if (n <= 512) return {256, n <= 256 ? 1 : 2};
+    return {1024, n <= 1024 ? 1 : 2};
+}
+
+constexpr long long kMostBlocks = 1 << 22;
+constexpr int kMostPlanes = 1024;
+
+// workgroups of the backward pass, each with a plane of dweight
+int planes_of(long long rows, int D, int vec)
+{
+    const Shape s = bwd_shape_of(D, vec);
+    const int groups = s.tpr && s.tpr < 256 ? 256 / s.tpr : 1;
+    return (int)std::max(1ll, std::min<long long>((rows + groups - 1) / groups, kMostPlanes));
+}
+
+template <typename TIO, int TPR, int K>
+void fwd_launch(const RmsArgs& a, hipStream_t s)
+{
+    constexpr int PER = kBlock<TPR> / TPR * kRows<K>;
+    const dim3 grid((unsigned)std::min(kMostBlocks, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
+    if (a.scale)
+        hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, true>), grid, block, 0, s, (const TIO*)a.X,
+                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
+                           a.D);
+    else
+        hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, false>), grid, block, 0, s, (const TIO*)a.X,
+                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
+                           a.D);
+}
+
+template <typename TIO, int TPR, int K>
+void bwd_launch(const RmsBwdArgs& a, int planes, hipStream_t s)
+{
+    hipLaunchKernelGGL((rms_bwd_kernel<TIO, TPR, K>), dim3(planes), dim3(kBlock<TPR>), 0, s,
+                       (const TIO*)a.R, a.weight, (const TIO*)a.dY, (const TIO*)a.dR, a.eps,
+                       (TIO*)a.dX, a.dweight ? (float*)a.workspace : nullptr, a.rows, a.D);
+}
+
+// a case of the switches over shapes
+#define RMS_SHAPE(f, TPR, K, ...) \
+    case TPR * 8 + K: f<TIO, TPR, K>(__VA_ARGS__); break;
 
 template <typename TIO>
 hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.rows), block(256);
+    const Shape shape = shape_of(a.D, kVec<TIO>);
+    if (shape.tpr) {
+        switch (shape.tpr * 8 + shape.k) {
+            RMS_SHAPE(fwd_launch, 8, 1, a, s)
+            RMS_SHAPE(fwd_launch, 16, 1, a, s)
+            RMS_SHAPE(fwd_launch, 32, 1, a, s)
+            RMS_SHAPE(fwd_launch, 64, 1, a, s)
+            RMS_SHAPE(fwd_launch, 64, 2, a, s)
+            RMS_SHAPE(fwd_launch, 64, 4, a, s)
+            RMS_SHAPE(fwd_launch, 256, 2, a, s)
+            RMS_SHAPE(fwd_launch, 256, 4, a, s)
+            RMS_SHAPE(fwd_launch, 1024, 2, a, s)
+        default: return hipErrorInvalidValue;
+        }
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)std::min(kMostBlocks, a.rows)), block(256);
     if (a.scale)
-        hipLaunchKernelGGL((rms_fwd_kernel<TIO, true>), grid, block, 0, s, (const TIO*)a.X,
-                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.D);
+        hipLaunchKernelGGL((rms_fwd_loop_kernel<TIO, true>), grid, block, 0, s, (const TIO*)a.X,
+                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
+                           a.D);
     else
-        hipLaunchKernelGGL((rms_fwd_kernel<TIO, false>), grid, block, 0, s, (const TIO*)a.X,
-                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.D);
+        hipLaunchKernelGGL((rms_fwd_loop_kernel<TIO, false>), grid, block, 0, s, (const TIO*)a.X,
+                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
+                           a.D);
     return hipGetLastError();
 }
 
 template <typename TIO>
 hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.rows), block(256);
-    const TIO *R = (const TIO*)a.R, *dY = (const TIO*)a.dY;
-    float* rate = (float*)a.workspace;
-    if (a.dweight) {   // first: dX may stand at dY's place
-        if (a.rows)
-            hipLaunchKernelGGL(rms_rate_kernel<TIO>, grid, block, 0, s, R, a.eps, rate, a.D);
-        hipLaunchKernelGGL(rms_dw_kernel<TIO>, dim3((a.D + 255) / 256), block, 0, s, R, dY, rate,
-                           a.dweight, a.rows, a.D);
+    const Shape shape = bwd_shape_of(a.D, kVec<TIO>);
+    const int planes = planes_of(a.rows, a.D, kVec<TIO>);
+    if (shape.tpr) {
+        switch (shape.tpr * 8 + shape.k) {
+            RMS_SHAPE(bwd_launch, 8, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 16, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 32, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 64, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 64, 2, a, planes, s)
+            RMS_SHAPE(bwd_launch, 256, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 256, 2, a, planes, s)
+            RMS_SHAPE(bwd_launch, 1024, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 1024, 2, a, planes, s)
+        default: return hipErrorInvalidValue;
+        }
+    } else {
+        hipLaunchKernelGGL(rms_bwd_loop_kernel<TIO>, dim3(planes), dim3(256), 0, s,
+                           (const TIO*)a.R, a.weight, (const TIO*)a.dY, (const TIO*)a.dR, a.eps,
+                           (TIO*)a.dX, a.dweight ? (float*)a.workspace : nullptr, a.rows, a.D);
     }
-    if (a.rows)
-        hipLaunchKernelGGL(rms_bwd_kernel<TIO>, grid, block, 0, s, R, a.weight, dY,
-                           (const TIO*)a.dR, a.eps, (TIO*)a.dX, a.D);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dweight) return e;
+    hipLaunchKernelGGL(rms_planes_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, s,
+                       (const float*)a.workspace, a.dweight, planes, a.D);
     return hipGetLastError();
 }
 
@@ -166,7 +569,10 @@ hipError_t launch_rmsnorm_fwd(const RmsArgs& a, hipStream_t s)
     return a.bf16 ? fwd_typed<uint16_t>(a, s) : fwd_typed<float>(a, s);
 }
 
-size_t rmsnorm_bwd_workspace(long long rows, int, bool) { return (size_t)rows * 4; }
+size_t rmsnorm_bwd_workspace(long long rows, int D, bool bf16)
+{
+    return (size_t)planes_of(rows, D, bf16 ? 8 : 4) * D * 4;
+}
 
 hipError_t launch_rmsnorm_bwd(const RmsBwdArgs& a, hipStream_t s)
 {
