@@ -57,7 +57,7 @@ KERNEL_SOURCES = {"linear_b16": ["linear_mfma.hip", "linear_coop.hip", "mfma_com
                             "block_launch.h"],
                   "rmsnorm": ["rmsnorm.hip", "mfma_common.h", "device_common.h",
                               "block_launch.h"],
-                  "clip": ["clip.hip", "device_common.h", "block_launch.h"]}
+                  "clip": ["clip.hip", "mfma_common.h", "device_common.h", "block_launch.h"]}
 HOST_ONLY_SOURCES = {"api.cpp", "api_block.cpp", "host_checks.h"}
 
 

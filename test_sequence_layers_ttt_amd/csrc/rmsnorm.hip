@@ -69,75 +69,116 @@ __device__ __forceinline__ quad narrow(const float (&v)[kVec<TIO>])
     return q;
 }
 
-// max with NaN winning
-__device__ __forceinline__ float nan_max(float a, float b)
+// what lane ^ (16 or 32) has, next to the lane's own, as (lower half's, upper half's)
+template <int O>
+__device__ __forceinline__ void halves(unsigned x, unsigned& lo, unsigned& hi)
 {
-    return a != a ? a : b != b ? b : fmaxf(a, b);
+    static_assert(O == 16 || O == 32, "");
+    if constexpr (O == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        lo = p[0];
+        hi = p[1];
+    } else {
+        const auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        lo = p[0];
+        hi = p[1];
+    }
 }
 
-// sum (or max) over the TPR threads of a row, the same bits in each; `lds` holds a float
-// per wave where a row takes several
-template <int TPR, bool MAX>
-__device__ __forceinline__ float over_row(float x, float* lds)
+template <int CTRL>
+__device__ __forceinline__ unsigned moved(unsigned x)
 {
-    constexpr int W = TPR < 64 ? TPR : 64;
-#pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-        const float other = __shfl_xor(x, o);
-        x = MAX ? nan_max(x, other) : x + other;
+    return (unsigned)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, false);
+}
+
+// reduction over W <= 64 neighbouring lanes, the same bits in each: `f` is symmetric
+template <int W, typename F>
+__device__ __forceinline__ unsigned over_lanes(unsigned x, F&& f)
+{
+    if constexpr (W > 1) x = f(x, moved<kDppQuadXor1>(x));
+    if constexpr (W > 2) x = f(x, moved<kDppQuadXor2>(x));
+    if constexpr (W > 4) x = f(x, moved<kDppRowHalfMirror>(x));
+    if constexpr (W > 8) x = f(x, moved<kDppRowMirror>(x));
+    unsigned lo, hi;
+    if constexpr (W > 16) {
+        halves<16>(x, lo, hi);
+        x = f(lo, hi);
     }
-    if constexpr (TPR > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-        __syncthreads();
-        x = lds[0];
-#pragma unroll
-        for (int i = 1; i < TPR / 64; ++i) x = MAX ? nan_max(x, lds[i]) : x + lds[i];
+    if constexpr (W > 32) {
+        halves<32>(x, lo, hi);
+        x = f(lo, hi);
     }
     return x;
 }
 
-// two sums at once
-template <int TPR>
-__device__ __forceinline__ void sums_over_row(float& x, float& y, float* lds)
+__device__ __forceinline__ unsigned add_bits(unsigned a, unsigned b)
 {
-    constexpr int W = TPR < 64 ? TPR : 64, N = TPR / 64;
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+
+// magnitudes compared as their bits: a NaN is above everything
+__device__ __forceinline__ unsigned max_bits(unsigned a, unsigned b) { return a > b ? a : b; }
+
+// N sums (or maxima of magnitudes) over the TPR threads of a row, the same bits in each; `lds`
+// holds N words per wave where a row takes several
+template <int TPR, int N, bool MAX>
+__device__ __forceinline__ void over_row(unsigned (&x)[N], unsigned* lds)
+{
+    constexpr int W = TPR < 64 ? TPR : 64, WAVES = TPR / 64;
 #pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-        const float ox = __shfl_xor(x, o), oy = __shfl_xor(y, o);
-        x += ox;
-        y += oy;
-    }
+    for (int n = 0; n < N; ++n) x[n] = over_lanes<W>(x[n], MAX ? max_bits : add_bits);
     if constexpr (TPR > 64) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) {
-            lds[threadIdx.x >> 6] = x;
-            lds[N + (threadIdx.x >> 6)] = y;
+#pragma unroll
+            for (int n = 0; n < N; ++n) lds[n * WAVES + (threadIdx.x >> 6)] = x[n];
         }
         __syncthreads();
-        x = lds[0];
-        y = lds[N];
 #pragma unroll
-        for (int i = 1; i < N; ++i) {
-            x += lds[i];
-            y += lds[N + i];
+        for (int n = 0; n < N; ++n) {
+            x[n] = lds[n * WAVES];
+#pragma unroll
+            for (int i = 1; i < WAVES; ++i)
+                x[n] = (MAX ? max_bits : add_bits)(x[n], lds[n * WAVES + i]);
         }
     }
 }
 
-// y / scale rounded to e4m3, four at a time.  A scale of 0 (a row of zeros) gives 0; NaN stays.
-__device__ __forceinline__ float clamp448(float v)
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, unsigned* lds)
 {
+    unsigned b[1] = {__float_as_uint(x)};
+    over_row<TPR, 1, false>(b, lds);
+    return __uint_as_float(b[0]);
+}
+
+template <int TPR>
+__device__ __forceinline__ float row_max(unsigned x, unsigned* lds)
+{
+    unsigned b[1] = {x};
+    over_row<TPR, 1, true>(b, lds);
+    return __uint_as_float(b[0]);
+}
+
+__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// four values as e4m3, rounded to nearest even (up to 464 in magnitude that is 448; NaN stays)
+__device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
+{
+    const int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// y / scale where 1 / scale may leave fp32's range: a scale of 0 (a row of zeros) gives 0, and
+// one so small that it has few bits is held to the largest value
+__device__ __forceinline__ float small_quotient(float y, float scale)
+{
+    const float v = scale == 0.f ? 0.f : y / scale;
     return v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;
 }
 
-__device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
-{
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(a), clamp448(b), 0, false);
-    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(clamp448(c), clamp448(d), r, true);
-}
-
-// y / scale to a rounding, given 1 / scale to one: the quotient's remainder put right
+// y / scale to a rounding, given 1 / scale to one: the quotient's remainder put right (at most
+// 448 and a rounding, as scale is the row's largest |y| / 448)
 __device__ __forceinline__ float quotient(float y, float scale, float inv)
 {
     const float q = y * inv;
@@ -147,23 +188,26 @@ __device__ __forceinline__ float quotient(float y, float scale, float inv)
 // threads of a workgroup
 template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
 // rows a thread has under way at once
-template <int K> constexpr int kRows = K == 1 ? 4 : K == 2 ? 2 : 1;
+template <int TPR, int K> constexpr int kRows = TPR <= 64 && K == 1 ? 2 : 1;
 
 template <typename TIO, int TPR, int K, bool Q8>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
     const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, void* Y,
     float* scale, TIO* R, long long rows, int D)
 {
-    constexpr int V = kVec<TIO>, U = kRows<K>, GROUPS = kBlock<TPR> / TPR;
-    __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+    constexpr int V = kVec<TIO>, U = kRows<TPR, K>, GROUPS = kBlock<TPR> / TPR;
+    __shared__ unsigned lds[TPR > 64 ? TPR / 64 : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int vectors = (D + V - 1) / V;
     int col[K], dup[K];        // first column of each vector, and how many the one before has
+    float w[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int v = lane + k * TPR;
         col[k] = min(v * V, D - V);
         dup[k] = v < vectors ? v * V - col[k] : V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[k][i] = weight && dup[k] < V ? weight[col[k] + i] : 1.f;
     }
     const float inv_d = 1.f / D;
     for (long long r0 = ((long long)blockIdx.x * GROUPS + group) * U; r0 - group * U < rows;
@@ -200,34 +244,36 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
                     for (int i = 0; i < V; ++i) ss = i >= dup[k] ? fmaf(r[k][i], r[k][i], ss) : ss;
                 }
             }
-            const float mean = over_row<TPR, false>(ss, lds) * inv_d;
-            const float rate = rsqrtf(mean + eps);
+            const float rate = rsqrtf(row_sum<TPR>(ss, lds) * inv_d + eps);
             const bool live = r0 + u < rows;
-            float m = 0.f;
+            unsigned m = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
+                const bool mine = live && dup[k] < V;
                 const size_t at = (size_t)(r0 + u) * D + col[k];
-                if (R && live && dup[k] < V) store16(R + at, narrow<TIO>(r[k]));
+                if (R && mine) store16(R + at, narrow<TIO>(r[k]));
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    r[k][i] *= rate;
-                    if (weight && dup[k] < V) r[k][i] *= weight[col[k] + i];
-                    if constexpr (Q8) m = dup[k] < V ? nan_max(m, fabsf(r[k][i])) : m;
+                    r[k][i] *= rate * w[k][i];
+                    if constexpr (Q8) m = max_bits(m, magnitude(r[k][i]));
                 }
                 if constexpr (!Q8)
-                    if (live && dup[k] < V) store16((TIO*)Y + at, narrow<TIO>(r[k]));
+                    if (mine) store16((TIO*)Y + at, narrow<TIO>(r[k]));
             }
             if constexpr (Q8) {
-                const float sc = over_row<TPR, true>(m, lds) / kE4m3Max;
+                const float sc = row_max<TPR>(m, lds) / kE4m3Max;
                 if (live && lane == 0) scale[r0 + u] = sc;
-                const bool tiny = sc < 1e-30f;       // whose reciprocal may leave fp32's range
                 const float inv = 1.f / sc;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     if (!live || dup[k] == V) continue;
+                    if (sc < 1e-30f) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        r[k][i] = tiny ? (sc == 0.f ? 0.f : r[k][i] / sc) : quotient(r[k][i], sc, inv);
+                        for (int i = 0; i < V; ++i) r[k][i] = small_quotient(r[k][i], sc);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) r[k][i] = quotient(r[k][i], sc, inv);
+                    }
                     unsigned q[V / 4];
 #pragma unroll
                     for (int i = 0; i < V / 4; ++i)
@@ -241,15 +287,13 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
 
 // Rows too long (or too short) for the registers' layout: a workgroup per row, the row read again
 // for every pass.
-__device__ __forceinline__ float block_sum(float x, float* lds) { return over_row<256, false>(x, lds); }
-
 template <typename TIO, bool Q8>
 __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const TIO* residual,
                                                            const float* __restrict__ weight,
                                                            float eps, void* Y, float* scale, TIO* R,
                                                            long long rows, int D)
 {
-    __shared__ float lds[4];
+    __shared__ unsigned lds[4];
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
         const size_t base = (size_t)row * D;
         auto r_at = [&](int i) {
@@ -261,20 +305,20 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
             const float r = r_at(i);
             ss = fmaf(r, r, ss);
         }
-        const float rate = rsqrtf(block_sum(ss, lds) / D + eps);
+        const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
         float sc = 0.f;
         if constexpr (Q8) {
-            float m = 0.f;
+            unsigned m = 0;
             for (int i = threadIdx.x; i < D; i += 256)
-                m = nan_max(m, fabsf(r_at(i) * rate * (weight ? weight[i] : 1.f)));
-            sc = over_row<256, true>(m, lds) / kE4m3Max;
+                m = max_bits(m, magnitude(r_at(i) * (rate * (weight ? weight[i] : 1.f))));
+            sc = row_max<256>(m, lds) / kE4m3Max;
             if (threadIdx.x == 0) scale[row] = sc;
         }
         for (int i = threadIdx.x; i < D; i += 256) {
             const float r = r_at(i);
-            const float y = r * rate * (weight ? weight[i] : 1.f);
+            const float y = r * (rate * (weight ? weight[i] : 1.f));
             if constexpr (Q8)
-                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(sc == 0.f ? 0.f : y / sc, 0.f, 0.f, 0.f);
+                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(small_quotient(y, sc), 0.f, 0.f, 0.f);
             else
                 io<TIO>::store((TIO*)Y, base + i, y);
             if (R) io<TIO>::store(R, base + i, r);
@@ -288,7 +332,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
     float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
 {
     constexpr int V = kVec<TIO>, GROUPS = kBlock<TPR> / TPR;
-    __shared__ float lds[TPR > 64 ? 2 * (TPR / 64) : 1];
+    __shared__ unsigned lds[TPR > 64 ? 2 * (TPR / 64) : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int vectors = (D + V - 1) / V;
     int col[K], dup[K];
@@ -339,9 +383,10 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
                 }
             }
         }
-        sums_over_row<TPR>(ss, su, lds);
-        const float rate = rsqrtf(ss * inv_d + eps);
-        const float m = su * rate * inv_d;               // mean(u n)
+        unsigned both[2] = {__float_as_uint(ss), __float_as_uint(su)};
+        over_row<TPR, 2, false>(both, lds);
+        const float rate = rsqrtf(__uint_as_float(both[0]) * inv_d + eps);
+        const float m = __uint_as_float(both[1]) * rate * inv_d;   // mean(u n)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             // (widened again from the words: the first pass's values would take as many
@@ -395,7 +440,7 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
     const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
     float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
 {
-    __shared__ float lds[4];
+    __shared__ unsigned lds[4];
     if (plane)
         for (int i = threadIdx.x; i < D; i += 256) plane[(size_t)blockIdx.x * D + i] = 0.f;
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -406,8 +451,8 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
             ss = fmaf(r, r, ss);
             su = fmaf(io<TIO>::load(dY, base + i) * (weight ? weight[i] : 1.f), r, su);
         }
-        const float rate = rsqrtf(block_sum(ss, lds) / D + eps);
-        const float m = block_sum(su, lds) * rate / D;
+        const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
+        const float m = row_sum<256>(su, lds) * rate / D;
         for (int i = threadIdx.x; i < D; i += 256) {
             const float n = io<TIO>::load(R, base + i) * rate, dy = io<TIO>::load(dY, base + i);
             if (plane) plane[(size_t)blockIdx.x * D + i] += dy * n;
@@ -447,29 +492,18 @@ Shape shape_of(int D, int vec)
     const int n = (D + vec - 1) / vec;
     if (D < vec || n > 2048) return {0, 0};
     if (n <= 64) return {n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1};
-    if (n <= 256) return {64, n <= 128 ? 2 : 4};
-    if (n <= 1024) return {256, n <= 512 ? 2 : 4};
-    return {1024, 2};
-}
-
-// The backward pass holds three inputs and two rows of fp32 (weight, dweight): fewer vectors a
-// thread.
-Shape bwd_shape_of(int D, int vec)
-{
-    const int n = (D + vec - 1) / vec;
-    if (n <= 64 || n > 2048 || D < vec) return shape_of(D, vec);
     if (n <= 128) return {64, 2};
     if (n <= 512) return {256, n <= 256 ? 1 : 2};
     return {1024, n <= 1024 ? 1 : 2};
 }
 
-constexpr long long kMostBlocks = 1 << 22;
+constexpr long long kMostBlocks = 2048;    // eight a compute unit: each loads the weight once
 constexpr int kMostPlanes = 1024;
 
 // workgroups of the backward pass, each with a plane of dweight
 int planes_of(long long rows, int D, int vec)
 {
-    const Shape s = bwd_shape_of(D, vec);
+    const Shape s = shape_of(D, vec);
     const int groups = s.tpr && s.tpr < 256 ? 256 / s.tpr : 1;
     return (int)std::max(1ll, std::min<long long>((rows + groups - 1) / groups, kMostPlanes));
 }
@@ -477,7 +511,7 @@ int planes_of(long long rows, int D, int vec)
 template <typename TIO, int TPR, int K>
 void fwd_launch(const RmsArgs& a, hipStream_t s)
 {
-    constexpr int PER = kBlock<TPR> / TPR * kRows<K>;
+    constexpr int PER = kBlock<TPR> / TPR * kRows<TPR, K>;
     const dim3 grid((unsigned)std::min(kMostBlocks, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
     if (a.scale)
         hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, true>), grid, block, 0, s, (const TIO*)a.X,
@@ -512,9 +546,9 @@ hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
             RMS_SHAPE(fwd_launch, 32, 1, a, s)
             RMS_SHAPE(fwd_launch, 64, 1, a, s)
             RMS_SHAPE(fwd_launch, 64, 2, a, s)
-            RMS_SHAPE(fwd_launch, 64, 4, a, s)
+            RMS_SHAPE(fwd_launch, 256, 1, a, s)
             RMS_SHAPE(fwd_launch, 256, 2, a, s)
-            RMS_SHAPE(fwd_launch, 256, 4, a, s)
+            RMS_SHAPE(fwd_launch, 1024, 1, a, s)
             RMS_SHAPE(fwd_launch, 1024, 2, a, s)
         default: return hipErrorInvalidValue;
         }
@@ -535,7 +569,7 @@ hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
 template <typename TIO>
 hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
 {
-    const Shape shape = bwd_shape_of(a.D, kVec<TIO>);
+    const Shape shape = shape_of(a.D, kVec<TIO>);
     const int planes = planes_of(a.rows, a.D, kVec<TIO>);
     if (shape.tpr) {
         switch (shape.tpr * 8 + shape.k) {
