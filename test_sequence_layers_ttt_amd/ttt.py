@@ -482,11 +482,13 @@ def mlp_fwd(K, Q, V, eta, W1, b1, W2, b2, chunk: int, eta_scalar: float = 0.0, *
 
 
 # ---- operators around the scan: gated recurrence, RMS norm, gradient clipping ----
+# A decoded token's call is a few microseconds of kernel, so what it checks it checks
+# cheaply: the device as an index, and no context or stream object on the usual path.
 
-def _match(t, name, shape, dtype, device):
-    """_check for the operators below: also on one device."""
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _match(t, name, shape, dtype, index):
+    """_check for the operators below: on the device of that index."""
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
     if t.dtype != dtype:
         raise ValueError("%s must be %s" % (name, dtype))
     if t.shape != shape:
@@ -496,41 +498,32 @@ def _match(t, name, shape, dtype, device):
 
 
 def _first(t, name):
-    """Checks the tensor that the others are held to; returns its ttt_dtype."""
-    if not t.is_cuda:
+    """Checks the tensor that the others are held to: (its ttt_dtype, its device's index)."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("%s must be a device tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return _io_dtype(t)
+    return _io_dtype(t), index
 
 
-class _On:
-    """The device and stream a call runs on: the tensors' device is made current, and
-    what the call allocates belongs to its stream (so a workspace that it drops is
-    not handed out to another stream while the call still runs)."""
-    __slots__ = ("device", "stream", "guards")
+def _elsewhere(index, stream):
+    """None where a call runs on the current device and stream; else what makes them so.
+    A call enters it before it allocates: a workspace that it drops then belongs to the
+    stream it runs on, and is not handed to another while it still runs."""
+    import torch
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("the stream belongs to %s, the tensors to cuda:%d"
+                             % (stream.device, index))
+        return torch.cuda.stream(stream)
+    return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
 
-    def __enter__(self):
-        import torch
-        if self.stream is not None:
-            guard = torch.cuda.stream(self.stream)   # sets its device too
-            if self.stream.device != self.device:
-                raise ValueError("the stream belongs to %s, the tensors to %s"
-                                 % (self.stream.device, self.device))
-        elif torch.cuda.current_device() != self.device.index:
-            guard = torch.cuda.device(self.device)
-        else:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        guard.__enter__()
-        self.guards = (guard,)
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
+def _raw_stream(index) -> int:
+    """The current stream of the device (without the object that current_stream makes)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def gated_workspace_bytes(B, H, T, d, io_dtype) -> int:
@@ -542,25 +535,29 @@ def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None)
     bf16 (G <= 0; -inf starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
     (Z, h_T): the states in the I/O type, and the last one in fp32."""
     import torch
-    B, H, T, d = X.shape
-    io, dev = _first(X, "X"), X.device
-    _match(G, "G", X.shape, X.dtype, dev)
+    io, dev = _first(X, "X")
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return gated_fwd(X, G, h0, Z=Z, h_out=h_out, workspace=workspace)
+    shape = X.shape
+    B, H, T, d = shape
+    _match(G, "G", shape, X.dtype, dev)
     if h0 is not None:
         _match(h0, "h0", (B, H, d), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if Z is None:
-            Z = torch.empty_like(X)
-        else:
-            _match(Z, "Z", X.shape, X.dtype, dev)
-        if h_out is None:
-            h_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
-        else:
-            _match(h_out, "h_out", (B, H, d), torch.float32, dev)
-        L = lib()
-        ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), dev, workspace)
-        rc = L.ttt_gated_fwd(X.data_ptr(), G.data_ptr(), _ptr(h0), Z.data_ptr(),
-                             h_out.data_ptr(), B, H, T, d, io, _ptr(ws),
-                             0 if ws is None else ws.numel(), st)
+    if Z is None:
+        Z = torch.empty_like(X)
+    else:
+        _match(Z, "Z", shape, X.dtype, dev)
+    if h_out is None:
+        h_out = torch.empty((B, H, d), dtype=torch.float32, device=X.device)
+    else:
+        _match(h_out, "h_out", (B, H, d), torch.float32, dev)
+    L = lib()
+    ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), X.device, workspace)
+    rc = L.ttt_gated_fwd(X.data_ptr(), G.data_ptr(), _ptr(h0), Z.data_ptr(), h_out.data_ptr(),
+                         B, H, T, d, io, _ptr(ws), 0 if ws is None else ws.numel(),
+                         _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_gated_fwd")
     return Z, h_out
@@ -570,17 +567,21 @@ def gated_step(X, G, h, *, Z=None, stream=None):
     """Continue gated recurrences by the n tokens of X, G [B, H, n, d] from the state h
     [B, H, d] fp32, which is updated in place.  Returns Z."""
     import torch
-    B, H, n, d = X.shape
-    io, dev = _first(X, "X"), X.device
-    _match(G, "G", X.shape, X.dtype, dev)
+    io, dev = _first(X, "X")
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return gated_step(X, G, h, Z=Z)
+    shape = X.shape
+    B, H, n, d = shape
+    _match(G, "G", shape, X.dtype, dev)
     _match(h, "h", (B, H, d), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if Z is None:
-            Z = torch.empty_like(X)
-        else:
-            _match(Z, "Z", X.shape, X.dtype, dev)
-        rc = lib().ttt_gated_step(X.data_ptr(), G.data_ptr(), h.data_ptr(), Z.data_ptr(),
-                                  B, H, n, d, io, st)
+    if Z is None:
+        Z = torch.empty_like(X)
+    else:
+        _match(Z, "Z", shape, X.dtype, dev)
+    rc = lib().ttt_gated_step(X.data_ptr(), G.data_ptr(), h.data_ptr(), Z.data_ptr(), B, H, n, d,
+                              io, _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_gated_step")
     return Z
@@ -591,44 +592,50 @@ def gated_bwd(G, Z, dZ, h0=None, dh_T=None, *, dX=None, dG=None, dh0=None, works
     """Gradients of <dZ, Z> + <dh_T, h_T> through Z, h_T = gated_fwd(X, G, h0).  Z is the
     forward call's; h0 and dh_T: [B, H, d] fp32 or None (zero).  Returns (dX, dG, dh0)."""
     import torch
-    B, H, T, d = G.shape
-    io, dev = _first(G, "G"), G.device
-    _match(Z, "Z", G.shape, G.dtype, dev)
-    _match(dZ, "dZ", G.shape, G.dtype, dev)
+    io, dev = _first(G, "G")
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return gated_bwd(G, Z, dZ, h0, dh_T, dX=dX, dG=dG, dh0=dh0, workspace=workspace)
+    shape = G.shape
+    B, H, T, d = shape
+    _match(Z, "Z", shape, G.dtype, dev)
+    _match(dZ, "dZ", shape, G.dtype, dev)
     for t, name in ((h0, "h0"), (dh_T, "dh_T"), (dh0, "dh0")):
         if t is not None:
             _match(t, name, (B, H, d), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if dX is None:
-            dX = torch.empty_like(G)
-        else:
-            _match(dX, "dX", G.shape, G.dtype, dev)
-        if dG is None:
-            dG = torch.empty_like(G)
-        else:
-            _match(dG, "dG", G.shape, G.dtype, dev)
-        if dh0 is None:
-            dh0 = torch.empty((B, H, d), dtype=torch.float32, device=dev)
-        L = lib()
-        ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), dev, workspace)
-        rc = L.ttt_gated_bwd(G.data_ptr(), Z.data_ptr(), _ptr(h0), dZ.data_ptr(), _ptr(dh_T),
-                             dX.data_ptr(), dG.data_ptr(), dh0.data_ptr(), B, H, T, d, io,
-                             _ptr(ws), 0 if ws is None else ws.numel(), st)
+    if dX is None:
+        dX = torch.empty_like(G)
+    else:
+        _match(dX, "dX", shape, G.dtype, dev)
+    if dG is None:
+        dG = torch.empty_like(G)
+    else:
+        _match(dG, "dG", shape, G.dtype, dev)
+    if dh0 is None:
+        dh0 = torch.empty((B, H, d), dtype=torch.float32, device=G.device)
+    L = lib()
+    ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), G.device, workspace)
+    rc = L.ttt_gated_bwd(G.data_ptr(), Z.data_ptr(), _ptr(h0), dZ.data_ptr(), _ptr(dh_T),
+                         dX.data_ptr(), dG.data_ptr(), dh0.data_ptr(), B, H, T, d, io, _ptr(ws),
+                         0 if ws is None else ws.numel(), _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_gated_bwd")
     return dX, dG, dh0
 
 
-def _rms_args(X, weight, residual):
+def _rms_args(X, weight, residual, name="X"):
     import torch
-    if X.dim() == 0:
-        raise ValueError("X needs a feature axis")
-    io, dev, D = _first(X, "X"), X.device, X.shape[-1]
+    shape = X.shape
+    if not shape or not shape[-1]:
+        raise ValueError("%s needs a feature axis" % name)
+    io, dev = _first(X, name)
+    D = shape[-1]
     if weight is not None:
         _match(weight, "weight", (D,), torch.float32, dev)
     if residual is not None:
-        _match(residual, "residual", X.shape, X.dtype, dev)
-    return io, dev, D, X.numel() // D if D else 0
+        _match(residual, "residual", shape, X.dtype, dev)
+    return io, dev, D, X.numel() // D
 
 
 def rmsnorm_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y=None, R=None,
@@ -639,17 +646,20 @@ def rmsnorm_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y=None, R=N
     tensor for it is given)."""
     import torch
     io, dev, D, rows = _rms_args(X, weight, residual)
-    with _On(dev, stream) as st:
-        if Y is None:
-            Y = torch.empty_like(X)
-        else:
-            _match(Y, "Y", X.shape, X.dtype, dev)
-        if R is not None:
-            _match(R, "R", X.shape, X.dtype, dev)
-        elif residual is not None:
-            R = torch.empty_like(X)
-        rc = lib().ttt_rmsnorm_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps,
-                                   Y.data_ptr(), _ptr(R), rows, D, io, st)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return rmsnorm_fwd(X, weight, residual, eps, Y=Y, R=R)
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _match(Y, "Y", X.shape, X.dtype, dev)
+    if R is not None:
+        _match(R, "R", X.shape, X.dtype, dev)
+    elif residual is not None:
+        R = torch.empty_like(X)
+    rc = lib().ttt_rmsnorm_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps, Y.data_ptr(),
+                               _ptr(R), rows, D, io, _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_rmsnorm_fwd")
     return Y, R
@@ -661,21 +671,24 @@ def rmsnorm_q8_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y8=None,
     per row: y = Y8 * scale.  Returns (Y8, scale, R)."""
     import torch
     io, dev, D, rows = _rms_args(X, weight, residual)
-    with _On(dev, stream) as st:
-        if Y8 is None:
-            Y8 = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=dev)
-        else:
-            _match(Y8, "Y8", X.shape, torch.float8_e4m3fn, dev)
-        if scale is None:
-            scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=dev)
-        else:
-            _match(scale, "scale", X.shape[:-1], torch.float32, dev)
-        if R is not None:
-            _match(R, "R", X.shape, X.dtype, dev)
-        elif residual is not None:
-            R = torch.empty_like(X)
-        rc = lib().ttt_rmsnorm_q8_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps,
-                                      Y8.data_ptr(), scale.data_ptr(), _ptr(R), rows, D, io, st)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return rmsnorm_q8_fwd(X, weight, residual, eps, Y8=Y8, scale=scale, R=R)
+    if Y8 is None:
+        Y8 = torch.empty_like(X, dtype=torch.float8_e4m3fn)
+    else:
+        _match(Y8, "Y8", X.shape, torch.float8_e4m3fn, dev)
+    if scale is None:
+        scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    else:
+        _match(scale, "scale", X.shape[:-1], torch.float32, dev)
+    if R is not None:
+        _match(R, "R", X.shape, X.dtype, dev)
+    elif residual is not None:
+        R = torch.empty_like(X)
+    rc = lib().ttt_rmsnorm_q8_fwd(X.data_ptr(), _ptr(residual), _ptr(weight), eps, Y8.data_ptr(),
+                                  scale.data_ptr(), _ptr(R), rows, D, io, _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_rmsnorm_q8_fwd")
     return Y8, scale, R
@@ -692,26 +705,30 @@ def rmsnorm_bwd(R, weight, dY, dR=None, eps: float = 1e-6, *, dX=None, dweight=N
     dX is the gradient for X and for the residual, dweight [D] fp32 (None when
     want_dweight is False)."""
     import torch
-    io, dev, D, rows = _rms_args(R, weight, None)
+    io, dev, D, rows = _rms_args(R, weight, None, "R")
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return rmsnorm_bwd(R, weight, dY, dR, eps, dX=dX, dweight=dweight,
+                               want_dweight=want_dweight, workspace=workspace)
     _match(dY, "dY", R.shape, R.dtype, dev)
     if dR is not None:
         _match(dR, "dR", R.shape, R.dtype, dev)
-    with _On(dev, stream) as st:
-        if dX is None:
-            dX = torch.empty_like(R)
-        else:
-            _match(dX, "dX", R.shape, R.dtype, dev)
-        if dweight is not None:
-            _match(dweight, "dweight", (D,), torch.float32, dev)
-        elif want_dweight:
-            dweight = torch.empty(D, dtype=torch.float32, device=dev)
-        L = lib()
-        ws = None
-        if dweight is not None:
-            ws = _workspace(L.ttt_rmsnorm_bwd_workspace_bytes(rows, D, io), dev, workspace)
-        rc = L.ttt_rmsnorm_bwd(R.data_ptr(), _ptr(weight), dY.data_ptr(), _ptr(dR), eps,
-                               dX.data_ptr(), _ptr(dweight), rows, D, io, _ptr(ws),
-                               0 if ws is None else ws.numel(), st)
+    if dX is None:
+        dX = torch.empty_like(R)
+    else:
+        _match(dX, "dX", R.shape, R.dtype, dev)
+    if dweight is not None:
+        _match(dweight, "dweight", (D,), torch.float32, dev)
+    elif want_dweight:
+        dweight = torch.empty(D, dtype=torch.float32, device=R.device)
+    L = lib()
+    ws = None
+    if dweight is not None:
+        ws = _workspace(L.ttt_rmsnorm_bwd_workspace_bytes(rows, D, io), R.device, workspace)
+    rc = L.ttt_rmsnorm_bwd(R.data_ptr(), _ptr(weight), dY.data_ptr(), _ptr(dR), eps,
+                           dX.data_ptr(), _ptr(dweight), rows, D, io, _ptr(ws),
+                           0 if ws is None else ws.numel(), _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_rmsnorm_bwd")
     return dX, dweight
@@ -728,37 +745,44 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
     the list of tensors to write, which may be grads itself (in place); None makes new
     ones.  Returns (outs, norm): norm is a [1] fp32 device tensor."""
     import torch
+    grads = list(grads)
     n = len(grads)
     if n == 0 and norm is None:
         raise ValueError("no gradients, and no tensor for the norm")
-    dev = grads[0].device if n else norm.device
-    dtypes = (ctypes.c_int * n)()
-    sizes = (ctypes.c_longlong * n)()
-    gp = (ctypes.c_void_p * n)()
-    op = (ctypes.c_void_p * n)()
-    for k, g in enumerate(grads):
-        dtypes[k] = _first(g, "grads[%d]" % k)
-        if g.device != dev:
-            raise ValueError("grads[%d] is on %s, expected %s" % (k, g.device, dev))
-        sizes[k] = g.numel()
-        gp[k] = g.data_ptr()
-    if norm is not None:
+    ref = grads[0] if n else norm
+    dev = ref.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a device tensor" % ("grads[0]" if n else "norm"))
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return clip_grad_norm(grads, max_norm, eps, outs=outs, norm=norm, workspace=workspace)
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    kinds = [codes.get(g.dtype) if g.is_contiguous() and g.get_device() == dev else None
+             for g in grads]
+    if None in kinds:
+        k = kinds.index(None)
+        _first(grads[k], "grads[%d]" % k)       # says what is wrong with it
+        raise ValueError("grads[%d] is on %s, expected cuda:%d" % (k, grads[k].device, dev))
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=ref.device)
+    else:
         _match(norm, "norm", (1,), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if outs is None:
-            outs = [torch.empty_like(g) for g in grads]
-        if len(outs) != n:
-            raise ValueError("%d outputs for %d gradients" % (len(outs), n))
-        for k, (o, g) in enumerate(zip(outs, grads)):
-            if o is not g:
-                _match(o, "outs[%d]" % k, g.shape, g.dtype, dev)
-            op[k] = o.data_ptr()
-        if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=dev)
-        L = lib()
-        ws = _workspace(L.ttt_clip_workspace_bytes(), dev, workspace)
-        rc = L.ttt_clip_grad_norm(n, gp, op, sizes, dtypes, max_norm, eps, norm.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), st)
+    if outs is None:
+        outs = [torch.empty_like(g) for g in grads]
+    elif len(outs) != n:
+        raise ValueError("%d outputs for %d gradients" % (len(outs), n))
+    else:
+        for k in range(n):
+            if outs[k] is not grads[k]:
+                _match(outs[k], "outs[%d]" % k, grads[k].shape, grads[k].dtype, dev)
+    pointers, L = ctypes.c_void_p * n, lib()
+    ws = _workspace(L.ttt_clip_workspace_bytes(), ref.device, workspace)
+    rc = L.ttt_clip_grad_norm(n, pointers(*[g.data_ptr() for g in grads]),
+                              pointers(*[o.data_ptr() for o in outs]),
+                              (ctypes.c_longlong * n)(*[g.numel() for g in grads]),
+                              (ctypes.c_int * n)(*kinds), max_norm, eps, norm.data_ptr(),
+                              ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if rc != OK:
         raise TTTError(rc, "ttt_clip_grad_norm")
     return outs, norm

@@ -8,7 +8,7 @@ import pytest
 from test_sequence_layers_ttt_amd import ttt
 
 A = 0x10000000            # far apart, aligned, never dereferenced
-STEP = 0x1000000
+STEP = 0x10000000
 P = [A + k * STEP for k in range(12)]
 BIG = 1 << 40
 
