@@ -40,6 +40,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kShut = -__builtin_inff();   // the summed g of a run with a reset in it
 constexpr int kThreads = 256;
+constexpr int kTicket = 32;                  // words from ticket to ticket
 constexpr int kGroup = 8;                    // tiles of a group
 constexpr int kWindow = 8;                   // groups looked back over at once
 constexpr int kMostPolls = 1 << 22;          // seconds: only a workspace in use twice gets there
@@ -169,7 +170,9 @@ Layout layout_of(int d, bool bf16)
 
 constexpr int kRunFwd = 8, kRunBwd = 8;      // tokens of a thread's run
 
-// Workspace of a chain: tickets [sequences], then a 64-bit word for every channel slot of
+// Workspace of a chain: tickets [sequences], each in a cache line of its own (counts in one
+// line wait for each other, about 14 ns each: with the 15 of 15 x 4097 x 83 side by side the
+// last workgroup had its ticket after 9 us), then a 64-bit word for every channel slot of
 // every (sequence, tile), its pair (B above, S below), and one for every slot of every
 // (sequence, group), first the group's pair and then (state after the group, kShut): a
 // pair that needs no state before it.  A sequence here is one channel block of one row.
@@ -185,7 +188,8 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t chain_bytes(long long seqs, long long tiles, int width, Chain* c, void* ws)
 {
     const long long groups = (tiles + kGroup - 1) / kGroup;
-    const size_t t = up256(4 * (size_t)seqs), n = up256(8 * (size_t)seqs * tiles * width);
+    const size_t t = up256(4 * (size_t)kTicket * seqs);
+    const size_t n = up256(8 * (size_t)seqs * tiles * width);
     if (c) {
         unsigned char* p = (unsigned char*)ws;
         c->ticket = (unsigned*)p;
@@ -310,8 +314,8 @@ __device__ __forceinline__ Tile take_tile(const Layout& y, int d, int tiles, int
     t.j = 0;
     if (tiles > 1) {
         if (threadIdx.x == 0)
-            *lds = (int)__hip_atomic_fetch_add(chain.ticket + t.seq, 1u, __ATOMIC_RELAXED,
-                                               __HIP_MEMORY_SCOPE_AGENT);
+            *lds = (int)__hip_atomic_fetch_add(chain.ticket + (size_t)t.seq * kTicket, 1u,
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         t.j = *lds;
         if ((unsigned)t.j >= (unsigned)tiles) t.j = -1;
@@ -588,7 +592,7 @@ unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int&
     c = Chain{};
     if (nt > 1) {
         const size_t bytes = chain_bytes(ns, nt, y.width, &c, ws);
-        const size_t n = (bytes + 15) / 16, zeros = up256(4 * (size_t)ns) / 16;
+        const size_t n = (bytes + 15) / 16, zeros = up256(4 * (size_t)kTicket * ns) / 16;
         hipLaunchKernelGGL(gated_clear_kernel,
                            dim3((unsigned)std::min<size_t>(2048, (n + kThreads - 1) / kThreads)),
                            dim3(kThreads), 0, s, (uint4*)ws, zeros, n);
