@@ -16,12 +16,13 @@ using namespace ttt;
 
 namespace {
 
-bool gated_dims_ok(int B, int H, int T, int d)
+bool gated_dims_ok(int B, int H, int T, int d, int io_dtype)
 {
-    if (B <= 0 || H <= 0 || T <= 0 || d <= 0) return false;
-    // every element index inside 2^60, rows and the workgroups over them inside 2^31
+    if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || !dtype_ok(io_dtype)) return false;
+    // every element index inside 2^60, rows and grids inside 2^31
     const long double rows = (long double)B * H;
-    return rows * T * d < 1.0e18L && rows < 2.0e9L && rows * d * ((long double)T / 64 + 1) < 2.0e11L;
+    return rows * T * d < 1.0e18L && rows < 2.0e9L &&
+           gated_fits(B * H, T, d, io_dtype == TTT_DTYPE_BF16);
 }
 
 bool rms_dims_ok(long long rows, int D)
@@ -38,7 +39,7 @@ int gated_fwd_checked(const void* X, const void* G, const float* h0, void* Z, fl
     if (!aligned(X, 16) || !aligned(G, 16) || !aligned(Z, 16) || !aligned(h0, 16) ||
         !aligned(h_out, 16))
         return TTT_ERR_INVALID_ARG;
-    if (!gated_dims_ok(B, H, T, d) || !dtype_ok(io_dtype)) return TTT_ERR_INVALID_ARG;
+    if (!gated_dims_ok(B, H, T, d, io_dtype)) return TTT_ERR_INVALID_ARG;
     const size_t state = (size_t)B * H * d, n = state * T * elem_bytes(io_dtype);
     if (overlap(Z, n, X, n) || overlap(Z, n, G, n)) return TTT_ERR_INVALID_ARG;
     if ((h0 && overlap(Z, n, h0, 4 * state)) || (h_out && overlap(Z, n, h_out, 4 * state)))
@@ -60,7 +61,7 @@ extern "C" {
 
 size_t ttt_gated_workspace_bytes(int B, int H, int T, int d, int io_dtype)
 {
-    if (!gated_dims_ok(B, H, T, d) || !dtype_ok(io_dtype)) return 0;
+    if (!gated_dims_ok(B, H, T, d, io_dtype)) return 0;
     return gated_workspace(B * H, T, d, io_dtype == TTT_DTYPE_BF16);
 }
 
@@ -96,7 +97,7 @@ int ttt_gated_bwd(const void* G, const void* Z, const float* h0, const void* dZ,
     if (!aligned(G, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dX, 16) ||
         !aligned(dG, 16) || !aligned(h0, 16) || !aligned(dh_T, 16) || !aligned(dh0, 16))
         return TTT_ERR_INVALID_ARG;
-    if (!gated_dims_ok(B, H, T, d) || !dtype_ok(io_dtype)) return TTT_ERR_INVALID_ARG;
+    if (!gated_dims_ok(B, H, T, d, io_dtype)) return TTT_ERR_INVALID_ARG;
     const size_t state = (size_t)B * H * d, n = state * T * elem_bytes(io_dtype);
     const struct { const void* p; size_t n; } in[] = {{G, n}, {Z, n}, {dZ, n}, {h0, 4 * state},
                                                       {dh_T, 4 * state}},

@@ -19,7 +19,7 @@ struct GatedArgs {
     void* workspace;
 };
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s);
-// the same without workspace (few tokens)
+// the same by one thread per channel group, serial over the tokens (no workspace)
 hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s);
 
 struct GatedBwdArgs {
@@ -37,6 +37,7 @@ struct GatedBwdArgs {
 };
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s);
 size_t gated_workspace(int BH, int T, int d, bool bf16);
+bool gated_fits(int BH, int T, int d, bool bf16);
 
 // Root-mean-square norm over rows of D features.
 struct RmsArgs {

@@ -757,13 +757,19 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
     if on is not None:
         with on:
             return clip_grad_norm(grads, max_norm, eps, outs=outs, norm=norm, workspace=workspace)
+    # (whole lists at a time: a model has hundreds of tensors, and each check of one costs
+    # as much as scaling a small one)
+    tensor = torch.Tensor
+    types = [g.dtype for g in grads]
+    if any(map(dev.__ne__, map(tensor.get_device, grads))) \
+            or not all(map(tensor.is_contiguous, grads)):
+        for k, g in enumerate(grads):
+            _match(g, "grads[%d]" % k, g.shape, g.dtype, dev)
     codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-    kinds = [codes.get(g.dtype) if g.is_contiguous() and g.get_device() == dev else None
-             for g in grads]
+    kinds = [codes.get(t) for t in types]
     if None in kinds:
-        k = kinds.index(None)
-        _first(grads[k], "grads[%d]" % k)       # says what is wrong with it
-        raise ValueError("grads[%d] is on %s, expected cuda:%d" % (k, grads[k].device, dev))
+        raise TypeError("grads[%d] must be float32 or bfloat16, got %s"
+                        % (kinds.index(None), types[kinds.index(None)]))
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=ref.device)
     else:
@@ -772,15 +778,16 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
         outs = [torch.empty_like(g) for g in grads]
     elif len(outs) != n:
         raise ValueError("%d outputs for %d gradients" % (len(outs), n))
-    else:
+    elif [o.shape for o in outs] != [g.shape for g in grads] or [o.dtype for o in outs] != types \
+            or any(map(dev.__ne__, map(tensor.get_device, outs))) \
+            or not all(map(tensor.is_contiguous, outs)):
         for k in range(n):
-            if outs[k] is not grads[k]:
-                _match(outs[k], "outs[%d]" % k, grads[k].shape, grads[k].dtype, dev)
+            _match(outs[k], "outs[%d]" % k, grads[k].shape, types[k], dev)
     pointers, L = ctypes.c_void_p * n, lib()
     ws = _workspace(L.ttt_clip_workspace_bytes(), ref.device, workspace)
-    rc = L.ttt_clip_grad_norm(n, pointers(*[g.data_ptr() for g in grads]),
-                              pointers(*[o.data_ptr() for o in outs]),
-                              (ctypes.c_longlong * n)(*[g.numel() for g in grads]),
+    rc = L.ttt_clip_grad_norm(n, pointers(*map(tensor.data_ptr, grads)),
+                              pointers(*map(tensor.data_ptr, outs)),
+                              (ctypes.c_longlong * n)(*map(tensor.numel, grads)),
                               (ctypes.c_int * n)(*kinds), max_norm, eps, norm.data_ptr(),
                               ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if rc != OK:

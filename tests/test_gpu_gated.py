@@ -212,6 +212,36 @@ def test_step_continues_the_sequence(dev, io, d):
     check_fwd(X, G, h0, torch.cat(Zs, 2), h, io)
 
 
+@pytest.mark.parametrize("N,T,d,io", [(5000, 40, 64, "bf16"), (700, 60, 200, "f32"), (3000, 17, 50, "bf16")])
+def test_many_short_rows(dev, N, T, d, io):
+    """Rows that the serial kernel takes, and some that it does not."""
+    say("case", N, T, d, io)
+    X, G, h0 = make(dev, N, T, d, io, 55, resets=1)
+    Z, hT = ttt.gated_fwd(X, G, h0)
+    check_fwd(X, G, h0, Z, hT, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [3, 9, 83, 261, 520, 1029])
+@pytest.mark.parametrize("T", [1, 5, 40, 900])
+def test_state_in_place_at_any_width(dev, T, d, io):
+    """h_out at h0's place where the threads' channels do not divide the row: no channel's state is
+    read after it is written."""
+    import torch
+    X, G, h0 = make(dev, 6, T, d, io, 57)
+    Z, hT = ttt.gated_fwd(X, G, h0)
+    for k in range(3):
+        h = h0.clone()
+        Z2, _ = ttt.gated_fwd(X, G, h, h_out=h)
+        torch.cuda.synchronize()
+        assert torch.equal(Z, Z2) and torch.equal(hT, h)
+    check_fwd(X, G, h0, Z, hT, io)
+    h = h0.clone()
+    Z3 = ttt.gated_step(X, G, h)
+    torch.cuda.synchronize()
+    check_fwd(X, G, h0, Z3, h, io)
+
+
 def test_state_in_place(dev):
     """h_out at h0's place, over several tiles of a sequence."""
     import torch
