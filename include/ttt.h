@@ -393,8 +393,9 @@ int ttt_mlp_fwd_ex(const void* K, const void* Q, const void* V,
  * where the gate itself could not.
  *   - g_t <= 0 is required.  Values above 0 are not checked; the results are then
  *     unspecified (no access depends on them).
- *   - g_t = -inf forgets: h_t = x_t whatever h_{t-1} is, infinite and NaN included.
- *     Documents packed in one row start anew that way.
+ *   - g_t = -inf, or any g_t <= -1e30 (a type's lowest value as a mask), forgets:
+ *     h_t = x_t whatever h_{t-1} is, infinite and NaN included.  Documents packed in
+ *     one row start anew that way.
  *   - g_t = 0 with x_t = 0 carries the state through (padding of a shorter sequence:
  *     h_out is then the state at its own end).
  * Arithmetic is fp32 whatever the I/O type; every output is the same bits on every
@@ -403,7 +404,7 @@ int ttt_mlp_fwd_ex(const void* K, const void* Q, const void* V,
  *   h0      : [B, H, d] fp32 state before the first token, or NULL for zero.
  *   Z       : [B, H, T, d] in io_dtype (output; must not overlap an input).
  *   h_out   : [B, H, d] fp32 state after the last token (may alias h0), or NULL.
- *   d >= 1 (any), T >= 1; all pointers 16-byte aligned.
+ *   1 <= d <= 2^28, 1 <= T <= 2^30; all pointers 16-byte aligned.
  *   workspace : at least ttt_gated_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *           where that is 0).  Calls that may overlap in time need one each, graph
  *           replays included; its contents need not be kept between calls. */
@@ -426,7 +427,7 @@ int ttt_gated_step(const void* X, const void* G, float* h, void* Z,
  * L = <dZ, Z> + <dh_T, h_out>.  With lambda_T = dh_T,
  *   lambda_t = dz_t + exp(g_{t+1}) lambda_{t+1}   (g_T taken as 0),
  *   dx_t = lambda_t,   dg_t = exp(g_t) lambda_t h_{t-1},   dh0 = exp(g_0) lambda_0,
- * where a gate of g_t = -inf gives dg_t = 0 and passes nothing back.
+ * where a gate that forgets gives dg_t = 0 and passes nothing back.
  *   G       : as given to ttt_gated_fwd.
  *   Z       : what ttt_gated_fwd returned (h_{t-1} is read from it, in io_dtype).
  *   h0      : as given to ttt_gated_fwd (NULL for zero).
@@ -453,8 +454,8 @@ int ttt_gated_bwd(const void* G, const void* Z, const float* h0, const void* dZ,
  *   Y        : [rows, D] in io_dtype (output; may alias X).
  *   R        : [rows, D] in io_dtype (output: r, the residual of what follows; may alias
  *              residual or X, but not Y), or NULL to leave it out.
- *   eps      : > 0, finite.  rows >= 0 (0 does nothing), D >= 1; X, residual, Y and R
- *              16-byte aligned, weight 4-byte. */
+ *   eps      : > 0, finite.  rows >= 0 (0 does nothing), 1 <= D <= 2^28; X, residual,
+ *              Y and R 16-byte aligned, weight 4-byte. */
 int ttt_rmsnorm_fwd(const void* X, const void* residual, const float* weight, float eps,
                     void* Y, void* R, long long rows, int D, int io_dtype, void* stream);
 
@@ -503,7 +504,7 @@ size_t ttt_rmsnorm_bwd_workspace_bytes(long long rows, int D, int io_dtype);
  *              (TTT_ERR_INVALID_ARG), so a gradient that is listed twice is refused.
  *   sizes    : elements of each (0 allowed);  dtypes : ttt_dtype of each.
  *   max_norm : >= 0 (inf allowed);  eps : > 0, finite.
- *   norm     : DEVICE fp32 [1] (output).
+ *   norm     : DEVICE fp32 [1] (output; overlaps no tensor of the call).
  *   workspace: at least ttt_clip_workspace_bytes() bytes, 256-byte aligned; one for each
  *              call that may overlap in time.
  * Sums run in a fixed order: the same bits on every call. */

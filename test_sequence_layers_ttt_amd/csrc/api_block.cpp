@@ -16,10 +16,14 @@ using namespace ttt;
 
 namespace {
 
+constexpr int kMostFeatures = 1 << 28;
+
 bool gated_dims_ok(int B, int H, int T, int d, int io_dtype)
 {
     if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || !dtype_ok(io_dtype)) return false;
-    // every element index inside 2^60, rows and grids inside 2^31
+    // token and feature counts with room in an int, every element index inside 2^60, rows and
+    // grids inside 2^31
+    if (T > 1 << 30 || d > kMostFeatures) return false;
     const long double rows = (long double)B * H;
     return rows * T * d < 1.0e18L && rows < 2.0e9L &&
            gated_fits(B * H, T, d, io_dtype == TTT_DTYPE_BF16);
@@ -27,7 +31,7 @@ bool gated_dims_ok(int B, int H, int T, int d, int io_dtype)
 
 bool rms_dims_ok(long long rows, int D)
 {
-    return rows >= 0 && D > 0 && (long double)rows * D < 1.0e18L;
+    return rows >= 0 && D > 0 && D <= kMostFeatures && (long double)rows * D < 1.0e18L;
 }
 
 size_t elem_bytes(int io_dtype) { return io_dtype == TTT_DTYPE_BF16 ? 2 : 4; }
@@ -229,6 +233,7 @@ int ttt_clip_grad_norm(int n, const void* const* grads, void* const* outs,
             const size_t e = elem_bytes(dtypes[i]), bytes = (size_t)sizes[i] * e;
             if (!grads[i] || !aligned(grads[i], e)) return TTT_ERR_INVALID_ARG;
             const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+            if (overlap(grads[i], bytes, norm, 4)) return TTT_ERR_INVALID_ARG;
             if (!outs) continue;
             if (!outs[i] || !aligned(outs[i], e)) return TTT_ERR_INVALID_ARG;
             const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);

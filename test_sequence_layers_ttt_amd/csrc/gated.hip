@@ -2,8 +2,8 @@
 //
 // The step h -> exp(g) h + x is affine, and affine maps compose: a run of tokens is the
 // pair (sum of its g, B) with h_end = exp(sum g) h_start + B.  The gates' product is kept
-// as the sum of the g: -inf then marks a run with a reset in it, exactly, where a product
-// that underflowed would look the same.
+// as the sum of the g, with -inf for a run with a reset in it: a product that underflowed
+// would look the same.
 //
 // A tile is all that one workgroup holds in registers: `rows` runs of L tokens over the
 // channels of one block, each thread a run of L tokens of V neighbouring channels (16
@@ -39,6 +39,9 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kShut = -__builtin_inff();   // the summed g of a run with a reset in it
+// A gate below this (times log2(e)) is a reset: -inf, a type's lowest value.  Sums of the others
+// stay finite over any run.
+constexpr float kLowest = -1e30f * kLog2e;
 constexpr int kThreads = 256;
 constexpr int kTicket = 32;                  // words from ticket to ticket
 constexpr int kGroup = 8;                    // tiles of a group
@@ -124,10 +127,10 @@ struct Raw {
     }
 };
 
-// one token: g2 = g log2(e)
+// one token: g2 = g log2(e).  A reset takes x whatever h is, infinite and NaN included.
 __device__ __forceinline__ float token(float g2, float x, float h)
 {
-    return fmaf(__builtin_amdgcn_exp2f(g2), g2 == kShut ? 0.f : h, x);
+    return fmaf(__builtin_amdgcn_exp2f(g2), g2 <= kLowest ? 0.f : h, x);
 }
 
 // one run: (S, B) with S the summed g2.  The factor of an open run is kept above 0, so that an
@@ -447,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(
         for (int i = 0; i < V; ++i) {
             const float g2 = g[l].at(i) * kLog2e;
             B[i] = token(g2, x[l].at(i), B[i]);
-            S[i] = g2 == kShut ? kShut : S[i] + g2;
+            S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
     start_states<V>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, S, B, h);
     const int skip = own ? t.skip : 0;
@@ -509,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(
         for (int i = 0; i < V; ++i) {
             const float g2 = g[l].at(i) * kLog2e;
             B[i] = token(g2, dz[l].at(i), B[i]);
-            S[i] = g2 == kShut ? kShut : S[i] + g2;
+            S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
     start_states<V>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, S, B, lam);
     g[0].again();
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(
             if (first_token && l == n - 1) before = h0 ? h0[(size_t)t.row * d + t.c0 + i] : 0.f;
             const float g2 = g[l + 1].at(i) * kLog2e;
             const float back = token(g2, 0.f, lam[i]);
-            dg[i] = g2 == kShut ? 0.f : back * before;
+            dg[i] = g2 <= kLowest ? 0.f : back * before;
             if (dh0 && first_token && l == n - 1) dh0[(size_t)t.row * d + t.c0 + i] = back;
         }
         Raw<TIO, V> o;

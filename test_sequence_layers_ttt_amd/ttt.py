@@ -526,13 +526,23 @@ def _raw_stream(index) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _scratch(nbytes, like, workspace):
+    """_workspace for the operators below: a given one is bytes, on the tensors' device."""
+    if workspace is not None:
+        import torch
+        if workspace.device != like.device or workspace.dtype != torch.uint8 \
+                or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on %s" % like.device)
+    return _workspace(nbytes, like.device, workspace)
+
+
 def gated_workspace_bytes(B, H, T, d, io_dtype) -> int:
     return int(lib().ttt_gated_workspace_bytes(B, H, T, d, io_dtype))
 
 
 def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None) -> Tuple:
     """Gated linear recurrence h_t = exp(G_t) h_{t-1} + X_t over [B, H, T, d] fp32 or
-    bf16 (G <= 0; -inf starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
+    bf16 (G <= 0; -inf, or the type's lowest value, starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
     (Z, h_T): the states in the I/O type, and the last one in fp32."""
     import torch
     io, dev = _first(X, "X")
@@ -554,7 +564,7 @@ def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None)
     else:
         _match(h_out, "h_out", (B, H, d), torch.float32, dev)
     L = lib()
-    ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), X.device, workspace)
+    ws = _scratch(L.ttt_gated_workspace_bytes(B, H, T, d, io), X, workspace)
     rc = L.ttt_gated_fwd(X.data_ptr(), G.data_ptr(), _ptr(h0), Z.data_ptr(), h_out.data_ptr(),
                          B, H, T, d, io, _ptr(ws), 0 if ws is None else ws.numel(),
                          _raw_stream(dev))
@@ -615,7 +625,7 @@ def gated_bwd(G, Z, dZ, h0=None, dh_T=None, *, dX=None, dG=None, dh0=None, works
     if dh0 is None:
         dh0 = torch.empty((B, H, d), dtype=torch.float32, device=G.device)
     L = lib()
-    ws = _workspace(L.ttt_gated_workspace_bytes(B, H, T, d, io), G.device, workspace)
+    ws = _scratch(L.ttt_gated_workspace_bytes(B, H, T, d, io), G, workspace)
     rc = L.ttt_gated_bwd(G.data_ptr(), Z.data_ptr(), _ptr(h0), dZ.data_ptr(), _ptr(dh_T),
                          dX.data_ptr(), dG.data_ptr(), dh0.data_ptr(), B, H, T, d, io, _ptr(ws),
                          0 if ws is None else ws.numel(), _raw_stream(dev))
@@ -725,7 +735,7 @@ def rmsnorm_bwd(R, weight, dY, dR=None, eps: float = 1e-6, *, dX=None, dweight=N
     L = lib()
     ws = None
     if dweight is not None:
-        ws = _workspace(L.ttt_rmsnorm_bwd_workspace_bytes(rows, D, io), R.device, workspace)
+        ws = _scratch(L.ttt_rmsnorm_bwd_workspace_bytes(rows, D, io), R, workspace)
     rc = L.ttt_rmsnorm_bwd(R.data_ptr(), _ptr(weight), dY.data_ptr(), _ptr(dR), eps,
                            dX.data_ptr(), _ptr(dweight), rows, D, io, _ptr(ws),
                            0 if ws is None else ws.numel(), _raw_stream(dev))
@@ -784,7 +794,7 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
         for k in range(n):
             _match(outs[k], "outs[%d]" % k, grads[k].shape, types[k], dev)
     pointers, L = ctypes.c_void_p * n, lib()
-    ws = _workspace(L.ttt_clip_workspace_bytes(), ref.device, workspace)
+    ws = _scratch(L.ttt_clip_workspace_bytes(), ref, workspace)
     rc = L.ttt_clip_grad_norm(n, pointers(*map(tensor.data_ptr, grads)),
                               pointers(*map(tensor.data_ptr, outs)),
                               (ctypes.c_longlong * n)(*map(tensor.numel, grads)),

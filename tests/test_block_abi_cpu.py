@@ -24,6 +24,7 @@ def gated(**kw):
     dict(X=None), dict(G=None), dict(Z=None), dict(X=P[0] + 8), dict(G=P[1] + 2), dict(Z=P[3] + 4),
     dict(h0=P[2] + 4), dict(h_out=P[4] + 8), dict(B=0), dict(H=-1), dict(T=0), dict(d=0),
     dict(io=2), dict(io=-1), dict(B=1 << 20, H=1 << 20), dict(T=1 << 30, d=1 << 30),
+    dict(T=(1 << 30) + 1), dict(T=0x7fffffff), dict(d=(1 << 28) + 1), dict(d=0x7fffffff),
     dict(Z=P[0]), dict(Z=P[1] + 16), dict(Z=P[2]), dict(h_out=P[0]), dict(h_out=P[3]),
     dict(h_out=P[2] + 16),                              # a shifted overlap of the states
 ])
@@ -75,7 +76,7 @@ def test_gated_step_refuses(kw):
 @pytest.mark.parametrize("kw", [
     dict(X=None), dict(Y=None), dict(X=P[0] + 8), dict(res=P[1] + 4), dict(w=P[2] + 2),
     dict(Y=P[3] + 8), dict(R=P[5] + 4), dict(rows=-1), dict(D=0), dict(D=-4), dict(io=2),
-    dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
+    dict(D=(1 << 28) + 1), dict(D=0x7fffffff), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
     dict(Y=P[1]), dict(Y=P[0] + 16), dict(R=P[3]), dict(R=P[0] + 32), dict(R=P[1] + 16), dict(w=P[3]),
     dict(w=P[5]),
 ])
@@ -112,7 +113,7 @@ def rms_bwd(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(R=None), -1), (dict(dY=None), -1), (dict(dX=None), -1), (dict(R=P[0] + 2), -1),
     (dict(dw=P[5] + 2), -1), (dict(eps=0.0), -1), (dict(rows=-2), -1), (dict(D=0), -1),
-    (dict(io=9), -1), (dict(dX=P[0]), -1), (dict(dX=P[2] + 16), -1), (dict(dX=P[3] + 16), -1),
+    (dict(io=9), -1), (dict(D=0x7fffffff), -1), (dict(dX=P[0]), -1), (dict(dX=P[2] + 16), -1), (dict(dX=P[3] + 16), -1),
     (dict(dX=P[1]), -1), (dict(dw=P[0]), -1), (dict(dw=P[1]), -1), (dict(dw=P[4]), -1),
     (dict(ws=None), -3), (dict(wsb=3), -3), (dict(ws=P[6] + 64), -3),
 ])
@@ -149,6 +150,7 @@ def clip(ranges, outs=True, norm=P[11], max_norm=1.0, eps=1e-6, ws=P[10], wsb=BI
     [(P[0], P[2], 4, 0), (P[1], P[0], 4, 0)],              # an output on another's input
     [(P[0], P[1] - 396, 100, 0), (P[1], P[3], 4, 0)],      # reaching into another's input
     [(P[0], P[11] - 8, 4, 0)],                             # on the norm
+    [(P[11] - 8, P[0], 4, 0)],
 ])
 def test_clip_refuses_tensors(ranges):
     assert clip(ranges) == ttt.ERR_INVALID_ARG

@@ -273,6 +273,14 @@ def test_binding_refuses(dev):
         ttt.gated_fwd(X.half(), G.half())
     with pytest.raises(ttt.TTTError):
         ttt.gated_fwd(X, G, Z=X)
+    big = ttt.gated_workspace_bytes(1, 2, 4096, 16, 0)
+    XL, GL = (t.repeat(1, 1, 512, 1) for t in (X, G))
+    for ws in (torch.empty(big, dtype=torch.uint8), torch.empty(big, device=dev),
+               torch.empty(2 * big, dtype=torch.uint8, device=dev)[::2]):
+        with pytest.raises(ValueError):
+            ttt.gated_fwd(XL, GL, workspace=ws)
+    with pytest.raises(ttt.TTTError):
+        ttt.gated_fwd(XL, GL, workspace=torch.empty(big - 1, dtype=torch.uint8, device=dev))
     with pytest.raises(ValueError):
         ttt.rmsnorm_fwd(X, torch.ones(8, device=dev))
     with pytest.raises(ValueError):

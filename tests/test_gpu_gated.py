@@ -179,6 +179,28 @@ def test_what_is_not_finite_ends_at_a_reset(dev, at):
         assert np.array_equal(np.isnan(np64(got_k)), np.isnan(want_k))
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [12, 700])
+def test_the_lowest_value_is_a_reset(dev, T, io):
+    """Masks of a type's lowest value, and of -1e30, forget like -inf, bit for bit and NaN included."""
+    import torch
+    X, G, h0 = make(dev, 3, T, 64, io, 33)
+    X[0, 0, 2, 5] = float("nan")
+    h0[0, 1, 7] = float("inf")
+    want = None
+    for value in (-float("inf"), torch.finfo(G.dtype).min, -1.01e30):
+        G[:, :, 5] = value
+        G[:, :, T - 3] = value
+        G[:, :, T // 2] = value
+        Z, hT = ttt.gated_fwd(X, G, h0)
+        back = ttt.gated_bwd(G, Z.nan_to_num(0.0, 0.0, 0.0), X.nan_to_num(0.0, 0.0, 0.0), None, None)
+        got = [t.nan_to_num(3.0, 4.0, 5.0) for t in (Z, hT) + back]
+        assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+        want = got
+        assert torch.isfinite(Z[:, :, 5:]).all()
+        assert all((back[1][:, :, t] == 0).all() for t in (5, T // 2, T - 3))
+
+
 def test_packed_documents_are_the_separate_ones(dev):
     import torch
     lens = [1, 255, 256, 7, 600, 1, 1, 300]
