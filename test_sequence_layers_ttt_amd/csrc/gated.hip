@@ -335,6 +335,36 @@ __device__ __forceinline__ Tile take_tile(const Layout& y, int d, int tiles, int
     return t;
 }
 
+// V floats of LDS, 4 V-byte aligned: in 16-byte accesses (single words of lanes V apart would meet
+// in the same banks)
+template <int V>
+__device__ __forceinline__ void lds_put(float* p, const float (&v)[V])
+{
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = v[i];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void lds_get(const float* p, float (&v)[V])
+{
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + i);
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = p[i];
+    }
+}
+
 // The start state of each thread's run, from its pairs (S, B) and the states that enter the
 // sequence (`first` of the row's channels, or nullptr for zero).
 template <int V>
@@ -343,14 +373,17 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
                                              const float (&S)[V], const float (&B)[V],
                                              float (&h)[V])
 {
-    __shared__ float sS[kThreads * V], sB[kThreads * V], pS[kThreads], pB[kThreads];
+    __shared__ __align__(16) float sS[kThreads * V], sB[kThreads * V], pS[kThreads], pB[kThreads];
     const int w = y.width, tid = threadIdx.x;
     if (t.r < y.rows) {
+        float s[V], b[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            sS[t.r * w + t.lane * V + i] = t.on ? S[i] : 0.f;
-            sB[t.r * w + t.lane * V + i] = t.on ? B[i] : 0.f;
+            s[i] = t.on ? S[i] : 0.f;
+            b[i] = t.on ? B[i] : 0.f;
         }
+        lds_put<V>(sS + t.r * w + t.lane * V, s);
+        lds_put<V>(sB + t.r * w + t.lane * V, b);
     }
     __syncthreads();
     // threads as (part, channel): each part's runs in turn, exclusive pairs left in place
@@ -407,12 +440,12 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
     __syncthreads();
     if (t.on) {
-        const int p = t.r / y.per;
+        float s[V], b[V], start[V];
+        lds_get<V>(sS + t.r * w + t.lane * V, s);
+        lds_get<V>(sB + t.r * w + t.lane * V, b);
+        lds_get<V>(pB + t.r / y.per * w + t.lane * V, start);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int k = t.r * w + t.lane * V + i;
-            h[i] = run(sS[k], sB[k], pB[p * w + t.lane * V + i]);
-        }
+        for (int i = 0; i < V; ++i) h[i] = run(s[i], b[i], start[i]);
     }
 }
 
