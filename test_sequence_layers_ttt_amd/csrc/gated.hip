@@ -149,11 +149,13 @@ struct Layout {
     int parts;    // parts that the scan over the runs is split into
     int per;      // runs of a part
     int width;    // lanes * V: channel slots of a block
+    int threads;  // of a workgroup
 };
 
-Layout layout_of(int d, bool bf16)
+Layout layout_of(int d, bool bf16, int threads)
 {
     Layout y;
+    y.threads = threads;
     y.V = bf16 ? 8 : 4;
     while (y.V > d) y.V >>= 1;
     // Where rows are whole cache lines, a block is one line wide, or two where that makes more
@@ -161,12 +163,12 @@ Layout layout_of(int d, bool bf16)
     // forward: 17.5 us with lines, 19.2 with whole rows; x 96: 20.7 and 26.3).  Elsewhere
     // blocks would share lines (x 80: 29.2 with lines, 24.1 with whole rows).
     const int groups = (d + y.V - 1) / y.V, bytes = d * (bf16 ? 2 : 4);
-    const int most = bytes % 128 ? kThreads / y.V : bytes <= 512 ? 8 : 16;
+    const int most = bytes % 128 ? 256 / y.V : bytes <= 512 ? 8 : 16;
     y.blocks = (groups + most - 1) / most;
     y.lanes = (groups + y.blocks - 1) / y.blocks;
-    y.rows = kThreads / y.lanes;
+    y.rows = threads / y.lanes;
     y.width = y.lanes * y.V;
-    y.parts = std::min({kThreads / y.width, y.rows, 16});
+    y.parts = std::min({threads / y.width, y.rows, 16});
     y.per = (y.rows + y.parts - 1) / y.parts;
     return y;
 }
@@ -367,13 +369,13 @@ __device__ __forceinline__ void lds_get(const float* p, float (&v)[V])
 
 // The start state of each thread's run, from its pairs (S, B) and the states that enter the
 // sequence (`first` of the row's channels, or nullptr for zero).
-template <int V>
+template <int V, int NT>
 __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int d, int tiles,
                                              const Chain& chain, const float* first,
                                              const float (&S)[V], const float (&B)[V],
                                              float (&h)[V])
 {
-    __shared__ __align__(16) float sS[kThreads * V], sB[kThreads * V], pS[kThreads], pB[kThreads];
+    __shared__ __align__(16) float sS[NT * V], sB[NT * V], pS[NT], pB[NT];
     const int w = y.width, tid = threadIdx.x;
     if (t.r < y.rows) {
         float s[V], b[V];
@@ -451,8 +453,8 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
 
 // own: the states are updated in place, so a channel is written by one group alone (the
 // other group's copy may have started from what was written).
-template <typename TIO, int V>
-__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(
+template <typename TIO, int V, int NT>
+__global__ __launch_bounds__(NT) void gated_fwd_kernel(
     const TIO* __restrict__ X, const TIO* __restrict__ G, const float* h0, TIO* __restrict__ Z,
     float* h_out, int T, int d, int tiles, int seqs, Layout y, Chain chain, bool own)
 {
@@ -485,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(
             B[i] = token(g2, x[l].at(i), B[i]);
             S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
-    start_states<V>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, S, B, h);
+    start_states<V, NT>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, S, B, h);
     const int skip = own ? t.skip : 0;
 #pragma unroll
     for (int l = 0; l < L; ++l) {
@@ -505,8 +507,8 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(
     }
 }
 
-template <typename TIO, int V>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(
+template <typename TIO, int V, int NT>
+__global__ __launch_bounds__(NT) void gated_bwd_kernel(
     const TIO* __restrict__ G, const TIO* __restrict__ Z, const float* __restrict__ h0,
     const TIO* __restrict__ dZ, const float* __restrict__ dh_T, TIO* __restrict__ dX,
     TIO* __restrict__ dG, float* __restrict__ dh0, int T, int d, int tiles, int seqs, Layout y,
@@ -547,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(
             B[i] = token(g2, dz[l].at(i), B[i]);
             S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
-    start_states<V>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, S, B, lam);
+    start_states<V, NT>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, S, B, lam);
     g[0].again();
 #pragma unroll
     for (int l = 0; l < L; ++l) {
@@ -615,7 +617,33 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
     }
 }
 
-long long tiles_of(const Layout& y, int T, int L) { return (T + (long long)y.rows * L - 1) / ((long long)y.rows * L); }
+long long tiles_of(const Layout& y, int T, int L)
+{
+    return (T + (long long)y.rows * L - 1) / ((long long)y.rows * L);
+}
+
+// Workgroups of 512 threads where they hold a row's tokens in one tile and ones of 256 do not: no
+// chain to clear and to wait for.  bf16, d = 64, with 512 and with 256: 96 rows of 512 tokens,
+// forward 10.3 and 13.2 us, backward 14.5 and 15.7; 256 rows 12.3 and 15.2, 17.7 and 21.0.  (Rows
+// of two tiles and more gain nothing from 512: 96 x 2048 22.0 and 20.2 us.)  The backward kernel's
+// registers allow one such workgroup a compute unit, so it takes them up to 256: 384 rows of 512
+// are 31.6 and 25.4 us.
+bool one_tile_of_512(const Layout& y256, const Layout& y512, bool bf16, int T, int L)
+{
+    return y256.V == (bf16 ? 8 : 4) && tiles_of(y256, T, L) > 1 && tiles_of(y512, T, L) == 1;
+}
+
+Layout fwd_layout(int T, int d, bool bf16)
+{
+    const Layout y = layout_of(d, bf16, 256), z = layout_of(d, bf16, 512);
+    return one_tile_of_512(y, z, bf16, T, kRunFwd) ? z : y;
+}
+
+Layout bwd_layout(int BH, int T, int d, bool bf16)
+{
+    const Layout y = layout_of(d, bf16, 256), z = layout_of(d, bf16, 512);
+    return one_tile_of_512(y, z, bf16, T, kRunBwd) && (long long)BH * z.blocks <= 256 ? z : y;
+}
 
 // Sets up the chain of a call: the number of workgroups, or 0 where they would be too many.
 unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int& tiles, int& seqs,
@@ -636,18 +664,47 @@ unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int&
     return (unsigned)(nt * ns);
 }
 
-template <typename TIO, int V>
-hipError_t fwd_v(const GatedArgs& a, const Layout& y, hipStream_t s)
+template <typename TIO, int V, int NT>
+hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
 {
     Chain c;
     int tiles, seqs;
     const unsigned grid = prepare(y, a.BH, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
     if (!grid) return hipErrorInvalidValue;
     const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
-    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V>), dim3(grid), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT>), dim3(grid), dim3(NT), 0, s,
                        (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d, tiles,
                        seqs, y, c, own);
     return hipGetLastError();
+}
+
+template <typename TIO, int V, int NT>
+hipError_t bwd_nt(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
+{
+    Chain c;
+    int tiles, seqs;
+    const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
+    if (!grid) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT>), dim3(grid), dim3(NT), 0, s,
+                       (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
+                       (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
+    return hipGetLastError();
+}
+
+template <typename TIO, int V>
+hipError_t fwd_v(const GatedArgs& a, const Layout& y, hipStream_t s)
+{
+    if constexpr (V * sizeof(TIO) == 16)
+        if (y.threads == 512) return fwd_nt<TIO, V, 512>(a, y, s);
+    return fwd_nt<TIO, V, 256>(a, y, s);
+}
+
+template <typename TIO, int V>
+hipError_t bwd_v(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
+{
+    if constexpr (V * sizeof(TIO) == 16)
+        if (y.threads == 512) return bwd_nt<TIO, V, 512>(a, y, s);
+    return bwd_nt<TIO, V, 256>(a, y, s);
 }
 
 template <typename TIO, int V>
@@ -660,19 +717,6 @@ hipError_t step_v(const GatedArgs& a, hipStream_t s)
     hipLaunchKernelGGL((gated_step_kernel<TIO, V>), dim3((unsigned)grid), dim3(kThreads), 0, s,
                        (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d,
                        groups, n, own);
-    return hipGetLastError();
-}
-
-template <typename TIO, int V>
-hipError_t bwd_v(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
-{
-    Chain c;
-    int tiles, seqs;
-    const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
-    if (!grid) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V>), dim3(grid), dim3(kThreads), 0, s,
-                       (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
-                       (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
     return hipGetLastError();
 }
 
@@ -690,7 +734,7 @@ hipError_t bwd_v(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
 // Whether every grid of the shape stays inside 2^31 workgroups.
 bool gated_fits(int BH, int T, int d, bool bf16)
 {
-    const Layout y = layout_of(d, bf16);
+    const Layout y = layout_of(d, bf16, 256);
     const long double most = 0x7fffffff, rows = BH;
     return rows * y.blocks * std::max(tiles_of(y, T, kRunFwd), tiles_of(y, T, kRunBwd)) <= most &&
            rows * ((d + y.V - 1) / y.V) / kThreads + 1 <= most;
@@ -698,19 +742,20 @@ bool gated_fits(int BH, int T, int d, bool bf16)
 
 size_t gated_workspace(int BH, int T, int d, bool bf16)
 {
-    const Layout y = layout_of(d, bf16);
     size_t n = 0;
-    for (int L : {kRunFwd, kRunBwd}) {
+    auto add = [&](const Layout& y, int L) {
         const long long tiles = tiles_of(y, T, L);
         if (tiles > 1)
             n = std::max(n, chain_bytes((long long)BH * y.blocks, tiles, y.width, nullptr, nullptr));
-    }
+    };
+    add(fwd_layout(T, d, bf16), kRunFwd);
+    add(bwd_layout(BH, T, d, bf16), kRunBwd);
     return n;
 }
 
 hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s)
 {
-    const int V = layout_of(a.d, a.bf16).V;
+    const int V = layout_of(a.d, a.bf16, 256).V;
     if (a.bf16) {
         GATED_BY_WIDTH(V, (step_v<uint16_t, W>(a, s)))
         return step_v<uint16_t, 8>(a, s);
@@ -724,7 +769,7 @@ hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s)
 // 32 15.0 / 12.7; 10000 rows of 16 15.1 / 80.5, of 32 29.4 / 81.4, of 64 61 / 83.
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s)
 {
-    const Layout y = layout_of(a.d, a.bf16);
+    const Layout y = fwd_layout(a.T, a.d, a.bf16);
     const long long threads = (long long)a.BH * ((a.d + y.V - 1) / y.V);
     if (a.T <= 16 || (a.T <= 64 && threads >= 1 << 15)) return launch_gated_step(a, s);
     if (a.bf16) {
@@ -737,7 +782,7 @@ hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s)
 
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s)
 {
-    const Layout y = layout_of(a.d, a.bf16);
+    const Layout y = bwd_layout(a.BH, a.T, a.d, a.bf16);
     if (a.bf16) {
         GATED_BY_WIDTH(y.V, (bwd_v<uint16_t, W>(a, y, s)))
         return bwd_v<uint16_t, 8>(a, y, s);

@@ -97,7 +97,7 @@ def test_widths(dev, d, io):
 
 
 @pytest.mark.parametrize("N,T,d,io", [(96, 520, 64, "bf16"), (2, 20011, 64, "bf16"), (1, 9000, 3, "f32"),
-                                      (300, 70, 16, "bf16"), (1, 40000, 1, "bf16"), (7, 3001, 83, "f32")])
+                                      (300, 70, 16, "bf16"), (300, 400, 64, "bf16"), (40, 500, 128, "f32"), (1, 40000, 1, "bf16"), (7, 3001, 83, "f32")])
 def test_sizes(dev, N, T, d, io):
     say("case", N, T, d, io)
     X, G, h0 = make(dev, N, T, d, io, 500, resets=3)
