@@ -48,14 +48,16 @@ constexpr int kGroup = 8;                    // tiles of a group
 constexpr int kWindow = 8;                   // groups looked back over at once
 constexpr int kMostPolls = 1 << 22;          // seconds: only a workspace in use twice gets there
 
-// V elements of the I/O type at any element-aligned address, as raw words.  Every tensor is
-// read or written once: 16-byte accesses take the non-temporal policy (8 x 12 x 2048 x 64
-// bf16, forward / backward: 23.1 / 32.2 us without, 21.6 / 27.8 us with; 1 x 32 x 32768 x
-// 64: 105 / 162 and 93 / 144 us).
+// V elements of the I/O type at any element-aligned address, as raw words.  Where rows are whole
+// cache lines (LINES), every line is read or written once, at once, and 16-byte accesses take the
+// non-temporal policy (8 x 12 x 2048 x 64 bf16, forward / backward: 23.1 / 32.2 us without, 21.6 /
+// 27.8 with; 1 x 32 x 32768 x 64: 105 / 162 and 93 / 144).  Elsewhere a line takes several accesses,
+// which meet in the caches only without it (64 x 32768 x 16 bf16: 106 / 262 us with, 55 / 101
+// without; 64 x 8192 x 50: 64 / 139 and 46 / 77).
 typedef uint32_t quad __attribute__((ext_vector_type(4)));
 typedef quad quad_any __attribute__((aligned(2)));
 
-template <typename TIO, int V>
+template <typename TIO, int V, bool LINES>
 struct Raw {
     static constexpr int BYTES = V * (int)sizeof(TIO);
     static constexpr int WORDS = (BYTES + 3) / 4;
@@ -64,7 +66,8 @@ struct Raw {
     __device__ __forceinline__ void load(const TIO* p)
     {
         if constexpr (BYTES == 16) {
-            const quad q = __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(p));
+            auto from = reinterpret_cast<const quad_any*>(p);
+            const quad q = LINES ? __builtin_nontemporal_load(from) : *from;
             w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
             return;
         }
@@ -76,7 +79,9 @@ struct Raw {
     {
         if constexpr (BYTES == 16) {
             const quad q = {w[0], w[1], w[2], w[3]};
-            __builtin_nontemporal_store(q, reinterpret_cast<quad_any*>(p));
+            auto to = reinterpret_cast<quad_any*>(p);
+            if constexpr (LINES) __builtin_nontemporal_store(q, to);
+            else *to = q;
             return;
         }
         Mem m;
@@ -150,6 +155,7 @@ struct Layout {
     int per;      // runs of a part
     int width;    // lanes * V: channel slots of a block
     int threads;  // of a workgroup
+    bool lines;   // a row is whole cache lines
 };
 
 Layout layout_of(int d, bool bf16, int threads)
@@ -163,7 +169,8 @@ Layout layout_of(int d, bool bf16, int threads)
     // forward: 17.5 us with lines, 19.2 with whole rows; x 96: 20.7 and 26.3).  Elsewhere
     // blocks would share lines (x 80: 29.2 with lines, 24.1 with whole rows).
     const int groups = (d + y.V - 1) / y.V, bytes = d * (bf16 ? 2 : 4);
-    const int most = bytes % 128 ? 256 / y.V : bytes <= 512 ? 8 : 16;
+    y.lines = bytes % 128 == 0;
+    const int most = !y.lines ? 256 / y.V : bytes <= 512 ? 8 : 16;
     y.blocks = (groups + most - 1) / most;
     y.lanes = (groups + y.blocks - 1) / y.blocks;
     y.rows = threads / y.lanes;
@@ -453,7 +460,7 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
 
 // own: the states are updated in place, so a channel is written by one group alone (the
 // other group's copy may have started from what was written).
-template <typename TIO, int V, int NT>
+template <typename TIO, int V, int NT, bool LINES>
 __global__ __launch_bounds__(NT) void gated_fwd_kernel(
     const TIO* __restrict__ X, const TIO* __restrict__ G, const float* h0, TIO* __restrict__ Z,
     float* h_out, int T, int d, int tiles, int seqs, Layout y, Chain chain, bool own)
@@ -466,7 +473,7 @@ __global__ __launch_bounds__(NT) void gated_fwd_kernel(
     const int n = t.on ? (int)min(max(T - t0, 0ll), (long long)L) : 0;
     const size_t at = ((size_t)t.row * T + t0) * d + t.c0;
 
-    Raw<TIO, V> x[L], g[L];
+    Raw<TIO, V, LINES> x[L], g[L];
 #pragma unroll
     for (int l = 0; l < L; ++l) {
         x[l].zero();
@@ -496,7 +503,7 @@ __global__ __launch_bounds__(NT) void gated_fwd_kernel(
         x[l].again();
 #pragma unroll
         for (int i = 0; i < V; ++i) h[i] = token(g[l].at(i) * kLog2e, x[l].at(i), h[i]);
-        Raw<TIO, V> z;
+        Raw<TIO, V, LINES> z;
         z.put(h);
         z.store_from(Z + at + (size_t)l * d, skip);
     }
@@ -507,7 +514,7 @@ __global__ __launch_bounds__(NT) void gated_fwd_kernel(
     }
 }
 
-template <typename TIO, int V, int NT>
+template <typename TIO, int V, int NT, bool LINES>
 __global__ __launch_bounds__(NT) void gated_bwd_kernel(
     const TIO* __restrict__ G, const TIO* __restrict__ Z, const float* __restrict__ h0,
     const TIO* __restrict__ dZ, const float* __restrict__ dh_T, TIO* __restrict__ dX,
@@ -524,7 +531,7 @@ __global__ __launch_bounds__(NT) void gated_bwd_kernel(
     const size_t at = ((size_t)t.row * T + (T - 1 - p0)) * d + t.c0;
     const bool first_token = n > 0 && p0 + n == T;   // the run ends with token 0
 
-    Raw<TIO, V> dz[L], g[L + 1], z[L];               // g[l]: the gate after token l's
+    Raw<TIO, V, LINES> dz[L], g[L + 1], z[L];               // g[l]: the gate after token l's
     g[0].zero();
     if (n > 0 && p0 > 0) g[0].load(G + at + d);
 #pragma unroll
@@ -567,7 +574,7 @@ __global__ __launch_bounds__(NT) void gated_bwd_kernel(
             dg[i] = g2 <= kLowest ? 0.f : back * before;
             if (dh0 && first_token && l == n - 1) dh0[(size_t)t.row * d + t.c0 + i] = back;
         }
-        Raw<TIO, V> o;
+        Raw<TIO, V, LINES> o;
         o.put(lam);
         o.store(dX + at - (size_t)l * d);
         o.put(dg);
@@ -592,7 +599,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
     for (int i = 0; i < V; ++i) h[i] = h0 ? h0[row * d + c0 + i] : 0.f;
     size_t at = (size_t)row * T * d + c0;
     for (int t0 = 0; t0 < T; t0 += L, at += (size_t)L * d) {
-        Raw<TIO, V> x[L], g[L];
+        Raw<TIO, V, false> x[L], g[L];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             if (t0 + l < T) {
@@ -605,7 +612,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
             if (t0 + l >= T) break;
 #pragma unroll
             for (int i = 0; i < V; ++i) h[i] = token(g[l].at(i) * kLog2e, x[l].at(i), h[i]);
-            Raw<TIO, V> z;
+            Raw<TIO, V, false> z;
             z.put(h);
             z.store_from(Z + at + (size_t)l * d, skip);
         }
@@ -664,7 +671,7 @@ unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int&
     return (unsigned)(nt * ns);
 }
 
-template <typename TIO, int V, int NT>
+template <typename TIO, int V, int NT, bool LINES>
 hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
 {
     Chain c;
@@ -672,20 +679,20 @@ hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
     const unsigned grid = prepare(y, a.BH, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
     if (!grid) return hipErrorInvalidValue;
     const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
-    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT>), dim3(grid), dim3(NT), 0, s,
+    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
                        (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d, tiles,
                        seqs, y, c, own);
     return hipGetLastError();
 }
 
-template <typename TIO, int V, int NT>
+template <typename TIO, int V, int NT, bool LINES>
 hipError_t bwd_nt(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
 {
     Chain c;
     int tiles, seqs;
     const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
     if (!grid) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT>), dim3(grid), dim3(NT), 0, s,
+    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
                        (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
                        (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
     return hipGetLastError();
@@ -694,17 +701,23 @@ hipError_t bwd_nt(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
 template <typename TIO, int V>
 hipError_t fwd_v(const GatedArgs& a, const Layout& y, hipStream_t s)
 {
-    if constexpr (V * sizeof(TIO) == 16)
-        if (y.threads == 512) return fwd_nt<TIO, V, 512>(a, y, s);
-    return fwd_nt<TIO, V, 256>(a, y, s);
+    if constexpr (V * sizeof(TIO) == 16) {
+        if (y.threads == 512)
+            return y.lines ? fwd_nt<TIO, V, 512, true>(a, y, s) : fwd_nt<TIO, V, 512, false>(a, y, s);
+        if (y.lines) return fwd_nt<TIO, V, 256, true>(a, y, s);
+    }
+    return fwd_nt<TIO, V, 256, false>(a, y, s);
 }
 
 template <typename TIO, int V>
 hipError_t bwd_v(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
 {
-    if constexpr (V * sizeof(TIO) == 16)
-        if (y.threads == 512) return bwd_nt<TIO, V, 512>(a, y, s);
-    return bwd_nt<TIO, V, 256>(a, y, s);
+    if constexpr (V * sizeof(TIO) == 16) {
+        if (y.threads == 512)
+            return y.lines ? bwd_nt<TIO, V, 512, true>(a, y, s) : bwd_nt<TIO, V, 512, false>(a, y, s);
+        if (y.lines) return bwd_nt<TIO, V, 256, true>(a, y, s);
+    }
+    return bwd_nt<TIO, V, 256, false>(a, y, s);
 }
 
 template <typename TIO, int V>
