@@ -778,8 +778,8 @@ hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s)
 }
 
 // The serial kernel also takes short rows: a tile of them is mostly empty, and costs its
-// latencies all the same.  bf16, d = 64, serial / tiles: 1000 rows of 16 tokens 9.2 / 12.7 us, of
-// 32 15.0 / 12.7; 10000 rows of 16 15.1 / 80.5, of 32 29.4 / 81.4, of 64 61 / 83.
+// latencies all the same.  bf16, d = 64, serial / tiles: 1000 rows of 16 tokens 9.0 / 12.3 us, of
+// 32 15.0 / 12.0; 10000 rows of 16 14.8 / 73, of 32 28.4 / 75, of 64 56 / 76.
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s)
 {
     const Layout y = fwd_layout(a.T, a.d, a.bf16);

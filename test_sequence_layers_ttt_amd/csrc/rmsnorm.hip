@@ -2,16 +2,20 @@
 // with one scale per row, and the backward pass.
 //
 // A row of D features is held in registers by TPR threads, K vectors of 16 bytes each, so
-// every input is read once and every output written once: HBM bounds it.  Rows of up to
-// 64 K vectors stay within one wave (sums by lane exchanges, no LDS, no barrier); longer
-// ones take a workgroup.  A last vector that would pass the row's end starts early enough
+// every input is read once and every output written once: HBM bounds it (32768 x 2048
+// bf16 backward 99 us for 537 MB, 5.4 TB/s; 16384 x 2048 to e4m3 43 us for 235 MB; a
+// device copy reaches 5.2 TB/s).  Rows of up to 128 vectors stay within one wave (sums by
+// lane exchanges, no LDS, no barrier); longer ones take a workgroup: 256 threads with one
+// vector each beat one wave with four (16384 x 2048 to e4m3: 45 and 92 us), which had too
+// few loads under way.  A last vector that would pass the row's end starts early enough
 // to be whole: what it shares with the one before is left out of the sums and written
 // twice, with the same bits.  (All of a row's loads come before its first store, so
 // outputs may stand at their inputs' places.)
 //
 // dweight sums over the rows: each thread adds up its own columns over its workgroup's
-// rows, the workgroup's threads of one column are added in LDS, and a second kernel adds
-// the workgroups' planes, all in a fixed order.
+// rows, a wave's threads of one column are added by lane exchanges and the waves in LDS,
+// and a second kernel (4.7 us for 1024 planes of 2048) adds the workgroups' planes, all in
+// a fixed order.
 #include <stdint.h>
 
 #include <algorithm>
@@ -30,17 +34,23 @@ typedef quad quad_any __attribute__((aligned(2)));
 
 template <typename TIO> constexpr int kVec = 16 / (int)sizeof(TIO);
 
-// 16 bytes of the I/O type at any element-aligned address
-template <typename TIO>
+// 16 bytes of the I/O type at any element-aligned address; with the streaming policy where rows are
+// whole cache lines (LINES: 8192 x 4096 fp32 backward 96 us, against 106 without), without it where a
+// line takes several accesses, which then meet in the caches (200000 x 50 bf16 forward 8.7 us,
+// against 13.2)
+template <bool LINES, typename TIO>
 __device__ __forceinline__ quad load16(const TIO* p)
 {
-    return __builtin_nontemporal_load(reinterpret_cast<const quad_any*>(p));
+    auto from = reinterpret_cast<const quad_any*>(p);
+    return LINES ? __builtin_nontemporal_load(from) : *from;
 }
 
-template <typename TIO>
+template <bool LINES, typename TIO>
 __device__ __forceinline__ void store16(TIO* p, quad q)
 {
-    __builtin_nontemporal_store(q, reinterpret_cast<quad_any*>(p));
+    auto to = reinterpret_cast<quad_any*>(p);
+    if constexpr (LINES) __builtin_nontemporal_store(q, to);
+    else *to = q;
 }
 
 template <typename TIO>
@@ -190,7 +200,7 @@ template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
 // rows a thread has under way at once
 template <int TPR, int K> constexpr int kRows = TPR <= 64 && K == 1 ? 2 : 1;
 
-template <typename TIO, int TPR, int K, bool Q8>
+template <typename TIO, int TPR, int K, bool Q8, bool LINES>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
     const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, void* Y,
     float* scale, TIO* R, long long rows, int D)
@@ -220,8 +230,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
                 x[u][k] = z[u][k] = quad{0, 0, 0, 0};
                 if (r0 + u < rows && dup[k] < V) {
                     const size_t at = (size_t)(r0 + u) * D + col[k];
-                    x[u][k] = load16(X + at);
-                    if (residual) z[u][k] = load16(residual + at);
+                    x[u][k] = load16<LINES>(X + at);
+                    if (residual) z[u][k] = load16<LINES>(residual + at);
                 }
             }
 #pragma unroll
@@ -251,14 +261,14 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
             for (int k = 0; k < K; ++k) {
                 const bool mine = live && dup[k] < V;
                 const size_t at = (size_t)(r0 + u) * D + col[k];
-                if (R && mine) store16(R + at, narrow<TIO>(r[k]));
+                if (R && mine) store16<LINES>(R + at, narrow<TIO>(r[k]));
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     r[k][i] *= rate * w[k][i];
                     if constexpr (Q8) m = max_bits(m, magnitude(r[k][i]));
                 }
                 if constexpr (!Q8)
-                    if (mine) store16((TIO*)Y + at, narrow<TIO>(r[k]));
+                    if (mine) store16<LINES>((TIO*)Y + at, narrow<TIO>(r[k]));
             }
             if constexpr (Q8) {
                 const float sc = row_max<TPR>(m, lds) / kE4m3Max;
@@ -326,7 +336,7 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
     }
 }
 
-template <typename TIO, int TPR, int K>
+template <typename TIO, int TPR, int K, bool LINES>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
     const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
     float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
@@ -358,9 +368,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
             r[k] = y[k] = e[k] = quad{0, 0, 0, 0};
             if (live && dup[k] < V) {
                 const size_t at = (size_t)row * D + col[k];
-                r[k] = load16(R + at);
-                y[k] = load16(dY + at);
-                if (dR) e[k] = load16(dR + at);
+                r[k] = load16<LINES>(R + at);
+                y[k] = load16<LINES>(dY + at);
+                if (dR) e[k] = load16<LINES>(dR + at);
             }
         }
         float ss = 0.f, su = 0.f;
@@ -402,26 +412,31 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
                 dw[k][i] = live ? fmaf(yv[i], n, dw[k][i]) : dw[k][i];
                 rv[i] = fmaf(rate, yv[i] * w[k][i] - n * m, ev[i]);
             }
-            if (live && dup[k] < V) store16(dX + (size_t)row * D + col[k], narrow<TIO>(rv));
+            if (live && dup[k] < V) store16<LINES>(dX + (size_t)row * D + col[k], narrow<TIO>(rv));
         }
     }
     if (!plane) return;
     float* out = plane + (size_t)blockIdx.x * D;
     if constexpr (GROUPS > 1) {
-        // the groups' sums of each column slot, added in the groups' order
-        constexpr int SLOTS = TPR * K * V;
-        __shared__ float part[GROUPS * SLOTS];
+        // each column slot over the wave's groups, then over the waves
+        constexpr int SLOTS = TPR * K * V, WAVES = kBlock<TPR> / 64;
+        __shared__ float part[WAVES * SLOTS];
+        const int wave = threadIdx.x >> 6;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) part[group * SLOTS + (k * TPR + lane) * V + i] = dw[k][i];
+            for (int i = 0; i < V; ++i) {
+#pragma unroll
+                for (int o = TPR; o < 64; o <<= 1) dw[k][i] += __shfl_xor(dw[k][i], o);
+                if ((threadIdx.x & 63) < TPR) part[wave * SLOTS + (k * TPR + lane) * V + i] = dw[k][i];
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < SLOTS; c += kBlock<TPR>) {
             const int v = c / V, i = c % V, c0 = min(v * V, D - V);
             if (v >= vectors || i < v * V - c0) continue;
             float sum = part[c];
-#pragma unroll 4
-            for (int g = 1; g < GROUPS; ++g) sum += part[g * SLOTS + c];
+#pragma unroll
+            for (int g = 1; g < WAVES; ++g) sum += part[g * SLOTS + c];
             out[c0 + i] = sum;
         }
     } else {
@@ -490,50 +505,61 @@ struct Shape { int tpr, k; };
 Shape shape_of(int D, int vec)
 {
     const int n = (D + vec - 1) / vec;
-    if (D < vec || n > 2048) return {0, 0};
-    if (n <= 64) return {n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1};
+    if (D < vec || n > 4096) return {0, 0};
+    if (n <= 64) return {n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64, 1};
     if (n <= 128) return {64, 2};
-    if (n <= 512) return {256, n <= 256 ? 1 : 2};
-    return {1024, n <= 1024 ? 1 : 2};
+    if (n <= 1024) return {256, n <= 256 ? 1 : n <= 512 ? 2 : 4};
+    return {n <= 2048 ? 512 : 1024, 4};
 }
 
-constexpr long long kMostBlocks = 2048;    // eight a compute unit: each loads the weight once
-constexpr int kMostPlanes = 1024;
+// Workgroups of a launch: 1024 threads a compute unit, each with many rows, as each loads the weight
+// (16384 x 2048 bf16 to e4m3: 45.0 us with twice as many, 41.2 with these).
+template <int TPR> constexpr long long kMostBlocks = 256 * (1024 / kBlock<TPR>);
 
-// workgroups of the backward pass, each with a plane of dweight
-int planes_of(long long rows, int D, int vec)
+// The backward pass holds weight and dweight in fp32 next to three inputs: past 2048 vectors there
+// are no registers for that.
+Shape bwd_shape_of(int D, int vec)
 {
     const Shape s = shape_of(D, vec);
-    const int groups = s.tpr && s.tpr < 256 ? 256 / s.tpr : 1;
-    return (int)std::max(1ll, std::min<long long>((rows + groups - 1) / groups, kMostPlanes));
+    return s.tpr == 1024 ? Shape{0, 0} : s;
 }
 
-template <typename TIO, int TPR, int K>
+// Its workgroups, each with a plane of dweight: half of what the forward pass has where a thread
+// holds several vectors, as planes cost twice their size (8192 x 4096 bf16: 52.7 us, 60.5 with all;
+// 200000 x 100: 35.8 with half, 34.3 with all).
+int planes_of(long long rows, int D, int vec)
+{
+    const Shape s = bwd_shape_of(D, vec);
+    const int block = std::max(256, s.tpr), groups = s.tpr ? block / s.tpr : 1;
+    const long long most = 256 * (1024 / block) / (s.k > 1 ? 2 : 1);
+    return (int)std::max(1ll, std::min<long long>((rows + groups - 1) / groups, most));
+}
+
+template <typename TIO, int TPR, int K, bool LINES>
 void fwd_launch(const RmsArgs& a, hipStream_t s)
 {
     constexpr int PER = kBlock<TPR> / TPR * kRows<TPR, K>;
-    const dim3 grid((unsigned)std::min(kMostBlocks, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
-    if (a.scale)
-        hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, true>), grid, block, 0, s, (const TIO*)a.X,
-                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
-                           a.D);
-    else
-        hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, false>), grid, block, 0, s, (const TIO*)a.X,
-                           (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
-                           a.D);
+    const dim3 grid((unsigned)std::min(kMostBlocks<TPR>, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
+    auto kernel = a.scale ? rms_fwd_kernel<TIO, TPR, K, true, LINES>
+                          : rms_fwd_kernel<TIO, TPR, K, false, LINES>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, (const TIO*)a.X, (const TIO*)a.residual, a.weight,
+                       a.eps, a.Y, a.scale, (TIO*)a.R, a.rows, a.D);
 }
 
-template <typename TIO, int TPR, int K>
+template <typename TIO, int TPR, int K, bool LINES>
 void bwd_launch(const RmsBwdArgs& a, int planes, hipStream_t s)
 {
-    hipLaunchKernelGGL((rms_bwd_kernel<TIO, TPR, K>), dim3(planes), dim3(kBlock<TPR>), 0, s,
+    hipLaunchKernelGGL((rms_bwd_kernel<TIO, TPR, K, LINES>), dim3(planes), dim3(kBlock<TPR>), 0, s,
                        (const TIO*)a.R, a.weight, (const TIO*)a.dY, (const TIO*)a.dR, a.eps,
                        (TIO*)a.dX, a.dweight ? (float*)a.workspace : nullptr, a.rows, a.D);
 }
 
 // a case of the switches over shapes
-#define RMS_SHAPE(f, TPR, K, ...) \
-    case TPR * 8 + K: f<TIO, TPR, K>(__VA_ARGS__); break;
+#define RMS_SHAPE(f, TPR, K, ...)                                                       \
+    case TPR * 8 + K:                                                                   \
+        if (a.D * sizeof(TIO) % 128) f<TIO, TPR, K, false>(__VA_ARGS__);                \
+        else f<TIO, TPR, K, true>(__VA_ARGS__);                                         \
+        break;
 
 template <typename TIO>
 hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
@@ -541,6 +567,8 @@ hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
     const Shape shape = shape_of(a.D, kVec<TIO>);
     if (shape.tpr) {
         switch (shape.tpr * 8 + shape.k) {
+            RMS_SHAPE(fwd_launch, 2, 1, a, s)
+            RMS_SHAPE(fwd_launch, 4, 1, a, s)
             RMS_SHAPE(fwd_launch, 8, 1, a, s)
             RMS_SHAPE(fwd_launch, 16, 1, a, s)
             RMS_SHAPE(fwd_launch, 32, 1, a, s)
@@ -548,13 +576,14 @@ hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
             RMS_SHAPE(fwd_launch, 64, 2, a, s)
             RMS_SHAPE(fwd_launch, 256, 1, a, s)
             RMS_SHAPE(fwd_launch, 256, 2, a, s)
-            RMS_SHAPE(fwd_launch, 1024, 1, a, s)
-            RMS_SHAPE(fwd_launch, 1024, 2, a, s)
+            RMS_SHAPE(fwd_launch, 256, 4, a, s)
+            RMS_SHAPE(fwd_launch, 512, 4, a, s)
+            RMS_SHAPE(fwd_launch, 1024, 4, a, s)
         default: return hipErrorInvalidValue;
         }
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)std::min(kMostBlocks, a.rows)), block(256);
+    const dim3 grid((unsigned)std::min(kMostBlocks<256>, a.rows)), block(256);
     if (a.scale)
         hipLaunchKernelGGL((rms_fwd_loop_kernel<TIO, true>), grid, block, 0, s, (const TIO*)a.X,
                            (const TIO*)a.residual, a.weight, a.eps, a.Y, a.scale, (TIO*)a.R, a.rows,
@@ -569,10 +598,12 @@ hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
 template <typename TIO>
 hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
 {
-    const Shape shape = shape_of(a.D, kVec<TIO>);
+    const Shape shape = bwd_shape_of(a.D, kVec<TIO>);
     const int planes = planes_of(a.rows, a.D, kVec<TIO>);
     if (shape.tpr) {
         switch (shape.tpr * 8 + shape.k) {
+            RMS_SHAPE(bwd_launch, 2, 1, a, planes, s)
+            RMS_SHAPE(bwd_launch, 4, 1, a, planes, s)
             RMS_SHAPE(bwd_launch, 8, 1, a, planes, s)
             RMS_SHAPE(bwd_launch, 16, 1, a, planes, s)
             RMS_SHAPE(bwd_launch, 32, 1, a, planes, s)
@@ -580,8 +611,8 @@ hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
             RMS_SHAPE(bwd_launch, 64, 2, a, planes, s)
             RMS_SHAPE(bwd_launch, 256, 1, a, planes, s)
             RMS_SHAPE(bwd_launch, 256, 2, a, planes, s)
-            RMS_SHAPE(bwd_launch, 1024, 1, a, planes, s)
-            RMS_SHAPE(bwd_launch, 1024, 2, a, planes, s)
+            RMS_SHAPE(bwd_launch, 256, 4, a, planes, s)
+            RMS_SHAPE(bwd_launch, 512, 4, a, planes, s)
         default: return hipErrorInvalidValue;
         }
     } else {
