@@ -179,21 +179,35 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// y / scale where 1 / scale may leave fp32's range: a scale of 0 (a row of zeros) gives 0, and
-// one so small that it has few bits is held to the largest value
-__device__ __forceinline__ float small_quotient(float y, float scale)
-{
-    const float v = scale == 0.f ? 0.f : y / scale;
-    return v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;
-}
-
-// y / scale to a rounding, given 1 / scale to one: the quotient's remainder put right (at most
-// 448 and a rounding, as scale is the row's largest |y| / 448)
-__device__ __forceinline__ float quotient(float y, float scale, float inv)
-{
-    const float q = y * inv;
-    return fmaf(fmaf(-q, scale, y), inv, q);
-}
+// A row's e4m3 values.  y / scale is t / (max|t| / 448) with t = r * weight: the rate cancels, and
+// with it its error; the quotient's remainder is put right, so that what e4m3 rounds is off by
+// little more than t's own rounding (at most 448 and a rounding of that).  Where the divisor or its
+// reciprocal would leave fp32's range both are scaled by a power of two first; a scale of 0 (a row
+// of zeros) gives 0; a NaN or an infinity in the row makes it NaN throughout.
+struct Row8 {
+    float scale, top, inv, by;
+    bool rare;
+    __device__ __forceinline__ Row8(float most, float rate)
+    {
+        scale = most * rate / kE4m3Max;
+        by = scale == 0.f ? 0.f : most < 1e-30f ? 0x1p80f : most > 1e30f ? 0x1p-80f : 1.f;
+        rare = by != 1.f;
+        top = scale == 0.f ? 1.f : most * by / kE4m3Max;
+        inv = 1.f / top;
+    }
+    template <int V>
+    __device__ __forceinline__ void apply(float (&t)[V]) const
+    {
+        if (rare)
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] *= by;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float q = t[i] * inv;
+            t[i] = fmaf(fmaf(-q, top, t[i]), inv, q);
+        }
+    }
+};
 
 // threads of a workgroup
 template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
@@ -264,26 +278,19 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
                 if (R && mine) store16<LINES>(R + at, narrow<TIO>(r[k]));
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    r[k][i] *= rate * w[k][i];
+                    r[k][i] *= Q8 ? w[k][i] : rate * w[k][i];
                     if constexpr (Q8) m = max_bits(m, magnitude(r[k][i]));
                 }
                 if constexpr (!Q8)
                     if (mine) store16<LINES>((TIO*)Y + at, narrow<TIO>(r[k]));
             }
             if constexpr (Q8) {
-                const float sc = row_max<TPR>(m, lds) / kE4m3Max;
-                if (live && lane == 0) scale[r0 + u] = sc;
-                const float inv = 1.f / sc;
+                const Row8 row(row_max<TPR>(m, lds), rate);
+                if (live && lane == 0) scale[r0 + u] = row.scale;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     if (!live || dup[k] == V) continue;
-                    if (sc < 1e-30f) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) r[k][i] = small_quotient(r[k][i], sc);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) r[k][i] = quotient(r[k][i], sc, inv);
-                    }
+                    row.apply(r[k]);
                     unsigned q[V / 4];
 #pragma unroll
                     for (int i = 0; i < V / 4; ++i)
@@ -316,21 +323,23 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
             ss = fmaf(r, r, ss);
         }
         const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
-        float sc = 0.f;
+        float most = 0.f;
         if constexpr (Q8) {
             unsigned m = 0;
             for (int i = threadIdx.x; i < D; i += 256)
-                m = max_bits(m, magnitude(r_at(i) * (rate * (weight ? weight[i] : 1.f))));
-            sc = row_max<256>(m, lds) / kE4m3Max;
-            if (threadIdx.x == 0) scale[row] = sc;
+                m = max_bits(m, magnitude(r_at(i) * (weight ? weight[i] : 1.f)));
+            most = row_max<256>(m, lds);
         }
+        const Row8 row8(most, rate);
+        if (Q8 && threadIdx.x == 0) scale[row] = row8.scale;
         for (int i = threadIdx.x; i < D; i += 256) {
-            const float r = r_at(i);
-            const float y = r * (rate * (weight ? weight[i] : 1.f));
-            if constexpr (Q8)
-                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(small_quotient(y, sc), 0.f, 0.f, 0.f);
-            else
-                io<TIO>::store((TIO*)Y, base + i, y);
+            const float r = r_at(i), w = weight ? weight[i] : 1.f;
+            if constexpr (Q8) {
+                float t[1] = {r * w};
+                row8.apply(t);
+                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(t[0], 0.f, 0.f, 0.f);
+            } else
+                io<TIO>::store((TIO*)Y, base + i, r * (rate * w));
             if (R) io<TIO>::store(R, base + i, r);
         }
     }

@@ -182,6 +182,32 @@ def test_small_and_large_values(dev):
     check_bwd(X, w, dY, None, dX, dw, "f32")
 
 
+@pytest.mark.parametrize("D", [3, 64, 300, 70000])
+def test_e4m3_at_the_ends_of_fp32(dev, D):
+    """Rows and weights whose products, or whose reciprocals, leave fp32's range; a row so small that
+    its scale is 0."""
+    import torch
+    X, w, res, dY = make(dev, 6, D, "f32", 23)
+    X[0] *= 1e-36
+    X[1] *= 1e-31
+    X[2] *= 1e15
+    for far in (1.0, 1e17, 1e-10):
+        weight = w * far
+        Y8, scale, _ = ttt.rmsnorm_q8_fwd(X, weight, None, EPS)
+        check_q8(X[1:], weight, None, Y8[1:], scale[1:], None, "f32")
+        assert torch.isfinite(Y8[0].float()).all()
+        y, _ = ref.rmsnorm(np64(X), np64(weight), None, EPS)
+        err = np.abs(np64(Y8[0].float()) * np64(scale[0]) - y[0])
+        # half an e4m3 step is 2^-4 of the value down to 2^-6 of the scale and, as the steps stay 2^-9
+        # below that, 2^-10 of the scale at the bottom (70000 columns have values there); 2^-140: half
+        # a step of a scale that is a denormal number, 2^-150, times 448
+        room = np.maximum(np.abs(y[0]) * 2.0 ** -4, np64(scale[0]) * 2.0 ** -10) * 1.001
+        assert (err <= room + 2.0 ** -140).all()
+    X[0] *= 1e-9
+    Y8, scale, _ = ttt.rmsnorm_q8_fwd(X, w * 1e-10, None, EPS)
+    assert scale[0] == 0 and (Y8[0].float() == 0).all()
+
+
 def test_no_rows(dev):
     import torch
     X = torch.empty(0, 64, dtype=torch.bfloat16, device=dev)
