@@ -179,17 +179,23 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// A row's e4m3 values.  y / scale is t / (max|t| / 448) with t = r * weight: the rate cancels, and
-// with it its error; the quotient's remainder is put right, so that what e4m3 rounds is off by
-// little more than t's own rounding (at most 448 and a rounding of that).  Where the divisor or its
+// A row's e4m3 values.  y / scale is t / (max|t| / 448) with t = r * weight * (the rate's power of
+// two, which is exact): the rest of the rate cancels, and with it its error; the quotient's remainder
+// is put right, so that what e4m3 rounds is off by little more than t's own rounding (at most 448 and
+// a rounding of that).  Where the divisor or its
 // reciprocal would leave fp32's range both are scaled by a power of two first; a scale of 0 (a row
 // of zeros) gives 0; a NaN or an infinity in the row makes it NaN throughout.
 struct Row8 {
     float scale, top, inv, by;
     bool rare;
+    // the power of two in a rate (1 for a rate of 0, as of a row whose squares leave fp32's range)
+    __device__ __forceinline__ static float power(float rate)
+    {
+        return rate == 0.f ? 1.f : __uint_as_float(__float_as_uint(rate) & 0x7f800000u);
+    }
     __device__ __forceinline__ Row8(float most, float rate)
     {
-        scale = most * rate / kE4m3Max;
+        scale = most * (rate / power(rate)) / kE4m3Max;
         by = scale == 0.f ? 0.f : most < 1e-30f ? 0x1p80f : most > 1e30f ? 0x1p-80f : 1.f;
         rare = by != 1.f;
         top = scale == 0.f ? 1.f : most * by / kE4m3Max;
@@ -269,6 +275,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
                 }
             }
             const float rate = rsqrtf(row_sum<TPR>(ss, lds) * inv_d + eps);
+            const float by = Q8 ? Row8::power(rate) : rate;
             const bool live = r0 + u < rows;
             unsigned m = 0;
 #pragma unroll
@@ -278,7 +285,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
                 if (R && mine) store16<LINES>(R + at, narrow<TIO>(r[k]));
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    r[k][i] *= Q8 ? w[k][i] : rate * w[k][i];
+                    r[k][i] *= by * w[k][i];
                     if constexpr (Q8) m = max_bits(m, magnitude(r[k][i]));
                 }
                 if constexpr (!Q8)
@@ -323,23 +330,24 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
             ss = fmaf(r, r, ss);
         }
         const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
+        const float by = Q8 ? Row8::power(rate) : rate;
         float most = 0.f;
         if constexpr (Q8) {
             unsigned m = 0;
             for (int i = threadIdx.x; i < D; i += 256)
-                m = max_bits(m, magnitude(r_at(i) * (weight ? weight[i] : 1.f)));
+                m = max_bits(m, magnitude(r_at(i) * (by * (weight ? weight[i] : 1.f))));
             most = row_max<256>(m, lds);
         }
         const Row8 row8(most, rate);
         if (Q8 && threadIdx.x == 0) scale[row] = row8.scale;
         for (int i = threadIdx.x; i < D; i += 256) {
-            const float r = r_at(i), w = weight ? weight[i] : 1.f;
+            const float r = r_at(i), y = r * (by * (weight ? weight[i] : 1.f));
             if constexpr (Q8) {
-                float t[1] = {r * w};
+                float t[1] = {y};
                 row8.apply(t);
                 ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(t[0], 0.f, 0.f, 0.f);
             } else
-                io<TIO>::store((TIO*)Y, base + i, r * (rate * w));
+                io<TIO>::store((TIO*)Y, base + i, y);
             if (R) io<TIO>::store(R, base + i, r);
         }
     }
