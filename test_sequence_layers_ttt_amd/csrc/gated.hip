@@ -380,10 +380,16 @@ template <int V, int NT>
 __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int d, int tiles,
                                              const Chain& chain, const float* first,
                                              const float (&S)[V], const float (&B)[V],
-                                             float (&h)[V])
+                                             float (&start)[V])
 {
     __shared__ __align__(16) float sS[NT * V], sB[NT * V], pS[NT], pB[NT];
     const int w = y.width, tid = threadIdx.x;
+    const int part = tid / w, c = tid - part * w;
+    float h = 0.f;               // of the thread's channel slot, before the tile
+    if (part == 0 && t.j < kGroup && first) {
+        const int ch = t.channel(y, d, c);
+        if (ch >= 0) h = first[ch];
+    }
     if (t.r < y.rows) {
         float s[V], b[V];
 #pragma unroll
@@ -396,7 +402,6 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
     __syncthreads();
     // threads as (part, channel): each part's runs in turn, exclusive pairs left in place
-    const int part = tid / w, c = tid - part * w;
     const bool scans = part < y.parts;
     if (scans) {
         float s = 0.f, b = 0.f;
@@ -412,12 +417,9 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
     __syncthreads();
     if (part == 0) {
-        // the tile's pair, then the state before it, then every part's start
-        float h = 0.f;
-        if (t.j < kGroup && first) {
-            const int ch = t.channel(y, d, c);
-            if (ch >= 0) h = first[ch];
-        }
+        // the tile's pair, then the state before it, then every part's start.  The row's last tile
+        // may write where `first` is read, once every tile has published: so the read is done by then.
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(h) : : "memory");
         if (tiles > 1) {
             float s = 0.f, b = 0.f;
             for (int p = 0; p < y.parts; ++p) follow(s, b, pS[p * w + c], pB[p * w + c]);
@@ -449,12 +451,12 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
     __syncthreads();
     if (t.on) {
-        float s[V], b[V], start[V];
+        float s[V], b[V];
         lds_get<V>(sS + t.r * w + t.lane * V, s);
         lds_get<V>(sB + t.r * w + t.lane * V, b);
         lds_get<V>(pB + t.r / y.per * w + t.lane * V, start);
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = run(s[i], b[i], start[i]);
+        for (int i = 0; i < V; ++i) start[i] = run(s[i], b[i], start[i]);
     }
 }
 
