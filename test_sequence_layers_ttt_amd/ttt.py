@@ -752,8 +752,8 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
                    workspace=None, stream=None) -> Tuple:
     """The 2-norm over all tensors of the list `grads` (fp32 or bf16, any contiguous
     shapes, one device), and each of them times min(1, max_norm / (norm + eps)).  outs:
-    the list of tensors to write, which may be grads itself (in place); None makes new
-    ones.  Returns (outs, norm): norm is a [1] fp32 device tensor."""
+    the list of tensors to write, of the same types and numbers of elements, which may be
+    grads itself (in place); None makes new ones.  Returns (outs, norm): norm is a [1] fp32 device tensor."""
     import torch
     grads = list(grads)
     n = len(grads)
@@ -776,7 +776,7 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
         for k, g in enumerate(grads):
             _match(g, "grads[%d]" % k, g.shape, g.dtype, dev)
     codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-    kinds = [codes.get(t) for t in types]
+    kinds, sizes = [codes.get(t) for t in types], list(map(tensor.numel, grads))
     if None in kinds:
         raise TypeError("grads[%d] must be float32 or bfloat16, got %s"
                         % (kinds.index(None), types[kinds.index(None)]))
@@ -788,16 +788,19 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
         outs = [torch.empty_like(g) for g in grads]
     elif len(outs) != n:
         raise ValueError("%d outputs for %d gradients" % (len(outs), n))
-    elif [o.shape for o in outs] != [g.shape for g in grads] or [o.dtype for o in outs] != types \
+    elif list(map(tensor.numel, outs)) != sizes or [o.dtype for o in outs] != types \
             or any(map(dev.__ne__, map(tensor.get_device, outs))) \
             or not all(map(tensor.is_contiguous, outs)):
         for k in range(n):
-            _match(outs[k], "outs[%d]" % k, grads[k].shape, types[k], dev)
+            if outs[k].numel() != sizes[k]:
+                raise ValueError("outs[%d] has %d elements, grads[%d] %d"
+                                 % (k, outs[k].numel(), k, sizes[k]))
+            _match(outs[k], "outs[%d]" % k, outs[k].shape, types[k], dev)
     pointers, L = ctypes.c_void_p * n, lib()
     ws = _scratch(L.ttt_clip_workspace_bytes(), ref, workspace)
     rc = L.ttt_clip_grad_norm(n, pointers(*map(tensor.data_ptr, grads)),
                               pointers(*map(tensor.data_ptr, outs)),
-                              (ctypes.c_longlong * n)(*map(tensor.numel, grads)),
+                              (ctypes.c_longlong * n)(*sizes),
                               (ctypes.c_int * n)(*kinds), max_norm, eps, norm.data_ptr(),
                               ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if rc != OK:
