@@ -454,8 +454,8 @@ int ttt_gated_bwd(const void* G, const void* Z, const float* h0, const void* dZ,
  *   Y        : [rows, D] in io_dtype (output; may alias X).
  *   R        : [rows, D] in io_dtype (output: r, the residual of what follows; may alias
  *              residual or X, but not Y), or NULL to leave it out.
- *   eps      : > 0, finite.  rows >= 0 (0 does nothing), 1 <= D <= 2^28; X, residual,
- *              Y and R 16-byte aligned, weight 4-byte. */
+ *   eps      : > 0, finite and no denormal number.  rows >= 0 (0 does nothing),
+ *              1 <= D <= 2^28; X, residual, Y and R 16-byte aligned, weight 4-byte. */
 int ttt_rmsnorm_fwd(const void* X, const void* residual, const float* weight, float eps,
                     void* Y, void* R, long long rows, int D, int io_dtype, void* stream);
 

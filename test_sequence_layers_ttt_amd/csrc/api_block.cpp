@@ -130,7 +130,7 @@ static int rmsnorm_fwd(const void* X, const void* residual, const float* weight,
                        int io_dtype, void* stream)
 {
     if (!rms_dims_ok(rows, D) || !dtype_ok(io_dtype)) return TTT_ERR_INVALID_ARG;
-    if (!std::isfinite(eps) || !(eps > 0.f)) return TTT_ERR_INVALID_ARG;
+    if (!std::isnormal(eps) || !(eps > 0.f)) return TTT_ERR_INVALID_ARG;
     if (rows == 0) return TTT_OK;
     if (!X || !Y || (q8 && !scale)) return TTT_ERR_INVALID_ARG;
     if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(Y, 16) || !aligned(R, 16) ||
@@ -184,7 +184,7 @@ int ttt_rmsnorm_bwd(const void* R, const float* weight, const void* dY, const vo
                     void* workspace, size_t workspace_bytes, void* stream)
 {
     if (!rms_dims_ok(rows, D) || !dtype_ok(io_dtype)) return TTT_ERR_INVALID_ARG;
-    if (!std::isfinite(eps) || !(eps > 0.f)) return TTT_ERR_INVALID_ARG;
+    if (!std::isnormal(eps) || !(eps > 0.f)) return TTT_ERR_INVALID_ARG;
     if (rows > 0 && (!R || !dY || !dX)) return TTT_ERR_INVALID_ARG;
     if (!aligned(R, 16) || !aligned(dY, 16) || !aligned(dR, 16) || !aligned(dX, 16) ||
         !aligned(weight, 4) || !aligned(dweight, 4))

@@ -182,9 +182,9 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
 // A row's e4m3 values.  y / scale is t / (max|t| / 448) with t = r * weight * (the rate's power of
 // two, which is exact): the rest of the rate cancels, and with it its error; the quotient's remainder
 // is put right, so that what e4m3 rounds is off by little more than t's own rounding (at most 448 and
-// a rounding of that).  Where the divisor or its
-// reciprocal would leave fp32's range both are scaled by a power of two first; a scale of 0 (a row
-// of zeros) gives 0; a NaN or an infinity in the row makes it NaN throughout.
+// a rounding of that).  Where the divisor or its reciprocal would leave fp32's range both are scaled by
+// a power of two first; a scale of 0 (a row of zeros) gives 0; a NaN or an infinity in the row makes
+// it NaN throughout.
 struct Row8 {
     float scale, top, inv, by;
     bool rare;

@@ -76,7 +76,7 @@ def test_gated_step_refuses(kw):
 @pytest.mark.parametrize("kw", [
     dict(X=None), dict(Y=None), dict(X=P[0] + 8), dict(res=P[1] + 4), dict(w=P[2] + 2),
     dict(Y=P[3] + 8), dict(R=P[5] + 4), dict(rows=-1), dict(D=0), dict(D=-4), dict(io=2),
-    dict(D=(1 << 28) + 1), dict(D=0x7fffffff), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
+    dict(D=(1 << 28) + 1), dict(D=0x7fffffff), dict(eps=0.0), dict(eps=1e-40), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
     dict(Y=P[1]), dict(Y=P[0] + 16), dict(R=P[3]), dict(R=P[0] + 32), dict(R=P[1] + 16), dict(w=P[3]),
     dict(w=P[5]),
 ])
@@ -112,7 +112,7 @@ def rms_bwd(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(R=None), -1), (dict(dY=None), -1), (dict(dX=None), -1), (dict(R=P[0] + 2), -1),
-    (dict(dw=P[5] + 2), -1), (dict(eps=0.0), -1), (dict(rows=-2), -1), (dict(D=0), -1),
+    (dict(dw=P[5] + 2), -1), (dict(eps=0.0), -1), (dict(eps=1e-39), -1), (dict(rows=-2), -1), (dict(D=0), -1),
     (dict(io=9), -1), (dict(D=0x7fffffff), -1), (dict(dX=P[0]), -1), (dict(dX=P[2] + 16), -1), (dict(dX=P[3] + 16), -1),
     (dict(dX=P[1]), -1), (dict(dw=P[0]), -1), (dict(dw=P[1]), -1), (dict(dw=P[4]), -1),
     (dict(ws=None), -3), (dict(wsb=3), -3), (dict(ws=P[6] + 64), -3),
