@@ -654,12 +654,11 @@ Layout bwd_layout(int BH, int T, int d, bool bf16)
     return one_tile_of_512(y, z, bf16, T, kRunBwd) && (long long)BH * z.blocks <= 256 ? z : y;
 }
 
-// Sets up the chain of a call: the number of workgroups, or 0 where they would be too many.
+// Sets up the chain of a call: the number of workgroups (inside 2^31, see gated_fits).
 unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int& tiles, int& seqs,
                  hipStream_t s)
 {
     const long long nt = tiles_of(y, T, L), ns = (long long)BH * y.blocks;
-    if (nt * ns > 0x7fffffffll) return 0;
     tiles = (int)nt;
     seqs = (int)ns;
     c = Chain{};
@@ -679,7 +678,6 @@ hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
     Chain c;
     int tiles, seqs;
     const unsigned grid = prepare(y, a.BH, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
-    if (!grid) return hipErrorInvalidValue;
     const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
     hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
                        (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d, tiles,
@@ -693,7 +691,6 @@ hipError_t bwd_nt(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
     Chain c;
     int tiles, seqs;
     const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
-    if (!grid) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
                        (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
                        (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
@@ -727,7 +724,6 @@ hipError_t step_v(const GatedArgs& a, hipStream_t s)
 {
     const int groups = (a.d + V - 1) / V;
     const long long n = (long long)a.BH * groups, grid = (n + kThreads - 1) / kThreads;
-    if (grid > 0x7fffffffll) return hipErrorInvalidValue;
     const bool own = a.h0 && a.h0 == a.h_out;
     hipLaunchKernelGGL((gated_step_kernel<TIO, V>), dim3((unsigned)grid), dim3(kThreads), 0, s,
                        (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d,

@@ -273,6 +273,14 @@ def test_binding_refuses(dev):
         ttt.gated_fwd(X.half(), G.half())
     with pytest.raises(ttt.TTTError):
         ttt.gated_fwd(X, G, Z=X)
+    # contiguous, but not where a 16-byte access may start
+    off = torch.zeros(X.numel() + 1, device=dev)[1:].view(X.shape)
+    for call in (lambda: ttt.gated_fwd(off, G), lambda: ttt.gated_fwd(X, off),
+                 lambda: ttt.gated_step(X, off, h), lambda: ttt.gated_bwd(G, X, off),
+                 lambda: ttt.rmsnorm_fwd(off), lambda: ttt.rmsnorm_q8_fwd(X, None, off),
+                 lambda: ttt.rmsnorm_bwd(X, None, off)):
+        with pytest.raises(ttt.TTTError):
+            call()
     big = ttt.gated_workspace_bytes(1, 2, 4096, 16, 0)
     XL, GL = (t.repeat(1, 1, 512, 1) for t in (X, G))
     for ws in (torch.empty(big, dtype=torch.uint8), torch.empty(big, device=dev),
