@@ -404,7 +404,7 @@ int ttt_mlp_fwd_ex(const void* K, const void* Q, const void* V,
  *   h0      : [B, H, d] fp32 state before the first token, or NULL for zero.
  *   Z       : [B, H, T, d] in io_dtype (output; must not overlap an input).
  *   h_out   : [B, H, d] fp32 state after the last token (may alias h0), or NULL.
- *   1 <= d <= 2^28, 1 <= T <= 2^30; all pointers 16-byte aligned.
+ *   1 <= d <= 2^26, 1 <= T <= 2^30, T d <= 2^34; all pointers 16-byte aligned.
  *   workspace : at least ttt_gated_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *           where that is 0).  Calls that may overlap in time need one each, graph
  *           replays included; its contents need not be kept between calls. */
@@ -455,7 +455,7 @@ int ttt_gated_bwd(const void* G, const void* Z, const float* h0, const void* dZ,
  *   R        : [rows, D] in io_dtype (output: r, the residual of what follows; may alias
  *              residual or X, but not Y), or NULL to leave it out.
  *   eps      : > 0, finite and no denormal number.  rows >= 0 (0 does nothing),
- *              1 <= D <= 2^28; X, residual, Y and R 16-byte aligned, weight 4-byte. */
+ *              1 <= D <= 2^26; X, residual, Y and R 16-byte aligned, weight 4-byte. */
 int ttt_rmsnorm_fwd(const void* X, const void* residual, const float* weight, float eps,
                     void* Y, void* R, long long rows, int D, int io_dtype, void* stream);
 

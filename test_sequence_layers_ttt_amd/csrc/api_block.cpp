@@ -16,17 +16,16 @@ using namespace ttt;
 
 namespace {
 
-constexpr int kMostFeatures = 1 << 28;
+constexpr int kMostFeatures = 1 << 26;
 
 bool gated_dims_ok(int B, int H, int T, int d, int io_dtype)
 {
     if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || !dtype_ok(io_dtype)) return false;
-    // token and feature counts with room in an int, every element index inside 2^60, rows and
-    // grids inside 2^31
-    if (T > 1 << 30 || d > kMostFeatures) return false;
+    // token and feature counts with room in an int, rows inside 2^31, one row inside a grid, every
+    // element index inside 2^60
+    if (T > 1 << 30 || d > kMostFeatures || (long long)T * d > 1ll << 34) return false;
     const long double rows = (long double)B * H;
-    return rows * T * d < 1.0e18L && rows < 2.0e9L &&
-           gated_fits(B * H, T, d, io_dtype == TTT_DTYPE_BF16);
+    return rows * T * d < 1.0e18L && rows < 2.0e9L;
 }
 
 bool rms_dims_ok(long long rows, int D)

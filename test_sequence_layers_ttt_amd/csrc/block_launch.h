@@ -7,7 +7,7 @@
 
 namespace ttt {
 
-// Gated linear recurrence over BH rows of [T, d]; any d.
+// Gated linear recurrence over BH rows of [T, d], T d <= 2^34; any d.
 struct GatedArgs {
     const void* X;
     const void* G;
@@ -37,7 +37,6 @@ struct GatedBwdArgs {
 };
 hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s);
 size_t gated_workspace(int BH, int T, int d, bool bf16);
-bool gated_fits(int BH, int T, int d, bool bf16);
 
 // Root-mean-square norm over rows of D features.
 struct RmsArgs {

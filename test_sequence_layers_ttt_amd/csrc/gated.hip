@@ -654,7 +654,19 @@ Layout bwd_layout(int BH, int T, int d, bool bf16)
     return one_tile_of_512(y, z, bf16, T, kRunBwd) && (long long)BH * z.blocks <= 256 ? z : y;
 }
 
-// Sets up the chain of a call: the number of workgroups (inside 2^31, see gated_fits).
+// Rows of one launch: a grid has room for fewer than 2^32 threads (a row of T d <= 2^34 has fewer
+// than 2^30).  The rows beyond take further launches, one after the other in the same workspace.
+constexpr long long kMostThreads = 0x7fffffff;
+
+int rows_of(const Layout& y, int BH, long long tiles)
+{
+    return (int)std::min<long long>(BH, kMostThreads / (y.threads * (long long)y.blocks * tiles));
+}
+
+// p + n, or nullptr
+template <typename T> T* shifted(T* p, size_t n) { return p ? p + n : nullptr; }
+
+// Sets up the chain of a launch: the number of workgroups.
 unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int& tiles, int& seqs,
                  hipStream_t s)
 {
@@ -675,25 +687,36 @@ unsigned prepare(const Layout& y, int BH, int T, int L, void* ws, Chain& c, int&
 template <typename TIO, int V, int NT, bool LINES>
 hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
 {
-    Chain c;
-    int tiles, seqs;
-    const unsigned grid = prepare(y, a.BH, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
+    const int per = rows_of(y, a.BH, tiles_of(y, a.T, kRunFwd));
     const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
-    hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
-                       (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d, tiles,
-                       seqs, y, c, own);
+    for (long long row = 0; row < a.BH; row += per) {
+        const size_t h = (size_t)row * a.d, at = h * a.T;
+        const int rows = (int)std::min<long long>(per, a.BH - row);
+        Chain c;
+        int tiles, seqs;
+        const unsigned grid = prepare(y, rows, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
+        hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
+                           (const TIO*)a.X + at, (const TIO*)a.G + at, shifted(a.h0, h),
+                           (TIO*)a.Z + at, shifted(a.h_out, h), a.T, a.d, tiles, seqs, y, c, own);
+    }
     return hipGetLastError();
 }
 
 template <typename TIO, int V, int NT, bool LINES>
 hipError_t bwd_nt(const GatedBwdArgs& a, const Layout& y, hipStream_t s)
 {
-    Chain c;
-    int tiles, seqs;
-    const unsigned grid = prepare(y, a.BH, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
-    hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
-                       (const TIO*)a.G, (const TIO*)a.Z, a.h0, (const TIO*)a.dZ, a.dh_T,
-                       (TIO*)a.dX, (TIO*)a.dG, a.dh0, a.T, a.d, tiles, seqs, y, c);
+    const int per = rows_of(y, a.BH, tiles_of(y, a.T, kRunBwd));
+    for (long long row = 0; row < a.BH; row += per) {
+        const size_t h = (size_t)row * a.d, at = h * a.T;
+        const int rows = (int)std::min<long long>(per, a.BH - row);
+        Chain c;
+        int tiles, seqs;
+        const unsigned grid = prepare(y, rows, a.T, kRunBwd, a.workspace, c, tiles, seqs, s);
+        hipLaunchKernelGGL((gated_bwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
+                           (const TIO*)a.G + at, (const TIO*)a.Z + at, shifted(a.h0, h),
+                           (const TIO*)a.dZ + at, shifted(a.dh_T, h), (TIO*)a.dX + at,
+                           (TIO*)a.dG + at, shifted(a.dh0, h), a.T, a.d, tiles, seqs, y, c);
+    }
     return hipGetLastError();
 }
 
@@ -723,11 +746,16 @@ template <typename TIO, int V>
 hipError_t step_v(const GatedArgs& a, hipStream_t s)
 {
     const int groups = (a.d + V - 1) / V;
-    const long long n = (long long)a.BH * groups, grid = (n + kThreads - 1) / kThreads;
+    const long long per = kMostThreads / groups;
     const bool own = a.h0 && a.h0 == a.h_out;
-    hipLaunchKernelGGL((gated_step_kernel<TIO, V>), dim3((unsigned)grid), dim3(kThreads), 0, s,
-                       (const TIO*)a.X, (const TIO*)a.G, a.h0, (TIO*)a.Z, a.h_out, a.T, a.d,
-                       groups, n, own);
+    for (long long row = 0; row < a.BH; row += per) {
+        const size_t h = (size_t)row * a.d, at = h * a.T;
+        const long long n = std::min<long long>(per, a.BH - row) * groups;
+        hipLaunchKernelGGL((gated_step_kernel<TIO, V>), dim3((unsigned)((n + kThreads - 1) / kThreads)),
+                           dim3(kThreads), 0, s, (const TIO*)a.X + at, (const TIO*)a.G + at,
+                           shifted(a.h0, h), (TIO*)a.Z + at, shifted(a.h_out, h), a.T, a.d, groups,
+                           n, own);
+    }
     return hipGetLastError();
 }
 
@@ -742,22 +770,14 @@ hipError_t step_v(const GatedArgs& a, hipStream_t s)
 
 }  // namespace
 
-// Whether every grid of the shape stays inside 2^31 workgroups.
-bool gated_fits(int BH, int T, int d, bool bf16)
-{
-    const Layout y = layout_of(d, bf16, 256);
-    const long double most = 0x7fffffff, rows = BH;
-    return rows * y.blocks * std::max(tiles_of(y, T, kRunFwd), tiles_of(y, T, kRunBwd)) <= most &&
-           rows * ((d + y.V - 1) / y.V) / kThreads + 1 <= most;
-}
-
 size_t gated_workspace(int BH, int T, int d, bool bf16)
 {
     size_t n = 0;
     auto add = [&](const Layout& y, int L) {
         const long long tiles = tiles_of(y, T, L);
         if (tiles > 1)
-            n = std::max(n, chain_bytes((long long)BH * y.blocks, tiles, y.width, nullptr, nullptr));
+            n = std::max(n, chain_bytes((long long)rows_of(y, BH, tiles) * y.blocks, tiles, y.width,
+                                        nullptr, nullptr));
     };
     add(fwd_layout(T, d, bf16), kRunFwd);
     add(bwd_layout(BH, T, d, bf16), kRunBwd);

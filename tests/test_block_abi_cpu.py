@@ -25,6 +25,7 @@ def gated(**kw):
     dict(h0=P[2] + 4), dict(h_out=P[4] + 8), dict(B=0), dict(H=-1), dict(T=0), dict(d=0),
     dict(io=2), dict(io=-1), dict(B=1 << 20, H=1 << 20), dict(T=1 << 30, d=1 << 30),
     dict(T=(1 << 30) + 1), dict(T=0x7fffffff), dict(d=(1 << 28) + 1), dict(d=0x7fffffff),
+    dict(d=(1 << 26) + 1), dict(T=1 << 20, d=(1 << 14) + 1),
     dict(Z=P[0]), dict(Z=P[1] + 16), dict(Z=P[2]), dict(h_out=P[0]), dict(h_out=P[3]),
     dict(h_out=P[2] + 16),                              # a shifted overlap of the states
 ])
@@ -76,7 +77,7 @@ def test_gated_step_refuses(kw):
 @pytest.mark.parametrize("kw", [
     dict(X=None), dict(Y=None), dict(X=P[0] + 8), dict(res=P[1] + 4), dict(w=P[2] + 2),
     dict(Y=P[3] + 8), dict(R=P[5] + 4), dict(rows=-1), dict(D=0), dict(D=-4), dict(io=2),
-    dict(D=(1 << 28) + 1), dict(D=0x7fffffff), dict(eps=0.0), dict(eps=1e-40), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
+    dict(D=(1 << 26) + 1), dict(D=(1 << 28) + 1), dict(D=0x7fffffff), dict(eps=0.0), dict(eps=1e-40), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rows=1 << 62),
     dict(Y=P[1]), dict(Y=P[0] + 16), dict(R=P[3]), dict(R=P[0] + 32), dict(R=P[1] + 16), dict(w=P[3]),
     dict(w=P[5]),
 ])

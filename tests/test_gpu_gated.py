@@ -361,3 +361,36 @@ def test_offsets_past_32_bits(dev):
     assert ref.within(np64(dX[:, :, -tail:]), wx, bx, "bf16")[0]
     assert ref.within(np64(dG[:, :, -tail:]), wg, bg, "bf16")[0]
     assert (dX[:, :, :-tail] == 0).all() and (dh0 == 0).all()
+
+
+@pytest.mark.parametrize("op,BH,T,d", [("fwd", (1 << 22) + 3, 2049, 1), ("fwd", (1 << 23) + 5, 65, 1),
+                                       ("step", (1 << 30) + 5, 1, 3), ("bwd", (1 << 23) + 5, 1, 1),
+                                       ("bwd", (1 << 22) + 3, 2049, 1)])
+def test_more_rows_than_a_grid_holds(dev, op, BH, T, d):
+    """Rows that one launch has no room for: those at both ends and on both sides of every place where
+    a launch may end have the bits that a call of their own gives them."""
+    import torch
+    say(op, BH, T, d)
+    edge = BH - 20
+    picked = torch.tensor([0, 1, *range(edge, BH)], device=dev)
+    gen = torch.Generator(device="cpu").manual_seed(BH + T)
+
+    def filled(shape, dtype, of):
+        full = torch.full(shape, -0.5, dtype=dtype, device=dev)
+        few = of(torch.randn(1, len(picked), *shape[2:], generator=gen)).to(dtype).to(dev)
+        full[:, picked] = few
+        return full, few
+
+    bf = torch.bfloat16
+    X, x = filled((1, BH, T, d), bf, lambda v: v)
+    G, g = filled((1, BH, T, d), bf, lambda v: -v.abs())
+    h, hs = filled((1, BH, d), torch.float32, lambda v: v)
+    if op == "step":
+        got, want = [ttt.gated_step(X, G, h), h], [ttt.gated_step(x, g, hs), hs]
+    elif op == "fwd":
+        got, want = ttt.gated_fwd(X, G, h), ttt.gated_fwd(x, g, hs)
+    else:
+        got, want = ttt.gated_bwd(G, X, X, h, h), ttt.gated_bwd(g, x, x, hs, hs)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[:, picked], b)
