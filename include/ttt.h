@@ -460,7 +460,8 @@ int ttt_rmsnorm_fwd(const void* X, const void* residual, const float* weight, fl
                     void* Y, void* R, long long rows, int D, int io_dtype, void* stream);
 
 /* The same with y in 8-bit floating point (OCP e4m3: largest value 448) and one scale
- * per row: scale = max|y| / 448, Y8 = y / scale rounded to nearest even.  A row of zeros
+ * per row: scale = max|y| / 448, Y8 = y / (max|y| / 448) rounded to nearest even, as the
+ * formula's value in fp64 is (a few 2^-52 off), whatever scale is rounded to.  A row of zeros
  * has scale 0 and Y8 0; a row whose r has a NaN or an infinity in it has a NaN scale, and
  * its Y8 is NaN throughout.
  *   Y8 : [rows, D] bytes (16-byte aligned);  scale : [rows] fp32. */

@@ -3,7 +3,7 @@
 //
 // A row of D features is held in registers by TPR threads, K vectors of 16 bytes each, so
 // every input is read once and every output written once: HBM bounds it (32768 x 2048
-// bf16 backward 99 us for 537 MB, 5.4 TB/s; 16384 x 2048 to e4m3 43 us for 235 MB; a
+// bf16 backward 99 us for 537 MB, 5.4 TB/s; 16384 x 2048 to e4m3 42 us for 235 MB; a
 // device copy reaches 5.2 TB/s).  Rows of up to 128 vectors stay within one wave (sums by
 // lane exchanges, no LDS, no barrier); longer ones take a workgroup: 256 threads with one
 // vector each beat one wave with four (16384 x 2048 to e4m3: 45 and 92 us), which had too
@@ -29,10 +29,16 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 
+typedef unsigned long long word64;
 typedef uint32_t quad __attribute__((ext_vector_type(4)));
 typedef quad quad_any __attribute__((aligned(2)));
 
 template <typename TIO> constexpr int kVec = 16 / (int)sizeof(TIO);
+// -0, which any value plus is that value
+template <typename TIO>
+constexpr quad kNoResidual = sizeof(TIO) == 4
+    ? quad{0x80000000u, 0x80000000u, 0x80000000u, 0x80000000u}
+    : quad{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
 
 // 16 bytes of the I/O type at any element-aligned address; with the streaming policy where rows are
 // whole cache lines (LINES: 8192 x 4096 fp32 backward 96 us, against 106 without), without it where a
@@ -101,15 +107,32 @@ __device__ __forceinline__ unsigned moved(unsigned x)
     return (unsigned)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, false);
 }
 
+// the same of 64-bit words
+template <int O>
+__device__ __forceinline__ void halves(word64 x, word64& lo, word64& hi)
+{
+    unsigned l[2], h[2];
+    halves<O>((unsigned)x, l[0], h[0]);
+    halves<O>((unsigned)(x >> 32), l[1], h[1]);
+    lo = (word64)l[1] << 32 | l[0];
+    hi = (word64)h[1] << 32 | h[0];
+}
+
+template <int CTRL>
+__device__ __forceinline__ word64 moved(word64 x)
+{
+    return (word64)moved<CTRL>((unsigned)(x >> 32)) << 32 | moved<CTRL>((unsigned)x);
+}
+
 // reduction over W <= 64 neighbouring lanes, the same bits in each: `f` is symmetric
-template <int W, typename F>
-__device__ __forceinline__ unsigned over_lanes(unsigned x, F&& f)
+template <int W, typename T, typename F>
+__device__ __forceinline__ T over_lanes(T x, F&& f)
 {
     if constexpr (W > 1) x = f(x, moved<kDppQuadXor1>(x));
     if constexpr (W > 2) x = f(x, moved<kDppQuadXor2>(x));
     if constexpr (W > 4) x = f(x, moved<kDppRowHalfMirror>(x));
     if constexpr (W > 8) x = f(x, moved<kDppRowMirror>(x));
-    unsigned lo, hi;
+    T lo, hi;
     if constexpr (W > 16) {
         halves<16>(x, lo, hi);
         x = f(lo, hi);
@@ -127,16 +150,17 @@ __device__ __forceinline__ unsigned add_bits(unsigned a, unsigned b)
 }
 
 // magnitudes compared as their bits: a NaN is above everything
-__device__ __forceinline__ unsigned max_bits(unsigned a, unsigned b) { return a > b ? a : b; }
+template <typename T>
+__device__ __forceinline__ T max_bits(T a, T b) { return a > b ? a : b; }
 
-// N sums (or maxima of magnitudes) over the TPR threads of a row, the same bits in each; `lds`
-// holds N words per wave where a row takes several
-template <int TPR, int N, bool MAX>
-__device__ __forceinline__ void over_row(unsigned (&x)[N], unsigned* lds)
+// N values of the TPR threads of a row reduced by `f`, the same bits in each; `lds` holds N of
+// them per wave where a row takes several
+template <int TPR, int N, typename T, typename F>
+__device__ __forceinline__ void over_row(T (&x)[N], T* lds, F&& f)
 {
     constexpr int W = TPR < 64 ? TPR : 64, WAVES = TPR / 64;
 #pragma unroll
-    for (int n = 0; n < N; ++n) x[n] = over_lanes<W>(x[n], MAX ? max_bits : add_bits);
+    for (int n = 0; n < N; ++n) x[n] = over_lanes<W>(x[n], f);
     if constexpr (TPR > 64) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) {
@@ -148,29 +172,50 @@ __device__ __forceinline__ void over_row(unsigned (&x)[N], unsigned* lds)
         for (int n = 0; n < N; ++n) {
             x[n] = lds[n * WAVES];
 #pragma unroll
-            for (int i = 1; i < WAVES; ++i)
-                x[n] = (MAX ? max_bits : add_bits)(x[n], lds[n * WAVES + i]);
+            for (int i = 1; i < WAVES; ++i) x[n] = f(x[n], lds[n * WAVES + i]);
         }
     }
 }
 
 template <int TPR>
-__device__ __forceinline__ float row_sum(float x, unsigned* lds)
+__device__ __forceinline__ float row_sum(float x, void* lds)
 {
     unsigned b[1] = {__float_as_uint(x)};
-    over_row<TPR, 1, false>(b, lds);
+    over_row<TPR>(b, (unsigned*)lds, add_bits);
     return __uint_as_float(b[0]);
 }
 
+// a row's sum and its largest magnitude at once
 template <int TPR>
-__device__ __forceinline__ float row_max(unsigned x, unsigned* lds)
+__device__ __forceinline__ void sum_and_max(unsigned (&x)[2], unsigned* lds)
 {
-    unsigned b[1] = {x};
-    over_row<TPR, 1, true>(b, lds);
-    return __uint_as_float(b[0]);
+    constexpr int W = TPR < 64 ? TPR : 64, WAVES = TPR / 64;
+    x[0] = over_lanes<W>(x[0], add_bits);
+    x[1] = over_lanes<W>(x[1], max_bits<unsigned>);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            lds[2 * (threadIdx.x >> 6)] = x[0];
+            lds[2 * (threadIdx.x >> 6) + 1] = x[1];
+        }
+        __syncthreads();
+        x[0] = lds[0];
+        x[1] = lds[1];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) {
+            x[0] = add_bits(x[0], lds[2 * i]);
+            x[1] = max_bits(x[1], lds[2 * i + 1]);
+        }
+    }
 }
 
-__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// the row's largest: `x` has the bits of a magnitude
+template <int TPR, typename T>
+__device__ __forceinline__ T row_max(T x, void* lds)
+{
+    T b[1] = {x};
+    over_row<TPR>(b, (T*)lds, [](T a, T c) { return max_bits(a, c); });
+    return b[0];
+}
 
 // four values as e4m3, rounded to nearest even (up to 464 in magnitude that is 448; NaN stays)
 __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
@@ -179,51 +224,89 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
-// A row's e4m3 values.  y / scale is t / (max|t| / 448) with t = r * weight * (the rate's power of
-// two, which is exact): the rest of the rate cancels, and with it its error; the quotient's remainder
-// is put right, so that what e4m3 rounds is off by little more than t's own rounding (at most 448 and
-// a rounding of that).  Where the divisor or its reciprocal would leave fp32's range both are scaled by
-// a power of two first; a scale of 0 (a row of zeros) gives 0; a NaN or an infinity in the row makes
-// it NaN throughout.
+// A row's e4m3 values: y / (max|y| / 448) is t / (max|t| / 448) with t = r * weight, as the rate
+// cancels.  The fp32 quotient is off by up to 7 roundings (two of t, two of the largest t, and one each
+// of 448 / top, of the factors below and of the product): where t times 448 / top (1 + 2^-21) and t times
+// 448 / top (1 - 2^-21) give the same e4m3 values, it is theirs.  Where they do not (one value in 10^5),
+// and in rows whose fp32 values leave the range in which those are relative errors, the quotient is
+// formed in fp64.  (fp64 throughout: 16384 x 2048 bf16 59 us, against 47.)
 struct Row8 {
-    float scale, top, inv, by;
-    bool rare;
-    // the power of two in a rate (1 for a rate of 0, as of a row whose squares leave fp32's range)
-    __device__ __forceinline__ static float power(float rate)
+    float hi, lo;        // 0 where the scale is 0
+    bool plain;          // the row's fp32 values are in range
+    __device__ __forceinline__ Row8(float top, float rate)
     {
-        return rate == 0.f ? 1.f : __uint_as_float(__float_as_uint(rate) & 0x7f800000u);
+        plain = top >= 0x1p-100f && top <= 0x1p100f && rate > 0.f;
+        const float inv = scale_of(top, rate) == 0.f ? 0.f : kE4m3Max / top;
+        hi = inv * (1.f + 0x1p-21f);
+        lo = inv * (1.f - 0x1p-21f);
     }
-    __device__ __forceinline__ Row8(float most, float rate)
+    // whether a thread whose largest fp32 |t| is m may have the row's largest in fp64
+    __device__ __forceinline__ bool may_have(float m, float top) const
     {
-        scale = most * (rate / power(rate)) / kE4m3Max;
-        by = scale == 0.f ? 0.f : most < 1e-30f ? 0x1p80f : most > 1e30f ? 0x1p-80f : 1.f;
-        rare = by != 1.f;
-        top = scale == 0.f ? 1.f : most * by / kE4m3Max;
-        inv = 1.f / top;
+        return !plain || m >= top * (1.f - 0x1p-21f);
     }
-    template <int V>
-    __device__ __forceinline__ void apply(float (&t)[V]) const
+    // max|y| / 448
+    __device__ __forceinline__ static float scale_of(double most, float rate)
     {
-        if (rare)
-#pragma unroll
-            for (int i = 0; i < V; ++i) t[i] *= by;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float q = t[i] * inv;
-            t[i] = fmaf(fmaf(-q, top, t[i]), inv, q);
-        }
+        return (float)(most * rate * (1.0 / kE4m3Max));
+    }
+    // four values, and whether they are certain
+    __device__ __forceinline__ unsigned four(const float* t, bool& sure) const
+    {
+        const unsigned a = pack_e4m3(t[0] * hi, t[1] * hi, t[2] * hi, t[3] * hi);
+        sure = sure && a == pack_e4m3(t[0] * lo, t[1] * lo, t[2] * lo, t[3] * lo);
+        return a;
     }
 };
+
+// The same in fp64, the quotient's remainder put right, so that what is rounded is the formula's value
+// to 2^-52 and a tie is a tie.  A scale of 0 (a row of zeros) gives 0; a NaN or an infinity in the row
+// makes it NaN throughout.
+struct Row64 {
+    double most, inv;
+    __device__ __forceinline__ Row64(double m, float scale)
+    {
+        most = m;
+        inv = scale == 0.f ? 0.0 : 1.0 / m;
+    }
+    // the quotient, in fp32 to the side of every e4m3 value and tie that it is on: 20 bits, the last
+    // one set where what is cut off is not 0
+    __device__ __forceinline__ float operator()(double t) const
+    {
+        const double n = t * (double)kE4m3Max, q = n * inv;
+        const word64 b = (word64)__double_as_longlong(fma(fma(-q, most, n), inv, q));
+        return (float)__longlong_as_double((long long)((b >> 32 | (unsigned)((unsigned)b != 0)) << 32));
+    }
+};
+
+// the larger of two magnitudes as fp64 bits, where a NaN is above everything
+__device__ __forceinline__ word64 larger(word64 a, double t)
+{
+    return max_bits(a, (word64)__double_as_longlong(fabs(t)));
+}
+
+// the squares of a vector's elements that the one before does not have
+template <int V>
+__device__ __forceinline__ void add_squares(const float (&r)[V], int dup, float& ss)
+{
+    if (dup == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = fmaf(r[i], r[i], ss);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = i >= dup ? fmaf(r[i], r[i], ss) : ss;
+    }
+}
 
 // threads of a workgroup
 template <int TPR> constexpr int kBlock = TPR < 256 ? 256 : TPR;
 // rows a thread has under way at once
 template <int TPR, int K> constexpr int kRows = TPR <= 64 && K == 1 ? 2 : 1;
 
-template <typename TIO, int TPR, int K, bool Q8, bool LINES>
+template <typename TIO, int TPR, int K, bool LINES>
 __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
-    const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, void* Y,
-    float* scale, TIO* R, long long rows, int D)
+    const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, TIO* Y, TIO* R,
+    long long rows, int D)
 {
     constexpr int V = kVec<TIO>, U = kRows<TPR, K>, GROUPS = kBlock<TPR> / TPR;
     __shared__ unsigned lds[TPR > 64 ? TPR / 64 : 1];
@@ -266,90 +349,221 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_fwd_kernel(
 #pragma unroll
                     for (int i = 0; i < V; ++i) r[k][i] += a[i];
                 }
-                if (dup[k] == 0) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) ss = fmaf(r[k][i], r[k][i], ss);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) ss = i >= dup[k] ? fmaf(r[k][i], r[k][i], ss) : ss;
-                }
+                add_squares<V>(r[k], dup[k], ss);
             }
             const float rate = rsqrtf(row_sum<TPR>(ss, lds) * inv_d + eps);
-            const float by = Q8 ? Row8::power(rate) : rate;
-            const bool live = r0 + u < rows;
-            unsigned m = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const bool mine = live && dup[k] < V;
+                if (r0 + u >= rows || dup[k] == V) continue;
                 const size_t at = (size_t)(r0 + u) * D + col[k];
-                if (R && mine) store16<LINES>(R + at, narrow<TIO>(r[k]));
+                if (R) store16<LINES>(R + at, narrow<TIO>(r[k]));
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    r[k][i] *= by * w[k][i];
-                    if constexpr (Q8) m = max_bits(m, magnitude(r[k][i]));
-                }
-                if constexpr (!Q8)
-                    if (mine) store16<LINES>((TIO*)Y + at, narrow<TIO>(r[k]));
-            }
-            if constexpr (Q8) {
-                const Row8 row(row_max<TPR>(m, lds), rate);
-                if (live && lane == 0) scale[r0 + u] = row.scale;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    if (!live || dup[k] == V) continue;
-                    row.apply(r[k]);
-                    unsigned q[V / 4];
-#pragma unroll
-                    for (int i = 0; i < V / 4; ++i)
-                        q[i] = pack_e4m3(r[k][4 * i], r[k][4 * i + 1], r[k][4 * i + 2], r[k][4 * i + 3]);
-                    __builtin_memcpy((uint8_t*)Y + (size_t)(r0 + u) * D + col[k], q, V);
-                }
+                for (int i = 0; i < V; ++i) r[k][i] *= rate * w[k][i];
+                store16<LINES>(Y + at, narrow<TIO>(r[k]));
             }
         }
     }
 }
 
+// The same to e4m3.
+template <typename TIO, int TPR, int K, bool LINES>
+__global__ __launch_bounds__(kBlock<TPR>) void rms_q8_kernel(
+    const TIO* X, const TIO* residual, const float* __restrict__ weight, float eps, uint8_t* Y,
+    float* scale, TIO* R, long long rows, int D)
+{
+    constexpr int V = kVec<TIO>, U = kRows<TPR, K>, GROUPS = kBlock<TPR> / TPR;
+    __shared__ unsigned lds[TPR > 64 ? 2 * (TPR / 64) : 1];
+    __shared__ word64 lds64[TPR > 64 ? TPR / 64 : 1];
+    __shared__ bool doubt;             // of a row that takes several waves
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int vectors = (D + V - 1) / V;
+    int col[K], dup[K];
+    float w[K][V], from = 0.f;         // from: inf where a weight is not finite, which fp64 has to see
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int v = lane + k * TPR;
+        col[k] = min(v * V, D - V);
+        dup[k] = v < vectors ? v * V - col[k] : V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            w[k][i] = weight && dup[k] < V ? weight[col[k] + i] : 1.f;
+            if (!isfinite(w[k][i])) from = __builtin_inff();
+        }
+    }
+    const float inv_d = 1.f / D;
+    for (long long r0 = ((long long)blockIdx.x * GROUPS + group) * U; r0 - group * U < rows;
+         r0 += (long long)gridDim.x * GROUPS * U) {
+        quad x[U][K], z[U][K];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                x[u][k] = quad{0, 0, 0, 0};
+                z[u][k] = kNoResidual<TIO>;
+                if (r0 + u < rows && dup[k] < V) {
+                    const size_t at = (size_t)(r0 + u) * D + col[k];
+                    x[u][k] = load16<LINES>(X + at);
+                    if (residual) z[u][k] = load16<LINES>(residual + at);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool live = r0 + u < rows;
+            // r of vector k, widened again from its words each time: fp64 may need the words, and there
+            // are no registers for both
+            auto values = [&](int k, float (&r)[V]) {
+                if constexpr (K > 1) asm volatile("" : "+v"(x[u][k]), "+v"(z[u][k]));
+                float a[V];
+                widen<TIO>(x[u][k], r);
+                widen<TIO>(z[u][k], a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) r[i] += a[i];
+            };
+            // t of vector k in fp64
+            auto exact = [&](int k, double (&t)[V]) {
+                asm volatile("" : "+v"(x[u][k]), "+v"(z[u][k]));
+                float b[V], a[V];
+                widen<TIO>(x[u][k], b);
+                widen<TIO>(z[u][k], a);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float by = w[k][i];
+                    asm volatile("" : "+v"(by));
+                    t[i] = ((double)b[i] + a[i]) * by;
+                }
+            };
+            auto exact_most = [&]() {
+                word64 most = 0;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    double t[V];
+                    exact(k, t);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) most = larger(most, t[i]);
+                }
+                return most;
+            };
+            float ss = 0.f, m = from;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float r[V];
+                values(k, r);
+                add_squares<V>(r, dup[k], ss);
+#pragma unroll
+                for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(r[i] * w[k][i]));
+            }
+            if constexpr (TPR > 64) {
+                __syncthreads();       // the row before has read what is in LDS
+                if (threadIdx.x == 0) doubt = false;
+            }
+            unsigned both[2] = {__float_as_uint(ss), __float_as_uint(m)};
+            sum_and_max<TPR>(both, lds);
+            const float rate = rsqrtf(__uint_as_float(both[0]) * inv_d + eps), top = __uint_as_float(both[1]);
+            const Row8 row(top, rate);
+            bool sure = row.plain;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float r[V];
+                values(k, r);
+                if (R && live && dup[k] < V)
+                    store16<LINES>(R + (size_t)(r0 + u) * D + col[k], narrow<TIO>(r));
+#pragma unroll
+                for (int i = 0; i < V; ++i) r[i] *= w[k][i];
+                unsigned q[V / 4];
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) q[i] = row.four(r + 4 * i, sure);
+                if (live && dup[k] < V) __builtin_memcpy(Y + (size_t)(r0 + u) * D + col[k], q, V);
+            }
+            float of_row = Row8::scale_of(top, rate);
+            bool again;
+            if constexpr (TPR > 64) {
+                if (!sure) doubt = true;
+                __syncthreads();
+                again = doubt;
+            } else {
+                again = __any(!sure);
+            }
+            if (again) {
+                word64 mine = 0;
+                if (row.may_have(m, top)) mine = exact_most();
+                const double most = __longlong_as_double((long long)row_max<TPR>(mine, lds64));
+                if (!row.plain) of_row = Row8::scale_of(most, rate);
+                const Row64 row64(most, of_row);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (sure) break;
+                    double t[V];
+                    exact(k, t);
+                    unsigned q[V / 4];
+#pragma unroll
+                    for (int i = 0; i < V / 4; ++i)
+                        q[i] = pack_e4m3(row64(t[4 * i]), row64(t[4 * i + 1]), row64(t[4 * i + 2]),
+                                         row64(t[4 * i + 3]));
+                    if (live && dup[k] < V) __builtin_memcpy(Y + (size_t)(r0 + u) * D + col[k], q, V);
+                }
+            }
+            if (live && lane == 0) scale[r0 + u] = of_row;
+        }
+    }
+}
+
 // Rows too long (or too short) for the registers' layout: a workgroup per row, the row read again
-// for every pass.
+// for every pass, 8 elements of a thread at a time.
 template <typename TIO, bool Q8>
 __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const TIO* residual,
                                                            const float* __restrict__ weight,
                                                            float eps, void* Y, float* scale, TIO* R,
                                                            long long rows, int D)
 {
-    __shared__ unsigned lds[4];
+    constexpr int N = 8;
+    __shared__ word64 lds[4];
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
         const size_t base = (size_t)row * D;
-        auto r_at = [&](int i) {
-            const float x = io<TIO>::load(X, base + i);
-            return residual ? x + io<TIO>::load(residual, base + i) : x;
+        // f(first element, x, residual, weight) for this thread's elements: first, first + 256, ...;
+        // zeros past the row's end
+        auto eights = [&](auto&& f) {
+            for (int i = threadIdx.x; i < D; i += 256 * N) {
+                float x[N], a[N], w[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const bool in = i + 256 * n < D;
+                    const size_t at = base + i + 256 * n;
+                    x[n] = in ? io<TIO>::load(X, at) : 0.f;
+                    a[n] = in && residual ? io<TIO>::load(residual, at) : -0.f;
+                    w[n] = in && weight ? weight[i + 256 * n] : 1.f;
+                }
+                f(i, x, a, w);
+            }
         };
         float ss = 0.f;
-        for (int i = threadIdx.x; i < D; i += 256) {
-            const float r = r_at(i);
-            ss = fmaf(r, r, ss);
-        }
+        word64 largest = 0;
+        eights([&](int, const float (&x)[N], const float (&a)[N], const float (&w)[N]) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const float r = x[n] + a[n];
+                ss = fmaf(r, r, ss);
+                if constexpr (Q8) largest = larger(largest, ((double)x[n] + a[n]) * w[n]);
+            }
+        });
         const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
-        const float by = Q8 ? Row8::power(rate) : rate;
-        float most = 0.f;
-        if constexpr (Q8) {
-            unsigned m = 0;
-            for (int i = threadIdx.x; i < D; i += 256)
-                m = max_bits(m, magnitude(r_at(i) * (by * (weight ? weight[i] : 1.f))));
-            most = row_max<256>(m, lds);
-        }
-        const Row8 row8(most, rate);
-        if (Q8 && threadIdx.x == 0) scale[row] = row8.scale;
-        for (int i = threadIdx.x; i < D; i += 256) {
-            const float r = r_at(i), y = r * (by * (weight ? weight[i] : 1.f));
-            if constexpr (Q8) {
-                float t[1] = {y};
-                row8.apply(t);
-                ((uint8_t*)Y)[base + i] = (uint8_t)pack_e4m3(t[0], 0.f, 0.f, 0.f);
-            } else
-                io<TIO>::store((TIO*)Y, base + i, y);
-            if (R) io<TIO>::store(R, base + i, r);
-        }
+        double most = 0.0;
+        if constexpr (Q8) most = __longlong_as_double((long long)row_max<256>(largest, lds));
+        const float of_row = Row8::scale_of(most, rate);
+        const Row64 row64(most, of_row);
+        if (Q8 && threadIdx.x == 0) scale[row] = of_row;
+        eights([&](int i, const float (&x)[N], const float (&a)[N], const float (&w)[N]) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (i + 256 * n >= D) break;
+                const size_t at = base + i + 256 * n;
+                const float r = x[n] + a[n];
+                if constexpr (Q8)
+                    ((uint8_t*)Y)[at] = (uint8_t)pack_e4m3(row64(((double)x[n] + a[n]) * w[n]), 0.f, 0.f, 0.f);
+                else
+                    io<TIO>::store((TIO*)Y, at, r * (rate * w[n]));
+                if (R) io<TIO>::store(R, at, r);
+            }
+        });
     }
 }
 
@@ -411,7 +625,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
             }
         }
         unsigned both[2] = {__float_as_uint(ss), __float_as_uint(su)};
-        over_row<TPR, 2, false>(both, lds);
+        over_row<TPR>(both, lds, add_bits);
         const float rate = rsqrtf(__uint_as_float(both[0]) * inv_d + eps);
         const float m = __uint_as_float(both[1]) * rate * inv_d;   // mean(u n)
 #pragma unroll
@@ -557,10 +771,18 @@ void fwd_launch(const RmsArgs& a, hipStream_t s)
 {
     constexpr int PER = kBlock<TPR> / TPR * kRows<TPR, K>;
     const dim3 grid((unsigned)std::min(kMostBlocks<TPR>, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
-    auto kernel = a.scale ? rms_fwd_kernel<TIO, TPR, K, true, LINES>
-                          : rms_fwd_kernel<TIO, TPR, K, false, LINES>;
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, (const TIO*)a.X, (const TIO*)a.residual, a.weight,
-                       a.eps, a.Y, a.scale, (TIO*)a.R, a.rows, a.D);
+    hipLaunchKernelGGL((rms_fwd_kernel<TIO, TPR, K, LINES>), grid, block, 0, s, (const TIO*)a.X,
+                       (const TIO*)a.residual, a.weight, a.eps, (TIO*)a.Y, (TIO*)a.R, a.rows, a.D);
+}
+
+template <typename TIO, int TPR, int K, bool LINES>
+void q8_launch(const RmsArgs& a, hipStream_t s)
+{
+    constexpr int PER = kBlock<TPR> / TPR * kRows<TPR, K>;
+    const dim3 grid((unsigned)std::min(kMostBlocks<TPR>, (a.rows + PER - 1) / PER)), block(kBlock<TPR>);
+    hipLaunchKernelGGL((rms_q8_kernel<TIO, TPR, K, LINES>), grid, block, 0, s, (const TIO*)a.X,
+                       (const TIO*)a.residual, a.weight, a.eps, (uint8_t*)a.Y, a.scale, (TIO*)a.R, a.rows,
+                       a.D);
 }
 
 template <typename TIO, int TPR, int K, bool LINES>
@@ -581,7 +803,30 @@ void bwd_launch(const RmsBwdArgs& a, int planes, hipStream_t s)
 template <typename TIO>
 hipError_t fwd_typed(const RmsArgs& a, hipStream_t s)
 {
-    const Shape shape = shape_of(a.D, kVec<TIO>);
+    Shape shape = shape_of(a.D, kVec<TIO>);
+    // To e4m3, four bf16 vectors and what fp64 may need of them fill the registers: two, and twice as
+    // many threads (4096 x 8192 bf16 49 us, against 53; fp32 vectors have half as many values, and
+    // take 81 us that way, against 75).
+    constexpr int W = sizeof(TIO) == 4 ? 4 : 2;
+    if (a.scale && shape.k == 4 && shape.tpr < 1024) shape = {shape.tpr * 4 / W, W};
+    if (shape.tpr && a.scale) {
+        switch (shape.tpr * 8 + shape.k) {
+            RMS_SHAPE(q8_launch, 2, 1, a, s)
+            RMS_SHAPE(q8_launch, 4, 1, a, s)
+            RMS_SHAPE(q8_launch, 8, 1, a, s)
+            RMS_SHAPE(q8_launch, 16, 1, a, s)
+            RMS_SHAPE(q8_launch, 32, 1, a, s)
+            RMS_SHAPE(q8_launch, 64, 1, a, s)
+            RMS_SHAPE(q8_launch, 64, 2, a, s)
+            RMS_SHAPE(q8_launch, 256, 1, a, s)
+            RMS_SHAPE(q8_launch, 256, 2, a, s)
+            RMS_SHAPE(q8_launch, 1024 / W, W, a, s)
+            RMS_SHAPE(q8_launch, 2048 / W, W, a, s)
+            RMS_SHAPE(q8_launch, 1024, 4, a, s)
+        default: return hipErrorInvalidValue;
+        }
+        return hipGetLastError();
+    }
     if (shape.tpr) {
         switch (shape.tpr * 8 + shape.k) {
             RMS_SHAPE(fwd_launch, 2, 1, a, s)
