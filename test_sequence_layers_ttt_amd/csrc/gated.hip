@@ -301,6 +301,17 @@ __device__ __forceinline__ float state_before(const unsigned long long* word, in
     return __builtin_nanf("");
 }
 
+// Waits until group 0 has its state, which it has once all of its tiles have published: whether it
+// came to that.
+__device__ __forceinline__ bool first_group_done(const unsigned long long* word)
+{
+    for (int poll = 0; poll < kMostPolls; ++poll) {
+        if (__hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != kNothing) return true;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return false;
+}
+
 struct Tile {
     int seq, j;        // sequence (row, channel block) and place of the tile in it
     int row;           // of the input
@@ -375,10 +386,11 @@ __device__ __forceinline__ void lds_get(const float* p, float (&v)[V])
 }
 
 // The start state of each thread's run, from its pairs (S, B) and the states that enter the
-// sequence (`first` of the row's channels, or nullptr for zero).
+// sequence (`first` of the row's channels, or nullptr for zero).  in_place: the row's last tile writes
+// where `first` is read; on return every tile that reads it has done so.
 template <int V, int NT>
 __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int d, int tiles,
-                                             const Chain& chain, const float* first,
+                                             const Chain& chain, const float* first, bool in_place,
                                              const float (&S)[V], const float (&B)[V],
                                              float (&start)[V])
 {
@@ -417,8 +429,8 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
     __syncthreads();
     if (part == 0) {
-        // the tile's pair, then the state before it, then every part's start.  The row's last tile
-        // may write where `first` is read, once every tile has published: so the read is done by then.
+        // the tile's pair, then the state before it, then every part's start.  A tile has read `first`
+        // before it publishes.
         asm volatile("s_waitcnt vmcnt(0)" : "+v"(h) : : "memory");
         if (tiles > 1) {
             float s = 0.f, b = 0.f;
@@ -442,6 +454,10 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
                 h = state_before(group, g, w);
             }
             h = run(before_s, before_b, h);
+            // The tiles of group 0 read `first`.  A last tile in group 0 has seen their pairs; one
+            // further on may have taken its state from a group with a reset in it, which waits for no
+            // tile of group 0.
+            if (in_place && !more && g > 0 && !first_group_done(group)) h = __builtin_nanf("");
         }
         for (int p = 0; p < y.parts; ++p) {
             const float ts = pS[p * w + c], tb = pB[p * w + c];
@@ -460,12 +476,12 @@ __device__ __forceinline__ void start_states(const Layout& y, const Tile& t, int
     }
 }
 
-// own: the states are updated in place, so a channel is written by one group alone (the
-// other group's copy may have started from what was written).
+// in_place: h_out is h0.  Where a row has several blocks a channel is then written by one group of
+// threads alone (the other group's copy may have started from what was written).
 template <typename TIO, int V, int NT, bool LINES>
 __global__ __launch_bounds__(NT) void gated_fwd_kernel(
     const TIO* __restrict__ X, const TIO* __restrict__ G, const float* h0, TIO* __restrict__ Z,
-    float* h_out, int T, int d, int tiles, int seqs, Layout y, Chain chain, bool own)
+    float* h_out, int T, int d, int tiles, int seqs, Layout y, Chain chain, bool in_place)
 {
     constexpr int L = kRunFwd;
     __shared__ int ticket;
@@ -496,8 +512,8 @@ __global__ __launch_bounds__(NT) void gated_fwd_kernel(
             B[i] = token(g2, x[l].at(i), B[i]);
             S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
-    start_states<V, NT>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, S, B, h);
-    const int skip = own ? t.skip : 0;
+    start_states<V, NT>(y, t, d, tiles, chain, h0 ? h0 + (size_t)t.row * d : nullptr, in_place, S, B, h);
+    const int skip = in_place && y.blocks > 1 ? t.skip : 0;
 #pragma unroll
     for (int l = 0; l < L; ++l) {
         if (l >= n) break;
@@ -558,7 +574,8 @@ __global__ __launch_bounds__(NT) void gated_bwd_kernel(
             B[i] = token(g2, dz[l].at(i), B[i]);
             S[i] = g2 <= kLowest ? kShut : S[i] + g2;
         }
-    start_states<V, NT>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, S, B, lam);
+    start_states<V, NT>(y, t, d, tiles, chain, dh_T ? dh_T + (size_t)t.row * d : nullptr, false, S, B,
+                        lam);
     g[0].again();
 #pragma unroll
     for (int l = 0; l < L; ++l) {
@@ -688,7 +705,7 @@ template <typename TIO, int V, int NT, bool LINES>
 hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
 {
     const int per = rows_of(y, a.BH, tiles_of(y, a.T, kRunFwd));
-    const bool own = a.h0 && a.h0 == a.h_out && y.blocks > 1;
+    const bool in_place = a.h0 && a.h0 == a.h_out;
     for (long long row = 0; row < a.BH; row += per) {
         const size_t h = (size_t)row * a.d, at = h * a.T;
         const int rows = (int)std::min<long long>(per, a.BH - row);
@@ -697,7 +714,8 @@ hipError_t fwd_nt(const GatedArgs& a, const Layout& y, hipStream_t s)
         const unsigned grid = prepare(y, rows, a.T, kRunFwd, a.workspace, c, tiles, seqs, s);
         hipLaunchKernelGGL((gated_fwd_kernel<TIO, V, NT, LINES>), dim3(grid), dim3(NT), 0, s,
                            (const TIO*)a.X + at, (const TIO*)a.G + at, shifted(a.h0, h),
-                           (TIO*)a.Z + at, shifted(a.h_out, h), a.T, a.d, tiles, seqs, y, c, own);
+                           (TIO*)a.Z + at, shifted(a.h_out, h), a.T, a.d, tiles, seqs, y, c,
+                           in_place);
     }
     return hipGetLastError();
 }
