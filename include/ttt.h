@@ -396,6 +396,9 @@ int ttt_mlp_fwd_ex(const void* K, const void* Q, const void* V,
  *   - g_t = -inf, or any g_t <= -1e30 (a type's lowest value as a mask), forgets:
  *     h_t = x_t whatever h_{t-1} is, infinite and NaN included.  Documents packed in
  *     one row start anew that way.
+ *   - Under any other gate an infinite state stays infinite, however small exp(g_t) is.
+ *     Of a finite state, what factors (of one gate, or of several in a row) below 2^-126
+ *     would leave is taken as 0.
  *   - g_t = 0 with x_t = 0 carries the state through (padding of a shorter sequence:
  *     h_out is then the state at its own end).
  * Arithmetic is fp32 whatever the I/O type; every output is the same bits on every
