@@ -508,7 +508,9 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_q8_kernel(
 }
 
 // Rows too long (or too short) for the registers' layout: a workgroup per row, the row read again
-// for every pass, 8 elements of a thread at a time.
+// for every pass, 8 elements of a thread at a time.  A thread adds 8 terms in fp32 and those sums in
+// fp64: one fp32 sum of all its D / 256 terms would be off by as many roundings (mean(r^2) of equal
+// values by 4e-4 at 2^23 features).
 template <typename TIO, bool Q8>
 __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const TIO* residual,
                                                            const float* __restrict__ weight,
@@ -535,17 +537,19 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
                 f(i, x, a, w);
             }
         };
-        float ss = 0.f;
+        double ss = 0.0;
         word64 largest = 0;
         eights([&](int, const float (&x)[N], const float (&a)[N], const float (&w)[N]) {
+            float s = 0.f;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 const float r = x[n] + a[n];
-                ss = fmaf(r, r, ss);
+                s = fmaf(r, r, s);
                 if constexpr (Q8) largest = larger(largest, ((double)x[n] + a[n]) * w[n]);
             }
+            ss += s;
         });
-        const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
+        const float rate = rsqrtf(row_sum<256>((float)ss, lds) / D + eps);
         double most = 0.0;
         if constexpr (Q8) most = __longlong_as_double((long long)row_max<256>(largest, lds));
         const float of_row = Row8::scale_of(most, rate);
@@ -686,26 +690,54 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
     const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
     float eps, TIO* dX, float* __restrict__ plane, long long rows, int D)
 {
+    constexpr int N = 8;
     __shared__ unsigned lds[4];
     if (plane)
         for (int i = threadIdx.x; i < D; i += 256) plane[(size_t)blockIdx.x * D + i] = 0.f;
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
         const size_t base = (size_t)row * D;
-        float ss = 0.f, su = 0.f;
-        for (int i = threadIdx.x; i < D; i += 256) {
-            const float r = io<TIO>::load(R, base + i);
-            ss = fmaf(r, r, ss);
-            su = fmaf(io<TIO>::load(dY, base + i) * (weight ? weight[i] : 1.f), r, su);
-        }
-        const float rate = rsqrtf(row_sum<256>(ss, lds) / D + eps);
-        const float m = row_sum<256>(su, lds) * rate / D;
-        for (int i = threadIdx.x; i < D; i += 256) {
-            const float n = io<TIO>::load(R, base + i) * rate, dy = io<TIO>::load(dY, base + i);
-            if (plane) plane[(size_t)blockIdx.x * D + i] += dy * n;
-            const float u = dy * (weight ? weight[i] : 1.f);
-            io<TIO>::store(dX, base + i,
-                           fmaf(rate, u - n * m, dR ? io<TIO>::load(dR, base + i) : 0.f));
-        }
+        // f(first element, r, dy, weight) for this thread's elements: first, first + 256, ...; zeros past
+        // the row's end
+        auto eights = [&](auto&& f) {
+            for (int i = threadIdx.x; i < D; i += 256 * N) {
+                float r[N], dy[N], w[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const bool in = i + 256 * n < D;
+                    const size_t at = base + i + 256 * n;
+                    r[n] = in ? io<TIO>::load(R, at) : 0.f;
+                    dy[n] = in ? io<TIO>::load(dY, at) : 0.f;
+                    w[n] = in && weight ? weight[i + 256 * n] : 1.f;
+                }
+                f(i, r, dy, w);
+            }
+        };
+        double ss = 0.0, su = 0.0;
+        eights([&](int, const float (&r)[N], const float (&dy)[N], const float (&w)[N]) {
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                a = fmaf(r[n], r[n], a);
+                b = fmaf(dy[n] * w[n], r[n], b);
+            }
+            ss += a;
+            su += b;
+        });
+        const float rate = rsqrtf(row_sum<256>((float)ss, lds) / D + eps);
+        const float m = row_sum<256>((float)su, lds) * rate / D;
+        eights([&](int i, const float (&r)[N], const float (&dy)[N], const float (&w)[N]) {
+            float dr[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                dr[n] = dR && i + 256 * n < D ? io<TIO>::load(dR, base + i + 256 * n) : 0.f;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (i + 256 * n >= D) break;
+                const float k = r[n] * rate;
+                if (plane) plane[(size_t)blockIdx.x * D + i + 256 * n] += dy[n] * k;
+                io<TIO>::store(dX, base + i + 256 * n, fmaf(rate, dy[n] * w[n] - k * m, dr[n]));
+            }
+        });
     }
 }
 
