@@ -522,17 +522,23 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
     for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
         const size_t base = (size_t)row * D;
         // f(first element, x, residual, weight) for this thread's elements: first, first + 256, ...;
-        // zeros past the row's end
+        // zeros past the row's end.  (Loads without a condition: each one with one would be waited for
+        // by itself.)
+        const TIO* z = residual ? residual : X;
         auto eights = [&](auto&& f) {
             for (int i = threadIdx.x; i < D; i += 256 * N) {
                 float x[N], a[N], w[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const bool in = i + 256 * n < D;
-                    const size_t at = base + i + 256 * n;
-                    x[n] = in ? io<TIO>::load(X, at) : 0.f;
-                    a[n] = in && residual ? io<TIO>::load(residual, at) : -0.f;
-                    w[n] = in && weight ? weight[i + 256 * n] : 1.f;
+                    const int at = min(i + 256 * n, D - 1);
+                    x[n] = io<TIO>::load(X, base + at);
+                    a[n] = io<TIO>::load(z, base + at);
+                    w[n] = weight ? weight[at] : 1.f;
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if (i + 256 * n >= D) x[n] = a[n] = 0.f;
+                    if (!residual) a[n] = -0.f;
                 }
                 f(i, x, a, w);
             }
@@ -683,8 +689,8 @@ __global__ __launch_bounds__(kBlock<TPR>) void rms_bwd_kernel(
     }
 }
 
-// the same, a workgroup per row at a time, for the rows of rms_fwd_loop_kernel: each thread keeps
-// its columns' sums in the plane
+// the same, a workgroup per row at a time, for the rows of rms_fwd_loop_kernel; where rows are short
+// each thread keeps its columns' sums in the plane
 template <typename TIO>
 __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
     const TIO* __restrict__ R, const float* __restrict__ weight, const TIO* dY, const TIO* dR,
@@ -703,15 +709,18 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
                 float r[N], dy[N], w[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const bool in = i + 256 * n < D;
-                    const size_t at = base + i + 256 * n;
-                    r[n] = in ? io<TIO>::load(R, at) : 0.f;
-                    dy[n] = in ? io<TIO>::load(dY, at) : 0.f;
-                    w[n] = in && weight ? weight[i + 256 * n] : 1.f;
+                    const int at = min(i + 256 * n, D - 1);
+                    r[n] = io<TIO>::load(R, base + at);
+                    dy[n] = io<TIO>::load(dY, base + at);
+                    w[n] = weight ? weight[at] : 1.f;
                 }
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    if (i + 256 * n >= D) r[n] = dy[n] = 0.f;
                 f(i, r, dy, w);
             }
         };
+        const TIO* e = dR ? dR : R;
         double ss = 0.0, su = 0.0;
         eights([&](int, const float (&r)[N], const float (&dy)[N], const float (&w)[N]) {
             float a = 0.f, b = 0.f;
@@ -728,17 +737,67 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
         eights([&](int i, const float (&r)[N], const float (&dy)[N], const float (&w)[N]) {
             float dr[N];
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-                dr[n] = dR && i + 256 * n < D ? io<TIO>::load(dR, base + i + 256 * n) : 0.f;
+            for (int n = 0; n < N; ++n) dr[n] = io<TIO>::load(e, base + min(i + 256 * n, D - 1));
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (i + 256 * n >= D) break;
                 const float k = r[n] * rate;
                 if (plane) plane[(size_t)blockIdx.x * D + i + 256 * n] += dy[n] * k;
-                io<TIO>::store(dX, base + i + 256 * n, fmaf(rate, dy[n] * w[n] - k * m, dr[n]));
+                io<TIO>::store(dX, base + i + 256 * n, fmaf(rate, dy[n] * w[n] - k * m, dR ? dr[n] : 0.f));
             }
         });
     }
+}
+
+// dweight of long rows: the rows' rates first, then every column's sum by a thread, the rows dealt out to
+// gridDim.y workgroups, 8 rows at a time: 8 terms in fp32, those sums in fp64.  (A plane of dweight for
+// every workgroup of the kernel above would take 1024 times 4 D bytes, read and written for every row.)
+// Both run before that kernel, as it may write dX at dY's place.
+template <typename TIO>
+__global__ __launch_bounds__(256) void rms_rate_kernel(const TIO* __restrict__ R, float eps,
+                                                       float* __restrict__ rate, long long rows, int D)
+{
+    constexpr int N = 8;
+    __shared__ unsigned lds[4];
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        const TIO* p = R + (size_t)row * D;
+        double ss = 0.0;
+        for (int i = threadIdx.x; i < D; i += 256 * N) {
+            float s = 0.f;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const float r = io<TIO>::load(p, min(i + 256 * n, D - 1));
+                s = i + 256 * n < D ? fmaf(r, r, s) : s;
+            }
+            ss += s;
+        }
+        const float k = rsqrtf(row_sum<256>((float)ss, lds) / D + eps);
+        if (threadIdx.x == 0) rate[row] = k;
+    }
+}
+
+template <typename TIO>
+__global__ __launch_bounds__(256) void rms_columns_kernel(const TIO* __restrict__ R,
+                                                          const TIO* __restrict__ dY,
+                                                          const float* __restrict__ rate,
+                                                          float* __restrict__ plane, long long rows, int D)
+{
+    constexpr int N = 8;
+    const int c = blockIdx.x * 256 + threadIdx.x, P = gridDim.y;
+    if (c >= D) return;
+    double sum = 0.0;
+    for (long long row = blockIdx.y; row < rows; row += (long long)N * P) {
+        float s = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const long long at = row + (long long)n * P;
+            const size_t from = at < rows ? at : rows - 1;
+            const float r = io<TIO>::load(R, from * D + c), dy = io<TIO>::load(dY, from * D + c);
+            s = at < rows ? fmaf(dy, r * rate[from], s) : s;
+        }
+        sum += s;
+    }
+    plane[(size_t)blockIdx.y * D + c] = (float)sum;
 }
 
 // dweight: 32 columns a workgroup, the planes dealt out to 32 threads of each column
@@ -793,9 +852,17 @@ Shape bwd_shape_of(int D, int vec)
 int planes_of(long long rows, int D, int vec)
 {
     const Shape s = bwd_shape_of(D, vec);
+    // long rows: workgroups for 1024 threads a compute unit
+    if (!s.tpr && D >= vec) return (int)std::max(1ll, std::min<long long>(rows, (1ll << 18) / D));
     const int block = std::max(256, s.tpr), groups = s.tpr ? block / s.tpr : 1;
     const long long most = 256 * (1024 / block) / (s.k > 1 ? 2 : 1);
     return (int)std::max(1ll, std::min<long long>((rows + groups - 1) / groups, most));
+}
+
+// bytes of the workspace before the planes: the rates of long rows
+size_t rates_bytes(long long rows, int D, int vec)
+{
+    return bwd_shape_of(D, vec).tpr || D < vec ? 0 : ((size_t)rows * 4 + 255) / 256 * 256;
 }
 
 template <typename TIO, int TPR, int K, bool LINES>
@@ -894,6 +961,8 @@ hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
 {
     const Shape shape = bwd_shape_of(a.D, kVec<TIO>);
     const int planes = planes_of(a.rows, a.D, kVec<TIO>);
+    const size_t rates = rates_bytes(a.rows, a.D, kVec<TIO>);
+    float* plane = (float*)((char*)a.workspace + rates);
     if (shape.tpr) {
         switch (shape.tpr * 8 + shape.k) {
             RMS_SHAPE(bwd_launch, 2, 1, a, planes, s)
@@ -910,14 +979,22 @@ hipError_t bwd_typed(const RmsBwdArgs& a, hipStream_t s)
         default: return hipErrorInvalidValue;
         }
     } else {
-        hipLaunchKernelGGL(rms_bwd_loop_kernel<TIO>, dim3(planes), dim3(256), 0, s,
-                           (const TIO*)a.R, a.weight, (const TIO*)a.dY, (const TIO*)a.dR, a.eps,
-                           (TIO*)a.dX, a.dweight ? (float*)a.workspace : nullptr, a.rows, a.D);
+        const dim3 grid((unsigned)std::max(1ll, std::min(kMostBlocks<256>, a.rows)));
+        if (a.dweight && rates) {
+            hipLaunchKernelGGL(rms_rate_kernel<TIO>, grid, dim3(256), 0, s, (const TIO*)a.R, a.eps,
+                               (float*)a.workspace, a.rows, a.D);
+            hipLaunchKernelGGL(rms_columns_kernel<TIO>, dim3((a.D + 255) / 256, planes), dim3(256), 0, s,
+                               (const TIO*)a.R, (const TIO*)a.dY, (const float*)a.workspace, plane, a.rows,
+                               a.D);
+        }
+        hipLaunchKernelGGL(rms_bwd_loop_kernel<TIO>, grid, dim3(256), 0, s, (const TIO*)a.R, a.weight,
+                           (const TIO*)a.dY, (const TIO*)a.dR, a.eps, (TIO*)a.dX,
+                           a.dweight && !rates ? plane : nullptr, a.rows, a.D);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dweight) return e;
-    hipLaunchKernelGGL(rms_planes_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, s,
-                       (const float*)a.workspace, a.dweight, planes, a.D);
+    hipLaunchKernelGGL(rms_planes_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, s, (const float*)plane,
+                       a.dweight, planes, a.D);
     return hipGetLastError();
 }
 
@@ -930,7 +1007,8 @@ hipError_t launch_rmsnorm_fwd(const RmsArgs& a, hipStream_t s)
 
 size_t rmsnorm_bwd_workspace(long long rows, int D, bool bf16)
 {
-    return (size_t)planes_of(rows, D, bf16 ? 8 : 4) * D * 4;
+    const int vec = bf16 ? 8 : 4;
+    return rates_bytes(rows, D, vec) + (size_t)planes_of(rows, D, vec) * D * 4;
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsBwdArgs& a, hipStream_t s)

@@ -84,3 +84,24 @@ def test_backward(dev, rows, D, io, values):
         ok2, worst2 = ref.within(np64(dweight), dw, edw, "f32")
         say("  error over what is allowed: dx %.3f dw %.3f" % (worst, worst2))
         assert ok and ok2
+
+
+@pytest.mark.parametrize("rows,D,io", [(1500, 17000, "bf16"), (1100, 9001, "f32"), (4, 300000, "bf16"),
+                                       (0, 20000, "bf16")])
+def test_backward_in_place(dev, rows, D, io):
+    """dX at dY's or dR's place: dweight is formed of what stood there."""
+    import torch
+    say("case", rows, D, io)
+    R, w, dR, dY = make(dev, rows, D, io, "normal", 9)
+    dX, dw = ttt.rmsnorm_bwd(R, w, dY, dR, EPS)
+    r, dy = np64(R), np64(dY)
+    n = r / np.sqrt((r * r).mean(-1, keepdims=True) + EPS)
+    # 8 terms at a time in fp32, those sums in fp64 and rounded, up to 2^18 / 9001 = 29 planes in fp32, and
+    # k's and n's own
+    room = (8 + 1 + 29 + REL + 2) * U * (np.abs(dy) * np.abs(n)).sum(0)
+    assert ref.within(np64(dw), (dy * n).sum(0), room, "f32")[0]
+    for k in (0, 1):
+        a, b = dY.clone(), dR.clone()
+        _, dw2 = ttt.rmsnorm_bwd(R, w, a, b, EPS, dX=(a, b)[k])
+        torch.cuda.synchronize()
+        assert torch.equal((a, b)[k], dX) and torch.equal(dw, dw2)
