@@ -136,6 +136,16 @@ def plan_name(plan: int) -> str:
     return lib().ttt_plan_name(int(plan)).decode()
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _fits(*sizes):
+    """Refuses what the library's int arguments cannot hold: ctypes would drop the upper bits."""
+    for n in sizes:
+        if not -_INT_MAX - 1 <= n <= _INT_MAX:
+            raise ValueError("a size of %d is beyond the library's 32 bits" % n)
+
+
 def _io_dtype(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -160,6 +170,7 @@ def _check(t, name, shape, dtype=None):
     import torch
     if t is None:
         raise ValueError("%s is required" % name)
+    _fits(*t.shape)
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     if not t.is_contiguous():
@@ -172,6 +183,7 @@ def _check(t, name, shape, dtype=None):
 
 def linear_workspace_bytes(B, H, T, d, chunk, io_dtype=None, plan=PLAN_AUTO) -> int:
     """Workspace bytes for the shape; with io_dtype, for that dtype and plan exactly."""
+    _fits(B, H, T, d, chunk)
     if io_dtype is None:
         return int(lib().ttt_linear_workspace_bytes(B, H, T, d, chunk))
     return int(lib().ttt_linear_workspace_bytes_ex(B, H, T, d, chunk, io_dtype, plan))
@@ -179,6 +191,7 @@ def linear_workspace_bytes(B, H, T, d, chunk, io_dtype=None, plan=PLAN_AUTO) -> 
 
 def linear_select_plan(B, H, T, d, chunk, io_dtype, plan=PLAN_AUTO,
                        read_mode: int = READ_INCLUSIVE) -> int:
+    _fits(B, H, T, d, chunk)
     if read_mode == READ_INCLUSIVE:
         return int(lib().ttt_linear_select_plan(B, H, T, d, chunk, io_dtype, plan))
     return int(lib().ttt_linear_select_plan_ex(B, H, T, d, chunk, io_dtype, plan, read_mode))
@@ -186,12 +199,14 @@ def linear_select_plan(B, H, T, d, chunk, io_dtype, plan=PLAN_AUTO,
 
 def mlp_workspace_bytes(B, H, T, d, chunk, io_dtype=None, plan=PLAN_AUTO) -> int:
     """Workspace bytes for the shape; with io_dtype, for that dtype and plan exactly."""
+    _fits(B, H, T, d, chunk)
     if io_dtype is None:
         return int(lib().ttt_mlp_workspace_bytes(B, H, T, d, chunk))
     return int(lib().ttt_mlp_workspace_bytes_ex(B, H, T, d, chunk, io_dtype, plan))
 
 
 def mlp_select_plan(B, H, T, d, chunk, io_dtype, plan=PLAN_AUTO) -> int:
+    _fits(B, H, T, d, chunk)
     return int(lib().ttt_mlp_select_plan(B, H, T, d, chunk, io_dtype, plan))
 
 
@@ -253,6 +268,7 @@ def linear_fwd_noalloc(K, Q, V, eta, W0, chunk: int, eta_scalar: float = 0.0, *,
         _check(eta, "eta", (B, H, T), torch.float32)
     _check(Z, "Z", (B, H, T, d), K.dtype)
     _check(W_out, "W_out", (B, H, d, d), torch.float32)
+    _fits(chunk)
     rc = lib().ttt_linear_fwd_noalloc(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta),
                                       float(eta_scalar), W0.data_ptr(), Z.data_ptr(),
                                       W_out.data_ptr(), B, H, T, d, int(chunk), _io_dtype(K),
@@ -267,6 +283,7 @@ def linear_noalloc_scratch_bytes() -> int:
 
 
 def linear_bwd_workspace_bytes(B, H, T, d, chunk, io_dtype) -> int:
+    _fits(B, H, T, d, chunk)
     return int(lib().ttt_linear_bwd_workspace_bytes(B, H, T, d, chunk, io_dtype))
 
 
@@ -332,6 +349,7 @@ def linear_step(K, Q, V, eta, W_chunk, G, pos: int, chunk: int, eta_scalar: floa
     if Z is None:
         Z = torch.empty_like(K)
     _check(Z, "Z", (B, H, n, d), K.dtype)
+    _fits(pos, chunk)
     rc = lib().ttt_linear_step(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta),
                                float(eta_scalar), W_chunk.data_ptr(), G.data_ptr(), int(pos),
                                Z.data_ptr(), B, H, n, d, int(chunk), _io_dtype(K),
@@ -396,6 +414,7 @@ def linear_ln_fwd(K, Q, V, eta, W0, b0, ln_weight, ln_bias, chunk: int, eps: flo
     Z = torch.empty_like(K) if Z is None else Z
     W_out = torch.empty_like(W0) if W_out is None else W_out
     b_out = torch.empty_like(b0) if b_out is None else b_out
+    _fits(chunk)
     rc = lib().ttt_linear_ln_fwd(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta),
                                  float(eta_scalar), W0.data_ptr(), b0.data_ptr(), _ptr(ln_weight),
                                  _ptr(ln_bias), float(eps), Z.data_ptr(), W_out.data_ptr(),
@@ -407,6 +426,7 @@ def linear_ln_fwd(K, Q, V, eta, W0, b0, ln_weight, ln_bias, chunk: int, eps: flo
 
 
 def linear_select_plan_varlen(n_docs, H, total_T, d, chunk, io_dtype, plan=PLAN_AUTO) -> int:
+    _fits(n_docs, H, total_T, d, chunk)
     return int(lib().ttt_linear_select_plan_varlen(n_docs, H, total_T, d, chunk, io_dtype, plan))
 
 
@@ -431,6 +451,7 @@ def linear_fwd_varlen(K, Q, V, eta, W0, cu_seqlens, chunk: int, eta_scalar: floa
         W_out = torch.empty_like(W0)
     _check(Z, "Z", (H, total_T, d), K.dtype)
     _check(W_out, "W_out", (n_docs, H, d, d), torch.float32)
+    _fits(chunk)
     rc = lib().ttt_linear_fwd_varlen(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta),
                                      float(eta_scalar), W0.data_ptr(), Z.data_ptr(),
                                      W_out.data_ptr(), cu_seqlens.data_ptr(), n_docs, H, total_T,
@@ -537,6 +558,7 @@ def _scratch(nbytes, like, workspace):
 
 
 def gated_workspace_bytes(B, H, T, d, io_dtype) -> int:
+    _fits(B, H, T, d)
     return int(lib().ttt_gated_workspace_bytes(B, H, T, d, io_dtype))
 
 
@@ -545,6 +567,7 @@ def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None)
     bf16 (G <= 0; -inf, or the type's lowest value, starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
     (Z, h_T): the states in the I/O type, and the last one in fp32."""
     import torch
+    _fits(*X.shape)
     io, dev = _first(X, "X")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -577,6 +600,7 @@ def gated_step(X, G, h, *, Z=None, stream=None):
     """Continue gated recurrences by the n tokens of X, G [B, H, n, d] from the state h
     [B, H, d] fp32, which is updated in place.  Returns Z."""
     import torch
+    _fits(*X.shape)
     io, dev = _first(X, "X")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -602,6 +626,7 @@ def gated_bwd(G, Z, dZ, h0=None, dh_T=None, *, dX=None, dG=None, dh0=None, works
     """Gradients of <dZ, Z> + <dh_T, h_T> through Z, h_T = gated_fwd(X, G, h0).  Z is the
     forward call's; h0 and dh_T: [B, H, d] fp32 or None (zero).  Returns (dX, dG, dh0)."""
     import torch
+    _fits(*G.shape)
     io, dev = _first(G, "G")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -639,8 +664,9 @@ def _rms_args(X, weight, residual, name="X"):
     shape = X.shape
     if not shape or not shape[-1]:
         raise ValueError("%s needs a feature axis" % name)
-    io, dev = _first(X, name)
     D = shape[-1]
+    _fits(D)
+    io, dev = _first(X, name)
     if weight is not None:
         _match(weight, "weight", (D,), torch.float32, dev)
     if residual is not None:
@@ -705,6 +731,7 @@ def rmsnorm_q8_fwd(X, weight=None, residual=None, eps: float = 1e-6, *, Y8=None,
 
 
 def rmsnorm_bwd_workspace_bytes(rows, D, io_dtype) -> int:
+    _fits(D)
     return int(lib().ttt_rmsnorm_bwd_workspace_bytes(rows, D, io_dtype))
 
 
