@@ -838,8 +838,9 @@ Shape shape_of(int D, int vec)
 // (16384 x 2048 bf16 to e4m3: 45.0 us with twice as many, 41.2 with these).
 template <int TPR> constexpr long long kMostBlocks = 256 * (1024 / kBlock<TPR>);
 
-// The backward pass holds weight and dweight in fp32 next to three inputs: past 2048 vectors there
-// are no registers for that.
+// The backward pass holds weight and dweight in fp32 next to three inputs: past 2048 vectors a row
+// takes 1024 threads, which have 128 registers each, and four bf16 vectors take 161.  (fp32 vectors
+// take 116; their rows go the same way.)
 Shape bwd_shape_of(int D, int vec)
 {
     const Shape s = shape_of(D, vec);
@@ -892,11 +893,11 @@ void bwd_launch(const RmsBwdArgs& a, int planes, hipStream_t s)
                        (TIO*)a.dX, a.dweight ? (float*)a.workspace : nullptr, a.rows, a.D);
 }
 
-// a case of the switches over shapes
+// A case of the switches over shapes.  Rows of less than a line are never whole lines.
 #define RMS_SHAPE(f, TPR, K, ...)                                                       \
     case TPR * 8 + K:                                                                   \
         if (a.D * sizeof(TIO) % 128) f<TIO, TPR, K, false>(__VA_ARGS__);                \
-        else f<TIO, TPR, K, true>(__VA_ARGS__);                                         \
+        else f<TIO, TPR, K, (TPR) * (K) * 16 >= 128>(__VA_ARGS__);                      \
         break;
 
 template <typename TIO>
