@@ -567,7 +567,8 @@ def gated_fwd(X, G, h0=None, *, Z=None, h_out=None, workspace=None, stream=None)
     bf16 (G <= 0; -inf, or the type's lowest value, starts anew).  h0: [B, H, d] fp32 or None (zero).  Returns
     (Z, h_T): the states in the I/O type, and the last one in fp32."""
     import torch
-    _fits(*X.shape)
+    if X.numel() > _INT_MAX:       # (else no size is)
+        _fits(*X.shape)
     io, dev = _first(X, "X")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -600,7 +601,8 @@ def gated_step(X, G, h, *, Z=None, stream=None):
     """Continue gated recurrences by the n tokens of X, G [B, H, n, d] from the state h
     [B, H, d] fp32, which is updated in place.  Returns Z."""
     import torch
-    _fits(*X.shape)
+    if X.numel() > _INT_MAX:       # (else no size is)
+        _fits(*X.shape)
     io, dev = _first(X, "X")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -626,7 +628,8 @@ def gated_bwd(G, Z, dZ, h0=None, dh_T=None, *, dX=None, dG=None, dh0=None, works
     """Gradients of <dZ, Z> + <dh_T, h_T> through Z, h_T = gated_fwd(X, G, h0).  Z is the
     forward call's; h0 and dh_T: [B, H, d] fp32 or None (zero).  Returns (dX, dG, dh0)."""
     import torch
-    _fits(*G.shape)
+    if G.numel() > _INT_MAX:       # (else no size is)
+        _fits(*G.shape)
     io, dev = _first(G, "G")
     on = _elsewhere(dev, stream)
     if on is not None:
@@ -665,7 +668,8 @@ def _rms_args(X, weight, residual, name="X"):
     if not shape or not shape[-1]:
         raise ValueError("%s needs a feature axis" % name)
     D = shape[-1]
-    _fits(D)
+    if D > _INT_MAX:
+        _fits(D)
     io, dev = _first(X, name)
     if weight is not None:
         _match(weight, "weight", (D,), torch.float32, dev)
