@@ -17,7 +17,7 @@
 // the tiles before it in its group, which wait for nothing; the group's last tile publishes
 // the group's pair and then the state after the group; and a tile takes the state before
 // its group from the nearest group that has one and the pairs of the groups since.  (With
-// the states chained from tile to tile instead, 1 x 131072 x 64 took 75 us, against 27.)
+// the states chained from tile to tile instead, 1 x 131072 x 64 took 75 us, against 28.)
 // Tiles take their place by a ticket, so a tile only ever waits for tiles that run already.
 // The words they pass on are 64 bits wide, written whole and read until they are there (an
 // unwritten word is all ones, which no published one is): no fence, no flag.  What is
@@ -50,10 +50,10 @@ constexpr int kMostPolls = 1 << 22;          // seconds: only a workspace in use
 
 // V elements of the I/O type at any element-aligned address, as raw words.  Where rows are whole
 // cache lines (LINES), every line is read or written once, at once, and 16-byte accesses take the
-// non-temporal policy (8 x 12 x 2048 x 64 bf16, forward / backward: 23.1 / 32.2 us without, 21.6 /
-// 27.8 with; 1 x 32 x 32768 x 64: 105 / 162 and 93 / 144).  Elsewhere a line takes several accesses,
-// which meet in the caches only without it (64 x 32768 x 16 bf16: 106 / 262 us with, 55 / 101
-// without; 64 x 8192 x 50: 64 / 139 and 46 / 77).
+// non-temporal policy (8 x 12 x 2048 x 64 bf16, forward / backward: 23.0 / 35.0 us without, 21.1 /
+// 27.0 with; 1 x 32 x 32768 x 64: 96 / 157 and 85 / 138).  Elsewhere a line takes several accesses,
+// which meet in the caches only without it (64 x 32768 x 16 bf16: 106 / 260 us with, 60 / 109
+// without; 64 x 8192 x 50: 64 / 142 and 50 / 85).
 typedef uint32_t quad __attribute__((ext_vector_type(4)));
 typedef quad quad_any __attribute__((aligned(2)));
 
@@ -236,9 +236,9 @@ Layout layout_of(int d, bool bf16, int threads)
     y.V = bf16 ? 8 : 4;
     while (y.V > d) y.V >>= 1;
     // Where rows are whole cache lines, a block is one line wide, or two where that makes more
-    // than four blocks: long tiles, so few of them wait for each other (15 x 4097 x 64 fp32,
-    // forward: 17.5 us with lines, 19.2 with whole rows; x 96: 20.7 and 26.3).  Elsewhere
-    // blocks would share lines (x 80: 29.2 with lines, 24.1 with whole rows).
+    // than four blocks: long tiles, so few of them wait for each other (15 x 4097 x 96 fp32,
+    // forward: 19.1 us with lines, 20.0 with whole rows; x 64: 16 either way).  Elsewhere blocks
+    // would share lines (x 80: 22.2 with lines, 19.3 with whole rows).
     const int groups = (d + y.V - 1) / y.V, bytes = d * (bf16 ? 2 : 4);
     y.lines = bytes % 128 == 0;
     const int most = !y.lines ? 256 / y.V : bytes <= 512 ? 8 : 16;
@@ -791,10 +791,10 @@ long long tiles_of(const Layout& y, int T, int L)
 
 // Workgroups of 512 threads where they hold a row's tokens in one tile and ones of 256 do not: no
 // chain to clear and to wait for.  bf16, d = 64, with 512 and with 256: 96 rows of 512 tokens,
-// forward 10.3 and 13.2 us, backward 14.5 and 15.7; 256 rows 12.3 and 15.2, 17.7 and 21.0.  (Rows
-// of two tiles and more gain nothing from 512: 96 x 2048 22.0 and 20.2 us.)  The backward kernel's
+// forward 11.3 and 14.3 us, backward 14.9 and 17.1; 256 rows 12.9 and 16.4, 18.0 and 21.2.  (Rows
+// of two tiles and more gain nothing from 512: 96 x 2048 22.7 and 20.5 us.)  The backward kernel's
 // registers allow one such workgroup a compute unit, so it takes them up to 256: 384 rows of 512
-// are 31.6 and 25.4 us.
+// are 31.3 and 25.9 us.
 bool one_tile_of_512(const Layout& y256, const Layout& y512, bool bf16, int T, int L)
 {
     return y256.V == (bf16 ? 8 : 4) && tiles_of(y256, T, L) > 1 && tiles_of(y512, T, L) == 1;
@@ -955,8 +955,8 @@ hipError_t launch_gated_step(const GatedArgs& a, hipStream_t s)
 }
 
 // The serial kernel also takes short rows: a tile of them is mostly empty, and costs its
-// latencies all the same.  bf16, d = 64, serial / tiles: 1000 rows of 16 tokens 9.0 / 12.3 us, of
-// 32 15.0 / 12.0; 10000 rows of 16 14.8 / 73, of 32 28.4 / 75, of 64 56 / 76.
+// latencies all the same.  bf16, d = 64, serial / tiles: 1000 rows of 16 tokens 9.0 / 12.8 us, of
+// 32 13.9 / 12.8; 10000 rows of 16 16 / 79, of 32 35 / 79, of 64 62 / 80.
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t s)
 {
     const Layout y = fwd_layout(a.T, a.d, a.bf16);

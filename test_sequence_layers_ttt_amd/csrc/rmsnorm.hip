@@ -6,7 +6,7 @@
 // bf16 backward 99 us for 537 MB, 5.4 TB/s; 16384 x 2048 to e4m3 42 us for 235 MB; a
 // device copy reaches 5.2 TB/s).  Rows of up to 128 vectors stay within one wave (sums by
 // lane exchanges, no LDS, no barrier); longer ones take a workgroup: 256 threads with one
-// vector each beat one wave with four (16384 x 2048 to e4m3: 45 and 92 us), which had too
+// vector each beat one wave with four (16384 x 2048 to e4m3: 46 and 53 us), which has too
 // few loads under way.  A last vector that would pass the row's end starts early enough
 // to be whole: what it shares with the one before is left out of the sums and written
 // twice, with the same bits.  (All of a row's loads come before its first store, so
@@ -835,7 +835,7 @@ Shape shape_of(int D, int vec)
 }
 
 // Workgroups of a launch: 1024 threads a compute unit, each with many rows, as each loads the weight
-// (16384 x 2048 bf16 to e4m3: 45.0 us with twice as many, 41.2 with these).
+// (16384 x 2048 bf16 to e4m3: 47.4 us with twice as many, 46.2 with these).
 template <int TPR> constexpr long long kMostBlocks = 256 * (1024 / kBlock<TPR>);
 
 // The backward pass holds weight and dweight in fp32 next to three inputs: past 2048 vectors a row
