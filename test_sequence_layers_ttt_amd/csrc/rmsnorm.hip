@@ -537,7 +537,10 @@ __global__ __launch_bounds__(256) void rms_fwd_loop_kernel(const TIO* X, const T
                 }
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    if (i + 256 * n >= D) x[n] = a[n] = 0.f;
+                    if (i + 256 * n >= D) {
+                        x[n] = a[n] = 0.f;
+                        w[n] = 1.f;
+                    }
                     if (!residual) a[n] = -0.f;
                 }
                 f(i, x, a, w);
@@ -716,7 +719,10 @@ __global__ __launch_bounds__(256) void rms_bwd_loop_kernel(
                 }
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    if (i + 256 * n >= D) r[n] = dy[n] = 0.f;
+                    if (i + 256 * n >= D) {
+                        r[n] = dy[n] = 0.f;
+                        w[n] = 1.f;
+                    }
                 f(i, r, dy, w);
             }
         };

@@ -108,12 +108,14 @@ def test_ordinary_rows(dev, rows, D, io):
 @pytest.mark.parametrize("D", [33, 64, 1024, 5000, 40000])
 def test_a_weight_that_is_not_finite(dev, D, io):
     """A NaN weight makes every row's scale and values NaN; an infinite one (the largest |y| is infinite)
-    the values."""
+    the values, and the scale infinite."""
     import torch
     X = torch.from_numpy(in_type(np.random.default_rng(D).standard_normal((5, D)), io)).to(dev)
     X = X.to(torch.bfloat16 if io == "bf16" else torch.float32)
     for bad in (float("nan"), float("inf")):
-        w = torch.ones(D, device=dev)
-        w[D // 2] = bad
-        Y8, scale, _ = ttt.rmsnorm_q8_fwd(X, w, None, EPS)
-        assert torch.isnan(Y8.float()).all() and not torch.isfinite(scale).any()
+        for at in (D // 2, D - 1):
+            w = torch.ones(D, device=dev)
+            w[at] = bad
+            Y8, scale, _ = ttt.rmsnorm_q8_fwd(X, w, None, EPS)
+            assert torch.isnan(Y8.float()).all()
+            assert (torch.isnan(scale) if bad != bad else torch.isposinf(scale)).all()
