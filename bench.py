@@ -57,8 +57,13 @@ KERNEL_SOURCES = {"linear_b16": ["linear_mfma.hip", "linear_coop.hip", "mfma_com
                             "block_launch.h"],
                   "rmsnorm": ["rmsnorm.hip", "mfma_common.h", "device_common.h",
                               "block_launch.h"],
-                  "clip": ["clip.hip", "mfma_common.h", "device_common.h", "block_launch.h"]}
-HOST_ONLY_SOURCES = {"api.cpp", "api_block.cpp", "host_checks.h"}
+                  "clip": ["clip.hip", "mfma_common.h", "device_common.h", "block_launch.h"],
+                  "delta": ["delta.hip", "delta_bwd.hip", "delta_common.h", "delta_launch.h",
+                            "mfma_f32.h", "mfma_common.h", "device_common.h"],
+                  "groupnorm": ["groupnorm.hip", "mfma_common.h", "device_common.h",
+                                "block_launch.h"],
+                  "dropout": ["dropout.hip", "mfma_common.h", "device_common.h", "block_launch.h"]}
+HOST_ONLY_SOURCES = {"api.cpp", "api_block.cpp", "api_delta.cpp", "host_checks.h"}
 
 
 def kernel_family(wl, plan_name: str) -> str:

@@ -115,6 +115,19 @@ typedef enum {
     TTT_READ_CHUNK_START = 1
 } ttt_read_mode;
 
+/* Order of the axes of token tensors, where a call takes one. */
+typedef enum {
+    TTT_LAYOUT_BHTD = 0,        /* [B, H, T, d]; per-token scalars [B, H, T] */
+    TTT_LAYOUT_BTHD = 1         /* [B, T, H, d]; per-token scalars [B, T, H] */
+} ttt_layout;
+
+/* Activations of ttt_groupnorm_fwd. */
+typedef enum {
+    TTT_ACT_NONE = 0,
+    TTT_ACT_SILU = 1,           /* v / (1 + exp(-v)) */
+    TTT_ACT_GELU = 2            /* the exact erf form */
+} ttt_act;
+
 /* ------------------------------------------------------------------------ */
 /* TTT-Linear                                                                */
 /* ------------------------------------------------------------------------ */
@@ -518,6 +531,131 @@ int ttt_clip_grad_norm(int n, const void* const* grads, void* const* outs,
 
 /* Bytes of workspace ttt_clip_grad_norm needs, whatever the tensors. */
 size_t ttt_clip_workspace_bytes(void);
+
+/* ------------------------------------------------------------------------ */
+/* Gated delta rule                                                          */
+/* ------------------------------------------------------------------------ */
+
+/* The fast-weight state of TTT-Linear with one gradient step per token, taken at the
+ * state right before it, and a decay of the state:
+ *   u_t = v_t - exp(g_t) W_{t-1} k_t,
+ *   W_t = exp(g_t) W_{t-1} + eta_t u_t k_t^T,      z_t = W_t q_t.
+ * With g = 0 it is ttt_linear_fwd with chunk = 1 (and any widths of keys and values).
+ *   K, Q    : tokens of Hk heads of dk features, in io_dtype;  H must be a multiple of Hk:
+ *             head h of values uses head h / (H / Hk) of keys and queries.
+ *   V, Z    : tokens of H heads of dv features, in io_dtype (Z: output).
+ *   layout  : a ttt_layout, for every token tensor of the call (eta and g too).
+ *   eta     : fp32 step size of each token and head, or NULL to use eta_scalar (finite).
+ *             A token with eta = 0 writes nothing.
+ *   g       : fp32 logarithm of each token's decay, or NULL for none.  g_t <= 0 is meant;
+ *             values above 0 grow the state and are not checked.  g_t = -inf, or any
+ *             g_t <= -1e30, forgets a finite state entirely: documents packed in one row
+ *             start anew that way.  eta_t = 0 with g_t = 0 carries the state through the
+ *             padding of a shorter sequence (whose keys and values have to be finite).
+ *   W0      : [B, H, dv, dk] fp32 state before the first token, or NULL for zero.
+ *   W_out   : [B, H, dv, dk] fp32 state after the last token (may be W0), or NULL.
+ *   1 <= dk <= 128, 1 <= dv <= 256 (TTT_ERR_UNSUPPORTED past that), T >= 1; token tensors
+ *   and states 16-byte aligned, eta and g 4-byte.
+ *   workspace : at least ttt_delta_workspace_bytes(...) bytes, 256-byte aligned; one for
+ *             each call that may overlap in time, graph replays included.
+ * Sums, states and the products behind W_out are fp32 (operands that are not exact in bf16
+ * go to the matrix cores in three bf16 parts); of the products behind a bf16 Z what is
+ * below 2^-16 of them is left out.  Non-finite values spread within their (batch, head) and
+ * may turn NaN.  Every output is the same bits on every call. */
+int ttt_delta_fwd(const void* K, const void* Q, const void* V, const float* eta, float eta_scalar,
+                  const float* g, const float* W0, void* Z, float* W_out,
+                  int B, int H, int Hk, int T, int dk, int dv, int layout, int io_dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_delta_fwd needs (0 for shapes it refuses and for few tokens). */
+size_t ttt_delta_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, int io_dtype);
+
+/* Streaming continuation (decode): n more tokens of every sequence, the state W
+ * [B, H, dv, dk] fp32 updated in place.  The same as ttt_delta_fwd from W0 = W to W_out = W,
+ * token by token without a workspace, so n is meant to be small (any n >= 1 is right). */
+int ttt_delta_step(const void* K, const void* Q, const void* V, const float* eta, float eta_scalar,
+                   const float* g, float* W, void* Z,
+                   int B, int H, int Hk, int n, int dk, int dv, int layout, int io_dtype,
+                   void* stream);
+
+/* Backward pass (vector-Jacobian product) of ttt_delta_fwd: the gradients of
+ * L = <dZ, Z> + <dW_T, W_out>.  The forward scan is run again from W0 (nothing is kept from
+ * a ttt_delta_fwd call).
+ *   K, Q, V, eta, eta_scalar, g, W0, layout : as given to ttt_delta_fwd.
+ *   dZ         : like Z;  dW_T : [B, H, dv, dk] fp32, or NULL for zero.
+ *   dK, dQ     : like K (outputs; summed over the heads that share them, in fp32).
+ *   dV         : like V (output).
+ *   deta, dg   : like eta and g, fp32 (outputs, also where eta or g is NULL), or NULL to
+ *                leave them out.  dg is 0 where g_t forgets.
+ *   dW0        : [B, H, dv, dk] fp32 (output), or NULL.
+ *   workspace  : at least ttt_delta_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ * Outputs must not overlap inputs or each other.  Every output is the same bits on every
+ * call. */
+int ttt_delta_bwd(const void* K, const void* Q, const void* V, const float* eta, float eta_scalar,
+                  const float* g, const float* W0, const void* dZ, const float* dW_T,
+                  void* dK, void* dQ, void* dV, float* deta, float* dg, float* dW0,
+                  int B, int H, int Hk, int T, int dk, int dv, int layout, int io_dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_delta_bwd needs (0 for shapes it refuses). */
+size_t ttt_delta_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, int io_dtype);
+
+/* ------------------------------------------------------------------------ */
+/* Group norm with an activation                                             */
+/* ------------------------------------------------------------------------ */
+
+/* Over channels-last tensors [N, S, C]: each row's S places and the C / G neighbouring
+ * channels of a group are normed together,
+ *   y = act((x - mean) / sqrt(var + eps) * weight + bias),   var = mean((x - mean)^2).
+ * S = 1 is the norm of each of G heads' features of each of N tokens.
+ *   X, Y         : [N, S, C] in io_dtype (Y: output; may be X).
+ *   weight, bias : [C] fp32, or NULL for ones and zeros.
+ *   mean, rstd   : [N, G] fp32 (outputs: the mean and 1 / sqrt(var + eps)).
+ *   act          : a ttt_act.  eps : > 0 and finite (no denormal number).
+ *   N, S >= 0 (0 does nothing), C a multiple of G, C <= 2^20; X and Y 16-byte aligned,
+ *   the others 4-byte.
+ *   workspace    : at least ttt_groupnorm_workspace_bytes(...) bytes, 256-byte aligned.
+ * Arithmetic is fp32, sums in a fixed order: the same bits on every call. */
+int ttt_groupnorm_fwd(const void* X, const float* weight, const float* bias, float eps, int act,
+                      void* Y, float* mean, float* rstd, long long N, long long S, int C, int G,
+                      int io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace ttt_groupnorm_fwd needs (0 for shapes it refuses and where S = 1 and a
+ * group is small). */
+size_t ttt_groupnorm_workspace_bytes(long long N, long long S, int C, int G, int io_dtype);
+
+/* Backward pass of ttt_groupnorm_fwd.  With n = (x - mean) rstd, v = n weight + bias and
+ * u = dy act'(v) weight,
+ *   dx = rstd (u - mean(u) - n mean(u n)),  dweight = sum of dy act'(v) n,
+ *   dbias = sum of dy act'(v).
+ *   X, weight, bias, act : as given to ttt_groupnorm_fwd;  mean, rstd : as it returned them.
+ *   dY      : [N, S, C] in io_dtype;  dX : [N, S, C] in io_dtype (output; may be dY or X).
+ *   dweight, dbias : [C] fp32 (outputs; zeros where N or S is 0), or NULL.
+ *   workspace : at least ttt_groupnorm_bwd_workspace_bytes(...) bytes, 256-byte aligned. */
+int ttt_groupnorm_bwd(const void* X, const float* weight, const float* bias, int act,
+                      const float* mean, const float* rstd, const void* dY, void* dX,
+                      float* dweight, float* dbias, long long N, long long S, int C, int G,
+                      int io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t ttt_groupnorm_bwd_workspace_bytes(long long N, long long S, int C, int G, int io_dtype);
+
+/* ------------------------------------------------------------------------ */
+/* Dropout                                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* y_i = keep_i x_i / (1 - p) + residual_i (no residual where NULL), where a dropped x_i
+ * leaves 0 whatever it is.  keep_i holds where a 32-bit number is at least p 2^32 (to the
+ * nearest): word i mod 4 of Philox 4x32 (10 rounds) of the key rng[0] and the counter
+ * rng[1] + floor(i / 4), a 64-bit number in the counter's lower words.  The gradient for x is
+ * the same call on dy without a residual, so no mask is kept; the next call's counter is this
+ * one's plus ceil(n / 4).
+ *   X, residual, Y : n elements in io_dtype, 16-byte aligned (Y: output; may be X or
+ *                    residual).  n >= 0.
+ *   p   : 0 <= p < 1.
+ *   rng : DEVICE int64 [2], 8-byte aligned: seed and first counter, read by the kernel, so
+ *         replays of a captured graph draw anew when it changes between them. */
+int ttt_dropout(const void* X, const void* residual, void* Y, long long n, double p,
+                const long long* rng, int io_dtype, void* stream);
 
 /* Static string for a ttt_status value (or "unknown status"). */
 const char* ttt_status_string(int status);

@@ -1,5 +1,5 @@
 // Internal launchers of the operators around the scan (gated recurrence, RMS norm,
-// gradient clipping).  The C ABI (api_block.cpp) validates every argument before calling
+// gradient clipping, group norm, dropout).  The C ABI (api_block.cpp) validates every argument before calling
 // these; they only size grids and launch.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -82,5 +82,46 @@ struct ClipArgs {
 };
 hipError_t launch_clip(const ClipArgs& a, hipStream_t s);
 size_t clip_workspace();
+
+// Group norm with an activation over channels-last tensors [N, S, C] (act: ttt_act).
+struct GroupArgs {
+    const void* X;
+    const float *weight, *bias;   // [C] or nullptr
+    float eps;
+    void* Y;
+    float *mean, *rstd;           // [N, G]
+    long long N, S;
+    int C, G, act;
+    int bf16;
+    void* workspace;
+};
+hipError_t launch_groupnorm_fwd(const GroupArgs& a, hipStream_t s);
+size_t groupnorm_fwd_workspace(long long N, long long S, int C, int G, bool bf16);
+
+struct GroupBwdArgs {
+    const void *X, *dY;
+    const float *weight, *bias, *mean, *rstd;
+    void* dX;
+    float *dweight, *dbias;       // [C] or nullptr
+    long long N, S;
+    int C, G, act;
+    int bf16;
+    void* workspace;
+};
+hipError_t launch_groupnorm_bwd(const GroupBwdArgs& a, hipStream_t s);
+size_t groupnorm_bwd_workspace(long long N, long long S, int C, int G, bool bf16);
+
+// Dropout by a counter-based generator, with the residual's addition.
+struct DropoutArgs {
+    const void* X;
+    const void* residual;         // or nullptr
+    void* Y;
+    long long n;
+    const long long* rng;         // device: seed, first counter
+    unsigned threshold;           // of 2^32
+    float scale;
+    int bf16;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
 
 }  // namespace ttt

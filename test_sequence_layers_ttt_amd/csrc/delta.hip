@@ -1,0 +1,507 @@
+// Gated delta rule: forward pass by chunks of 64 tokens, and the token-by-token form.
+// (delta_common.h has the formulas.)
+//
+// Two kernels.  The first prepares every chunk of every head by itself: decays, K K^T,
+// Q K^T and the triangular solve S.  The second scans the chunks in order: a wave keeps
+// W^T for 16 columns of values in fp32 registers for the whole sequence, since columns
+// never meet; the result tiles of one product are, as they lie in registers, operands of
+// the next, so nothing but keys and queries goes through LDS.
+#include <algorithm>
+
+#include "delta_common.h"
+#include "mfma_f32.h"
+
+namespace ttt {
+namespace {
+
+__device__ __forceinline__ double shift_up(double x, int by) { return __shfl_up(x, by, 64); }
+
+// ---- per chunk: decays, L, S, P -------------------------------------------------
+// One workgroup of four waves per (chunk, head).  S = (I + L eta)^-1 L column tile by
+// column tile: the four 16 x 16 diagonal blocks are inverted by substitution, the tiles
+// below follow from them in order, in fp32 throughout.
+template <typename TIO, int DK, bool BACKWARD>
+__global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
+{
+    constexpr int LD = kChunk + 4;
+    __shared__ __align__(16) Tile<TIO, DK> tk;
+    __shared__ __align__(16) Tile<TIO, DK> tq;
+    __shared__ __align__(16) float Lm[kChunk * LD], Pm[kChunk * LD], Sm[kChunk * LD], Tm[4 * 16 * 20];
+    __shared__ double G[kChunk];
+    __shared__ int cuts[kChunk];
+    __shared__ __align__(16) float eta[kChunk];
+
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int chunk = blockIdx.x % a.chunks, local = blockIdx.x / a.chunks;
+    const int head = a.head0 + local, b = head / a.f.H, h = head % a.f.H;
+    const int hk = h / (a.f.H / a.f.Hk), t0 = chunk * kChunk, T = a.f.T, dk = a.f.dk;
+    const bool whole = dk % kGran<TIO> == 0;
+
+    {
+        TileLoad<TIO, DK> lk, lq;
+        const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        lk.load(K, t0, T, dk, whole, tid);
+        lq.load(Q, t0, T, dk, whole, tid);
+        lk.put(tk, tid);
+        lq.put(tq, tid);
+    }
+    const size_t unit = (size_t)local * a.chunks + chunk;
+    Record& rec = a.records[unit];
+    if (w == 0) {
+        const int t = t0 + lane;
+        const Rows<const float> rg(a.f.g, b, h, a.f.H, T, 1, a.f.tokens_first);
+        const Rows<const float> re(a.f.eta, b, h, a.f.H, T, 1, a.f.tokens_first);
+        const float gt = a.f.g && t < T ? *rg.at(t) : 0.f;
+        const float et = t < T ? (a.f.eta ? *re.at(t) : a.f.eta_scalar) : 0.f;
+        int n = gt <= kForget;
+        // (sums in fp64: differences of far sums have to keep their own digits)
+        double x = n ? 0.0 : (double)gt;
+        for (int o = 1; o < 64; o <<= 1) {
+            const double y = shift_up(x, o);
+            const int m = __shfl_up(n, o, 64);
+            if (lane >= o) { x += y; n += m; }
+        }
+        G[lane] = x; cuts[lane] = n; eta[lane] = et;
+        const double xl = __shfl(x, 63, 64);
+        const int nl = __shfl(n, 63, 64);
+        rec.G[lane] = x; rec.cuts[lane] = n; rec.eta[lane] = et;
+        rec.start[lane] = n == 0 ? expf((float)x) : 0.f;
+        rec.end[lane] = n == nl ? expf((float)(xl - x)) : 0.f;
+    }
+    __syncthreads();
+
+    // row tile w of L and P
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+        if (i <= w) {
+#pragma unroll
+            for (int j = 0; j < DK / 32; ++j) {
+                const auto s = by_token(tk, i, j, lane);
+                kk = mma(by_token(tk, w, j, lane), s, kk);
+                qk = mma(by_token(tq, w, j, lane), s, qk);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int t = 16 * w + 4 * g + v, s = 16 * i + c;
+                const float e = s <= t ? pair_decay(G, cuts, t, s) : 0.f;
+                kk[v] = s < t ? kk[v] * e : 0.f;
+                qk[v] = s <= t ? qk[v] * e : 0.f;
+            }
+        }
+        put_cl<LD>(Lm + 16 * w * LD, 16 * i, lane, kk);
+        put_cl<LD>(Pm + 16 * w * LD, 16 * i, lane, qk);
+    }
+    __syncthreads();
+
+    // (I + L eta)^-1 of diagonal block w, column c (the four groups of lanes do the same)
+    {
+        float x[16];
+        const float* L = Lm + 16 * w * LD + 16 * w;
+        float e[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s) e[s] = eta[16 * w + s];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            float y = t == c ? 1.f : 0.f;
+#pragma unroll
+            for (int s = 0; s < t; ++s) y = fmaf(-L[t * LD + s] * e[s], x[s], y);
+            x[t] = y;
+        }
+        if (g == 0)
+#pragma unroll
+            for (int t = 0; t < 16; ++t) Tm[(16 * w + t) * 20 + c] = x[t];
+    }
+    __syncthreads();
+
+    // column tile w of S, from its diagonal block down
+    {
+        f32x4 S[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (i >= w) {
+                f32x4 r = cl<LD>(Lm + 16 * i * LD, 16 * w, lane);
+#pragma unroll
+                for (int j = 0; j < i; ++j)
+                    if (j >= w) {
+                        const f32x4 n = rl<LD>(Lm + 16 * i * LD, 16 * j, lane);
+                        const f32x4 e = *reinterpret_cast<const f32x4*>(eta + 16 * j + 4 * g);
+                        r = mm16(-(n * e), S[j], r);
+                    }
+                S[i] = mm16(rl<20>(Tm + 16 * i * 20, 0, lane), r, f32x4{0.f, 0.f, 0.f, 0.f});
+            }
+            put_cl<LD>(Sm + 16 * i * LD, 16 * w, lane, S[i]);
+        }
+    }
+    __syncthreads();
+
+    Frag* fs = a.S + unit * kFrags;
+    Frag* fp = a.P + unit * kFrags;
+    auto down = [&](const float* M, int i, int j) {   // column 16 i + c over the pair's rows
+        const float* p = M + (32 * j + 4 * g) * LD + 16 * i + c;
+        return f32x4{p[0], p[LD], p[2 * LD], p[3 * LD]};
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (j <= w / 2) {
+            const int f = frag_lower(w, j);
+            store_frag(fs[f], lane, rl<LD>(Sm + 16 * w * LD, 32 * j, lane),
+                       rl<LD>(Sm + 16 * w * LD, 32 * j + 16, lane));
+            if constexpr (!BACKWARD)
+                store_frag(fp[f], lane, rl<LD>(Pm + 16 * w * LD, 32 * j, lane),
+                           rl<LD>(Pm + 16 * w * LD, 32 * j + 16, lane));
+        }
+        if constexpr (BACKWARD) {
+            if (j >= w / 2) {
+                const int f = frag_upper(w, j);
+                store_frag(a.St[unit * kFrags + f], lane, down(Sm, w, j), down(Sm + 16 * LD, w, j));
+                store_frag(fp[f], lane, down(Pm, w, j), down(Pm + 16 * LD, w, j));
+            }
+        }
+    }
+}
+
+// ---- the scan over the chunks ------------------------------------------------------
+// One workgroup of four waves per head and 64 columns of values, a wave for 16 of them.
+// Keys and queries of the next chunk are loaded while this one is worked on and go to the
+// other half of the LDS buffer: one barrier a chunk.
+template <typename TIO, int DK, bool SAVE>
+__global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
+{
+    constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
+    // the order to which the products behind Z go: its own rounding to bf16 is far above 2^-17
+    constexpr int OZ = sizeof(TIO) == 2 ? 1 : 2, NZ = OZ + 1;
+    __shared__ __align__(16) Tile<TIO, DK> tk[2];
+    __shared__ __align__(16) Tile<TIO, DK> tq[SAVE ? 1 : 2];
+
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
+    const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
+    const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
+    const int col = 64 * (blockIdx.x % parts) + 16 * w + c;
+    const bool works = 64 * (int)(blockIdx.x % parts) + 16 * w < a.dvp;   // (else a wave only helps to load)
+    const bool whole = dk % kGran<TIO> == 0;
+    const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<const TIO> V((const TIO*)a.f.V, b, h, a.f.H, T, dv, a.f.tokens_first);
+    const Rows<TIO> Z((TIO*)a.f.Z, b, h, a.f.H, T, dv, a.f.tokens_first);
+    const size_t state = (size_t)head * dv * dk;
+
+    f32x4 W[M], vn[4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        W[m] = load_state(a.f.W0 ? a.f.W0 + state : nullptr, col, 16 * m + 4 * g, dv, dk);
+    TileLoad<TIO, DK> lk, lq;
+    lk.load(K, 0, T, dk, whole, tid);
+    lk.put(tk[0], tid);
+    if constexpr (!SAVE) {
+        lq.load(Q, 0, T, dk, whole, tid);
+        lq.put(tq[0], tid);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vn[i] = load_cl(V, 0, T, i, g, col, dv);
+    __syncthreads();
+
+    for (int n = 0; n < a.chunks; ++n) {
+        const int t0 = n * kChunk, next = t0 + kChunk;
+        const size_t unit = (size_t)local * a.chunks + n;
+        const Tile<TIO, DK>& k = tk[n & 1];
+        const Tile<TIO, DK>& q = tq[SAVE ? 0 : n & 1];
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = vn[i];
+        if (n + 1 < a.chunks) {
+            lk.load(K, next, T, dk, whole, tid);
+            if constexpr (!SAVE) lq.load(Q, next, T, dk, whole, tid);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vn[i] = load_cl(V, next, T, i, g, col, dv);
+        }
+        if (works) {
+            const Record& rec = a.records[unit];
+            const Frag* fs = a.S + unit * kFrags;
+            f32x4 start[4], eta[4], end[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                start[i] = *reinterpret_cast<const f32x4*>(rec.start + 16 * i + 4 * g);
+                eta[i] = *reinterpret_cast<const f32x4*>(rec.eta + 16 * i + 4 * g);
+                end[i] = *reinterpret_cast<const f32x4*>(rec.end + 16 * i + 4 * g);
+            }
+            const float all = rec.start[kChunk - 1];
+            Parts<3> S[kFrags];
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(fs[f], lane);
+
+            f32x4 r[4], z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const Parts<3> wp = split<3>(W[2 * j], W[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    r[i] = mma(by_token(k, i, j, lane), wp, r[i]);
+                    if constexpr (!SAVE) z[i] = mma<OZ>(by_token(q, i, j, lane), wp, z[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
+            Parts<3> x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j <= i / 2; ++j) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
+            if constexpr (SAVE) {
+                float* st = a.states + unit * DK * a.dvp + col;
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[(size_t)(16 * m + 4 * g + e) * a.dvp] = W[m][e];
+                float* u = a.U + unit * kChunk * a.dvp + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[(size_t)(16 * i + 4 * g + e) * a.dvp] = r[i][e];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] *= eta[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = split<3>(end[2 * j] * r[2 * j], end[2 * j + 1] * r[2 * j + 1]);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                W[m] *= all;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) W[m] = mma(by_feature(k, m, j, lane), x[j], W[m]);
+            }
+            if constexpr (!SAVE) {
+                const Frag* fp = a.P + unit * kFrags;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) x[j] = split<3>(r[2 * j], r[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    z[i] *= start[i];
+#pragma unroll
+                    for (int j = 0; j <= i / 2; ++j)
+                        z[i] = mma<OZ>(load_frag<NZ>(fp[frag_lower(i, j)], lane), x[j], z[i]);
+                    store_cl(Z, t0, T, i, g, col, dv, z[i]);
+                }
+            }
+        }
+        if (n + 1 < a.chunks) {
+            lk.put(tk[(n + 1) & 1], tid);
+            if constexpr (!SAVE) lq.put(tq[SAVE ? 0 : (n + 1) & 1], tid);
+        }
+        __syncthreads();
+    }
+    if constexpr (!SAVE)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            store_state(a.f.W_out ? a.f.W_out + state : nullptr, col, 16 * m + 4 * g, dv, dk, W[m]);
+}
+
+// ---- token after token ---------------------------------------------------------------
+// 16 lanes hold a row of the state, 4 X features each; a workgroup of 256 threads 16 rows.
+// HBM bounds the decoded token of a large batch (the state in and out).  W k and W q are
+// summed at once: z = exp(g) W q + eta u (k.q).
+template <typename TIO, int X>
+__global__ void __launch_bounds__(256) delta_step_kernel(DeltaArgs a, int parts)
+{
+    const int tid = threadIdx.x, c = tid & 15;
+    const int head = blockIdx.x / parts, row = (blockIdx.x % parts) * 16 + (tid >> 4);
+    const int b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk), T = a.T, dk = a.dk, dv = a.dv;
+    const Rows<const TIO> K((const TIO*)a.K, b, hk, a.Hk, T, dk, a.tokens_first);
+    const Rows<const TIO> Q((const TIO*)a.Q, b, hk, a.Hk, T, dk, a.tokens_first);
+    const Rows<const TIO> V((const TIO*)a.V, b, h, a.H, T, dv, a.tokens_first);
+    const Rows<TIO> Z((TIO*)a.Z, b, h, a.H, T, dv, a.tokens_first);
+    const Rows<const float> rg(a.g, b, h, a.H, T, 1, a.tokens_first);
+    const Rows<const float> re(a.eta, b, h, a.H, T, 1, a.tokens_first);
+    const bool in = row < dv, fours = dk % 4 == 0;
+    const size_t state = ((size_t)head * dv + (in ? row : 0)) * dk;
+
+    f32x4 W[X];
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+        const int f = 64 * x + 4 * c;
+        W[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (a.W0 && in) {
+            if (fours) {
+                if (f < dk) W[x] = *reinterpret_cast<const f32x4*>(a.W0 + state + f);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (f + v < dk) W[x][v] = a.W0[state + f + v];
+            }
+        }
+    }
+    auto four = [&](const TIO* p, int f) {
+        f32x4 r = {0.f, 0.f, 0.f, 0.f};
+        if (fours) {
+            if (f < dk) {
+                if constexpr (sizeof(TIO) == 2) r = widen4(*reinterpret_cast<const u32x2*>(p + f));
+                else r = *reinterpret_cast<const f32x4*>(p + f);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (f + v < dk) r[v] = load1(p + f + v);
+        }
+        return r;
+    };
+    for (int t = 0; t < T; ++t) {
+        f32x4 k[X], q[X];
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            k[x] = four(K.at(t), 64 * x + 4 * c);
+            q[x] = four(Q.at(t), 64 * x + 4 * c);
+        }
+        const float gt = a.g ? *rg.at(t) : 0.f, eta = a.eta ? *re.at(t) : a.eta_scalar;
+        const float v = in ? load1(V.at(t) + row) : 0.f;
+        const float decay = gt <= kForget ? 0.f : expf(gt);
+        float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            W[x] *= decay;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[0] = fmaf(W[x][e], k[x][e], sum[0]);
+                sum[1] = fmaf(W[x][e], q[x][e], sum[1]);
+                sum[2] = fmaf(k[x][e], q[x][e], sum[2]);
+            }
+        }
+        row_sum16_n(sum);
+        const float u = eta * (v - sum[0]);
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) W[x][e] = fmaf(u, k[x][e], W[x][e]);
+        if (in && c == 0) store1(Z.at(t) + row, fmaf(u, sum[2], sum[1]));
+    }
+    if (a.W_out && in)
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            const int f = 64 * x + 4 * c;
+            if (fours) {
+                if (f < dk) *reinterpret_cast<f32x4*>(a.W_out + state + f) = W[x];
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (f + v < dk) a.W_out[state + f + v] = W[x][v];
+            }
+        }
+}
+
+template <typename TIO, int DK>
+hipError_t prepare_as(const DeltaPass& p, bool backward, hipStream_t s)
+{
+    const unsigned grid = (unsigned)((size_t)p.heads * p.chunks);
+    if (backward) delta_prepare_kernel<TIO, DK, true><<<grid, 256, 0, s>>>(p);
+    else delta_prepare_kernel<TIO, DK, false><<<grid, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename TIO, int DK>
+hipError_t chain_as(const DeltaPass& p, bool save, hipStream_t s)
+{
+    const unsigned grid = (unsigned)(p.heads * ((p.dvp + 63) / 64));
+    if (save) delta_chain_kernel<TIO, DK, true><<<grid, 256, 0, s>>>(p);
+    else delta_chain_kernel<TIO, DK, false><<<grid, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+constexpr size_t kPassBytes = (size_t)1 << 30;   // of workspace, where one head needs no more
+
+struct Plan {
+    int chunks, groups;      // groups of heads that share keys, in one pass
+    size_t records, S, P, bytes;
+};
+
+Plan fwd_plan(int B, int H, int Hk, int T)
+{
+    Plan p;
+    p.chunks = (T + kChunk - 1) / kChunk;
+    const size_t unit = (size_t)p.chunks * (H / Hk);
+    const size_t one = unit * (sizeof(Record) + 2 * kFrags * sizeof(Frag));
+    p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
+    p.records = 0;
+    p.S = up256(unit * p.groups * sizeof(Record));
+    p.P = p.S + up256(unit * p.groups * kFrags * sizeof(Frag));
+    p.bytes = p.P + up256(unit * p.groups * kFrags * sizeof(Frag));
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_delta_prepare(const DeltaPass& p, bool backward, hipStream_t s)
+{
+    const int DK = delta_padded_dk(p.f.dk);
+    if (p.f.bf16)
+        return DK == 32 ? prepare_as<uint16_t, 32>(p, backward, s)
+             : DK == 64 ? prepare_as<uint16_t, 64>(p, backward, s)
+                        : prepare_as<uint16_t, 128>(p, backward, s);
+    return DK == 32 ? prepare_as<float, 32>(p, backward, s)
+         : DK == 64 ? prepare_as<float, 64>(p, backward, s)
+                    : prepare_as<float, 128>(p, backward, s);
+}
+
+hipError_t launch_delta_chain(const DeltaPass& p, bool save, hipStream_t s)
+{
+    const int DK = delta_padded_dk(p.f.dk);
+    if (p.f.bf16)
+        return DK == 32 ? chain_as<uint16_t, 32>(p, save, s)
+             : DK == 64 ? chain_as<uint16_t, 64>(p, save, s)
+                        : chain_as<uint16_t, 128>(p, save, s);
+    return DK == 32 ? chain_as<float, 32>(p, save, s)
+         : DK == 64 ? chain_as<float, 64>(p, save, s)
+                    : chain_as<float, 128>(p, save, s);
+}
+
+size_t delta_fwd_workspace(int B, int H, int Hk, int T, int, int, bool)
+{
+    return fwd_plan(B, H, Hk, T).bytes;
+}
+
+hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
+{
+    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T);
+    char* ws = (char*)a.workspace;
+    DeltaPass p = {};
+    p.f = a;
+    p.chunks = plan.chunks;
+    p.dvp = (a.dv + 31) / 32 * 32;
+    p.records = (Record*)(ws + plan.records);
+    p.S = (Frag*)(ws + plan.S);
+    p.P = (Frag*)(ws + plan.P);
+    const int share = a.H / a.Hk, all = a.B * a.Hk;
+    for (int first = 0; first < all; first += plan.groups) {
+        p.head0 = first * share;
+        p.heads = std::min(plan.groups, all - first) * share;
+        hipError_t e = launch_delta_prepare(p, false, s);
+        if (e == hipSuccess) e = launch_delta_chain(p, false, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t s)
+{
+    const int parts = (a.dv + 15) / 16;
+    const unsigned grid = (unsigned)(a.B * a.H * parts);
+    if (a.bf16) {
+        if (a.dk <= 64) delta_step_kernel<uint16_t, 1><<<grid, 256, 0, s>>>(a, parts);
+        else delta_step_kernel<uint16_t, 2><<<grid, 256, 0, s>>>(a, parts);
+    } else {
+        if (a.dk <= 64) delta_step_kernel<float, 1><<<grid, 256, 0, s>>>(a, parts);
+        else delta_step_kernel<float, 2><<<grid, 256, 0, s>>>(a, parts);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ttt

@@ -1,0 +1,471 @@
+// Gated delta rule: backward pass by chunks of 64 tokens (delta_common.h has the formulas).
+//
+// The forward scan is run again and keeps every chunk's first state and U; a second scan
+// carries the state's gradient D from the last chunk to the first, a wave for 16 columns of
+// values as in the forward pass; the gradients of keys, queries, step sizes and decays then
+// follow chunk by chunk, all chunks at once.  Every sum has a fixed order: the same bits on
+// every call.
+//
+// The decay's gradient is the product of D and the state across the token, that is of all
+// that is read from token t on with all that was written before it.  Within a chunk, with
+// row t of dQ, of the part of dK that reads (from R) and of the part that writes,
+//   dg_t = sum over s >= t of (q_s.dQ_s + k_s.dKread_s - k_s.dKwrite_s) + <D, W'> at the end.
+#include <algorithm>
+
+#include "delta_common.h"
+
+namespace ttt {
+namespace {
+
+struct BwdPass {
+    DeltaPass p;
+    DeltaBwdArgs a;
+};
+
+// ---- the scan from the last chunk to the first ---------------------------------------
+template <typename TIO, int DK>
+__global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
+{
+    constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
+    const DeltaPass& a = q_.p;
+    __shared__ __align__(16) Tile<TIO, DK> tk[2];
+    __shared__ __align__(16) Tile<TIO, DK> tq[2];
+
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
+    const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
+    const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
+    const int col = 64 * (blockIdx.x % parts) + 16 * w + c;
+    const bool works = 64 * (int)(blockIdx.x % parts) + 16 * w < a.dvp;
+    const bool whole = dk % kGran<TIO> == 0;
+    const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
+    const Rows<TIO> dV((TIO*)q_.a.dV, b, h, a.f.H, T, dv, a.f.tokens_first);
+    const size_t state = (size_t)head * dv * dk;
+
+    f32x4 D[M], zn[4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        D[m] = load_state(q_.a.dW_T ? q_.a.dW_T + state : nullptr, col, 16 * m + 4 * g, dv, dk);
+    const int last = a.chunks - 1;
+    TileLoad<TIO, DK> lk, lq;
+    lk.load(K, last * kChunk, T, dk, whole, tid);
+    lq.load(Q, last * kChunk, T, dk, whole, tid);
+    lk.put(tk[last & 1], tid);
+    lq.put(tq[last & 1], tid);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zn[i] = load_cl(dZ, last * kChunk, T, i, g, col, dv);
+    __syncthreads();
+
+    for (int n = last; n >= 0; --n) {
+        const int t0 = n * kChunk, next = t0 - kChunk;
+        const size_t unit = (size_t)local * a.chunks + n;
+        const Tile<TIO, DK>& k = tk[n & 1];
+        const Tile<TIO, DK>& q = tq[n & 1];
+        f32x4 z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = zn[i];
+        if (n > 0) {
+            lk.load(K, next, T, dk, whole, tid);
+            lq.load(Q, next, T, dk, whole, tid);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) zn[i] = load_cl(dZ, next, T, i, g, col, dv);
+        }
+        if (works) {
+            const Record& rec = a.records[unit];
+            f32x4 start[4], eta[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                start[i] = *reinterpret_cast<const f32x4*>(rec.start + 16 * i + 4 * g);
+                eta[i] = *reinterpret_cast<const f32x4*>(rec.eta + 16 * i + 4 * g);
+            }
+            const float all = rec.start[kChunk - 1];
+            const Frag* ft = a.St + unit * kFrags;
+            const Frag* fp = a.P + unit * kFrags;
+
+            float* out = a.cotangents + unit * DK * a.dvp + col;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[(size_t)(16 * m + 4 * g + e) * a.dvp] = D[m][e];
+
+            f32x4 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = mma(by_token(k, i, j, lane), dp, f[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] *= *reinterpret_cast<const f32x4*>(rec.end + 16 * i + 4 * g);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const Parts<NP> zp = split<NP>(z[2 * j], z[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j >= i / 2) f[i] = mma(load_frag<3>(fp[frag_upper(i, j)], lane), zp, f[i]);
+            }
+            Parts<3> x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = split<3>(-(eta[2 * j] * f[2 * j]), -(eta[2 * j + 1] * f[2 * j + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (j >= i / 2) f[i] = mma(load_frag<3>(ft[frag_upper(i, j)], lane), x[j], f[i]);
+
+            float* F = a.F + unit * kChunk * a.dvp + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) F[(size_t)(16 * i + 4 * g + e) * a.dvp] = f[i][e];
+                f[i] *= eta[i];
+                store_cl(dV, t0, T, i, g, col, dv, f[i]);
+                f[i] *= -start[i];
+                z[i] *= start[i];
+            }
+            Parts<3> y[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[j] = split<3>(f[2 * j], f[2 * j + 1]);
+                y[j] = split<3>(z[2 * j], z[2 * j + 1]);
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                D[m] *= all;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    D[m] = mma(by_feature(k, m, j, lane), x[j], D[m]);
+                    D[m] = mma(by_feature(q, m, j, lane), y[j], D[m]);
+                }
+            }
+        }
+        if (n > 0) {
+            lk.put(tk[(n - 1) & 1], tid);
+            lq.put(tq[(n - 1) & 1], tid);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        store_state(q_.a.dW0 ? q_.a.dW0 + state : nullptr, col, 16 * m + 4 * g, dv, dk, D[m]);
+}
+
+// ---- gradients of a chunk ------------------------------------------------------------
+// One workgroup of four waves per chunk and head of keys, going through the heads of values
+// that share it.  Wave w has the gradients of tokens 16 w .. 16 w + 15, transposed: tokens
+// in the lanes, features down the result tiles.  The 64 x 64 products over the columns
+// (dZ u^T and dV u^T, both ways up) come out as operands of what follows, as they lie.
+template <typename TIO, int DK>
+__global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
+{
+    constexpr int NP = kParts<TIO>, M = DK / 16;
+    const DeltaPass& a = q_.p;
+    __shared__ __align__(16) Tile<TIO, DK> tk;
+    __shared__ __align__(16) Tile<TIO, DK> tq;
+    __shared__ double G[kChunk], across[4];
+    __shared__ int cuts[kChunk];
+    __shared__ float eta[kChunk], start[kChunk], end[kChunk], dG[kChunk];
+
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int share = a.f.H / a.f.Hk, chunk = blockIdx.x % a.chunks, group = blockIdx.x / a.chunks;
+    const int key = a.head0 / share + group, b = key / a.f.Hk, hk = key % a.f.Hk;
+    const int T = a.f.T, dk = a.f.dk, dv = a.f.dv, dvp = a.dvp, t0 = chunk * kChunk;
+    const int own = 16 * w + c;
+    const bool whole = dk % kGran<TIO> == 0, fours = dv % 4 == 0;
+    {
+        TileLoad<TIO, DK> lk, lq;
+        const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        lk.load(K, t0, T, dk, whole, tid);
+        lq.load(Q, t0, T, dk, whole, tid);
+        lk.put(tk, tid);
+        lq.put(tq, tid);
+    }
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 sumq[M], sumk[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) sumq[m] = sumk[m] = zero;
+
+    for (int r = 0; r < share; ++r) {
+        const int local = group * share + r, h = hk * share + r;
+        const size_t unit = (size_t)local * a.chunks + chunk;
+        const Record& rec = a.records[unit];
+        __syncthreads();
+        if (tid < kChunk) {
+            G[tid] = rec.G[tid];
+            cuts[tid] = rec.cuts[tid];
+            eta[tid] = rec.eta[tid];
+            start[tid] = rec.start[tid];
+            end[tid] = rec.end[tid];
+        }
+        __syncthreads();
+        const float* U = a.U + unit * kChunk * dvp;
+        const float* F = a.F + unit * kChunk * dvp;
+        const float* W0 = a.states + unit * DK * dvp;
+        const float* D = a.cotangents + unit * DK * dvp;
+        const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
+
+        // rows `row` of a [.., dvp] fp32 plane as an operand over the columns 32 j ..
+        auto plane = [&](const float* X, int row, int j, float by) {
+            const float* p = X + (size_t)row * dvp + 32 * j + 4 * g;
+            return split<3>(by * *reinterpret_cast<const f32x4*>(p),
+                            by * *reinterpret_cast<const f32x4*>(p + 16));
+        };
+        auto four = [&](int t, int f) {   // of dZ
+            f32x4 x = zero;
+            if (t0 + t >= T) return x;
+            const TIO* p = dZ.at(t0 + t) + f;
+            if (fours) {
+                if (f < dv) {
+                    if constexpr (sizeof(TIO) == 2) x = widen4(*reinterpret_cast<const u32x2*>(p));
+                    else x = *reinterpret_cast<const f32x4*>(p);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (f + e < dv) x[e] = load1(p + e);
+            }
+            return x;
+        };
+        auto zrow = [&](int t, int j) {
+            return split<NP>(four(t, 32 * j + 4 * g), four(t, 32 * j + 16 + 4 * g));
+        };
+
+        f32x4 p[4], pt[4], l[4], lt[4], aw[M], av[M], ad[M];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = pt[i] = l[i] = lt[i] = zero;
+#pragma unroll
+        for (int m = 0; m < M; ++m) aw[m] = av[m] = ad[m] = zero;
+        float de = 0.f;
+        const float eo = eta[own];
+        for (int j = 0; j < dvp / 32; ++j) {
+            {
+                const float* x = U + (size_t)own * dvp + 32 * j + 4 * g;
+                const float* y = F + (size_t)own * dvp + 32 * j + 4 * g;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) de = fmaf(x[e], y[e], fmaf(x[16 + e], y[16 + e], de));
+            }
+            const Parts<3> uo = plane(U, own, j, eo), vo = plane(F, own, j, eo);
+            const Parts<NP> zo = zrow(own, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * i + c;
+                if (i <= w) {
+                    const Parts<3> u = plane(U, row, j, eta[row]);
+                    pt[i] = mma(u, zo, pt[i]);
+                    lt[i] = mma(u, vo, lt[i]);
+                }
+                if (i >= w) {
+                    p[i] = mma(zrow(row, j), uo, p[i]);
+                    l[i] = mma(plane(F, row, j, eta[row]), uo, l[i]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const Parts<3> s = plane(W0, 16 * m + c, j, 1.f);
+                aw[m] = mma(s, zo, aw[m]);
+                av[m] = mma(s, vo, av[m]);
+                ad[m] = mma(plane(D, 16 * m + c, j, 1.f), uo, ad[m]);
+            }
+        }
+        // pt, lt: rows s, column t = own; p, l: rows t, column s = own
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * i + 4 * g + e;
+                const float before = row <= own ? pair_decay(G, cuts, own, row) : 0.f;
+                const float after = row >= own ? pair_decay(G, cuts, row, own) : 0.f;
+                pt[i][e] = row <= own ? pt[i][e] * before : 0.f;
+                lt[i][e] = row < own ? -lt[i][e] * before : 0.f;
+                p[i][e] = row >= own ? p[i][e] * after : 0.f;
+                l[i][e] = row > own ? -l[i][e] * after : 0.f;
+            }
+        float wrote = 0.f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            aw[m] *= start[own];
+            av[m] *= -start[own];
+            ad[m] *= end[own];
+            const f32x4 k4 = token4(tk, own, 16 * m + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wrote = fmaf(k4[e], ad[m][e], wrote);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (2 * j <= w) {
+                const Parts<3> x = split<3>(pt[2 * j], pt[2 * j + 1]), y = split<3>(lt[2 * j], lt[2 * j + 1]);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const Parts<NP> kf = by_feature(tk, m, j, lane);
+                    aw[m] = mma(kf, x, aw[m]);
+                    av[m] = mma(kf, y, av[m]);
+                }
+            }
+            if (2 * j + 1 >= w) {
+                const Parts<3> x = split<3>(p[2 * j], p[2 * j + 1]), y = split<3>(l[2 * j], l[2 * j + 1]);
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    ad[m] = mma(by_feature(tq, m, j, lane), x, ad[m]);
+                    ad[m] = mma(by_feature(tk, m, j, lane), y, ad[m]);
+                }
+            }
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const f32x4 k4 = token4(tk, own, 16 * m + 4 * g), q4 = token4(tq, own, 16 * m + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum = fmaf(q4[e], aw[m][e], fmaf(k4[e], av[m][e] - ad[m][e], sum));
+            sumq[m] += aw[m];
+            sumk[m] += av[m] + ad[m];
+        }
+        // <D, W'> = start_C <D, W> + sum of k_s.(written part of dK_s)
+        float kept = 0.f;
+        for (int e = tid; e < DK * dvp; e += 256) kept = fmaf(D[e], W0[e], kept);
+        double cross = (double)kept * start[kChunk - 1] + wrote;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) cross += __shfl_xor(cross, o, 64);
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        de += __shfl_xor(de, 16, 64);
+        de += __shfl_xor(de, 32, 64);
+        if (g == 0) {
+            dG[own] = sum;
+            const Rows<float> o(q_.a.deta, b, h, a.f.H, T, 1, a.f.tokens_first);
+            if (q_.a.deta && t0 + own < T) *o.at(t0 + own) = de;
+        }
+        if (lane == 0) across[w] = cross;
+        __syncthreads();
+        if (w == 0 && q_.a.dg) {
+            double y = dG[lane];
+            for (int o = 1; o < 64; o <<= 1) {
+                const double z = __shfl_down(y, o, 64);
+                if (lane + o < 64) y += z;
+            }
+            y += across[0] + across[1] + across[2] + across[3];
+            const bool forgets = cuts[lane] != (lane ? cuts[lane - 1] : 0);
+            const Rows<float> o(q_.a.dg, b, h, a.f.H, T, 1, a.f.tokens_first);
+            if (t0 + lane < T) *o.at(t0 + lane) = forgets ? 0.f : (float)y;
+        }
+    }
+    if (t0 + own < T) {
+        const Rows<TIO> dQ((TIO*)q_.a.dQ, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<TIO> dK((TIO*)q_.a.dK, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        auto put = [&](TIO* row, int f, f32x4 x) {
+            if (dk % 4 == 0) {
+                if (f < dk) {
+                    if constexpr (sizeof(TIO) == 2) *reinterpret_cast<u32x2*>(row + f) = pack_bf16x4(x);
+                    else *reinterpret_cast<f32x4*>(row + f) = x;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (f + e < dk) store1(row + f + e, x[e]);
+            }
+        };
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            put(dQ.at(t0 + own), 16 * m + 4 * g, sumq[m]);
+            put(dK.at(t0 + own), 16 * m + 4 * g, sumk[m]);
+        }
+    }
+}
+
+template <typename TIO, int DK>
+hipError_t reverse_and_grads(const BwdPass& q, hipStream_t s)
+{
+    const DeltaPass& p = q.p;
+    delta_reverse_kernel<TIO, DK><<<(unsigned)(p.heads * ((p.dvp + 63) / 64)), 256, 0, s>>>(q);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const size_t groups = p.heads / (p.f.H / p.f.Hk);
+    delta_grads_kernel<TIO, DK><<<(unsigned)(groups * p.chunks), 256, 0, s>>>(q);
+    return hipGetLastError();
+}
+
+constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+constexpr size_t kPassBytes = (size_t)4 << 30;
+
+struct Plan {
+    int chunks, groups, dvp;
+    size_t S, St, P, states, cotangents, U, F, bytes;
+};
+
+Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
+{
+    Plan p;
+    p.chunks = (T + kChunk - 1) / kChunk;
+    p.dvp = (dv + 31) / 32 * 32;
+    const size_t unit = (size_t)p.chunks * (H / Hk), DK = delta_padded_dk(dk);
+    const size_t state = 4 * DK * p.dvp, rows = 4 * (size_t)kChunk * p.dvp, frags = kFrags * sizeof(Frag);
+    const size_t one = unit * (sizeof(Record) + 3 * frags + 2 * state + 2 * rows);
+    p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
+    const size_t units = unit * p.groups;
+    p.S = up256(units * sizeof(Record));
+    p.St = p.S + up256(units * frags);
+    p.P = p.St + up256(units * frags);
+    p.states = p.P + up256(units * frags);
+    p.cotangents = p.states + up256(units * state);
+    p.U = p.cotangents + up256(units * state);
+    p.F = p.U + up256(units * rows);
+    p.bytes = p.F + up256(units * rows);
+    return p;
+}
+
+}  // namespace
+
+size_t delta_bwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool)
+{
+    return bwd_plan(B, H, Hk, T, dk, dv).bytes;
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
+{
+    const DeltaArgs& f = a.f;
+    const Plan plan = bwd_plan(f.B, f.H, f.Hk, f.T, f.dk, f.dv);
+    char* ws = (char*)f.workspace;
+    BwdPass q = {};
+    q.a = a;
+    DeltaPass& p = q.p;
+    p.f = f;
+    p.chunks = plan.chunks;
+    p.dvp = plan.dvp;
+    p.records = (Record*)ws;
+    p.S = (Frag*)(ws + plan.S);
+    p.St = (Frag*)(ws + plan.St);
+    p.P = (Frag*)(ws + plan.P);
+    p.states = (float*)(ws + plan.states);
+    p.cotangents = (float*)(ws + plan.cotangents);
+    p.U = (float*)(ws + plan.U);
+    p.F = (float*)(ws + plan.F);
+    const int share = f.H / f.Hk, all = f.B * f.Hk, DK = delta_padded_dk(f.dk);
+    for (int first = 0; first < all; first += plan.groups) {
+        p.head0 = first * share;
+        p.heads = std::min(plan.groups, all - first) * share;
+        hipError_t e = launch_delta_prepare(p, true, s);
+        if (e == hipSuccess) e = launch_delta_chain(p, true, s);
+        if (e != hipSuccess) return e;
+        if (f.bf16)
+            e = DK == 32 ? reverse_and_grads<uint16_t, 32>(q, s)
+              : DK == 64 ? reverse_and_grads<uint16_t, 64>(q, s)
+                         : reverse_and_grads<uint16_t, 128>(q, s);
+        else
+            e = DK == 32 ? reverse_and_grads<float, 32>(q, s)
+              : DK == 64 ? reverse_and_grads<float, 64>(q, s)
+                         : reverse_and_grads<float, 128>(q, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace ttt

@@ -1,0 +1,283 @@
+// Shared pieces of the gated delta rule's kernels: chunk geometry, products of values
+// split into bf16 parts, the LDS tiles of keys and queries, and the workspace's records.
+//
+// A chunk is 64 tokens.  With G_t the sum of the log decays from the chunk's start
+// through t, E_ts = exp(G_t - G_s), W the state at the chunk's start and
+//   L_ts = E_ts k_t.k_s (s < t),   P_ts = E_ts q_t.k_s (s <= t),
+//   S = (I + L diag(eta))^-1 L     (strictly lower, so (I + L diag(eta))^-1 = I - S diag(eta)
+//                                   and (I + diag(eta) L)^-1 = I - diag(eta) S),
+// the forward pass of a chunk is
+//   R = V - exp(G) K W^T,   U = R - S (eta R),   u = eta U,
+//   Z = exp(G) Q W^T + P u,   W' = exp(G_C) W + (exp(G_C - G) u)^T K
+// and its adjoint, with D the gradient that reaches W',
+//   dU = P^T dZ + exp(G_C - G) K D^T,   F = dU - S^T (eta dU),   dV = eta F,
+//   D' = exp(G_C) D + (exp(G) dZ)^T Q - (exp(G) dV)^T K.
+// Nothing is divided by eta, so eta = 0 needs no case of its own.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_launch.h"
+#include "device_common.h"
+#include "mfma_common.h"
+
+namespace ttt {
+
+constexpr int kChunk = 64;
+constexpr float kForget = -1e30f;     // log decays from here down forget everything
+
+typedef uint32_t quad __attribute__((ext_vector_type(4)));
+
+// ---- values as sums of bf16 parts ----------------------------------------
+// An fp32 operand of a product is the exact sum of three bf16 parts (8 + 8 + 8 bits);
+// a bf16 input is one part.  Products of parts are exact in the matrix cores' fp32 sums,
+// and those below 2^-24 of the whole are left out: one part by three takes 3
+// instructions, three by three 6, against 16 times the time of one for the fp32 form.
+template <int N> struct Parts { u32x4 p[N]; };
+
+__device__ __forceinline__ f32x4 widen4(u32x2 v)
+{
+    return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                 __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+}
+
+// slots 0..3 from a, 4..7 from b
+template <int N>
+__device__ __forceinline__ Parts<N> split(f32x4 a, f32x4 b)
+{
+    Parts<N> r;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        r.p[k] = pack_bf16x8(a, b);
+        if (k + 1 < N) {
+            a -= widen4(lo_half(r.p[k]));
+            b -= widen4(hi_half(r.p[k]));
+        }
+    }
+    return r;
+}
+
+// c + a b over 32 contraction slots, part products of order up to O (2: fp32's accuracy,
+// 1: about 2^-17), the smallest first
+template <int O = 2, int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32x4 c)
+{
+#pragma unroll
+    for (int s = O; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < NB) c = mfma32(a.p[i], b.p[j], c);
+        }
+    return c;
+}
+
+template <typename TIO> constexpr int kParts = sizeof(TIO) == 2 ? 1 : 3;
+
+// ---- token tensors ---------------------------------------------------------
+// rows of one (batch, head) of [B, H, T, d] or [B, T, H, d]
+template <typename TIO>
+struct Rows {
+    TIO* p;
+    size_t stride;     // elements from token to token
+    __device__ __forceinline__ Rows(TIO* base, int b, int h, int H, int T, int d, bool tokens_first)
+        : p(base + (tokens_first ? ((size_t)b * T * H + h) * d : ((size_t)b * H + h) * T * d)),
+          stride(tokens_first ? (size_t)H * d : (size_t)d)
+    {
+    }
+    __device__ __forceinline__ TIO* at(int t) const { return p + (size_t)t * stride; }
+};
+
+template <typename TIO> constexpr int kGran = 16 / (int)sizeof(TIO);   // elements of 16 bytes
+
+// 16 bytes of row `row` from column `col` (columns past d are 0); `whole`: rows are
+// multiples of 16 bytes
+template <typename TIO>
+__device__ __forceinline__ quad load_granule(const TIO* row, int col, int d, bool whole)
+{
+    quad q = {0u, 0u, 0u, 0u};
+    if (whole) {
+        if (col < d) q = *reinterpret_cast<const quad*>(row + col);
+        return q;
+    }
+#pragma unroll
+    for (int i = 0; i < kGran<TIO>; ++i)
+        if (col + i < d) {
+            if constexpr (sizeof(TIO) == 4) q[i] = reinterpret_cast<const uint32_t*>(row)[col + i];
+            else q[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[col + i] << (16 * (i & 1));
+        }
+    return q;
+}
+
+// ---- LDS tile of 64 tokens by DK features, rows padded by 16 bytes ----------
+template <typename TIO, int DK>
+struct Tile {
+    static constexpr int LD = DK + kGran<TIO>;
+    static constexpr int GRANULES = kChunk * DK / kGran<TIO>;
+    TIO x[kChunk * LD];
+};
+
+// a tile on its way from memory: each of 256 threads holds its granules
+template <typename TIO, int DK>
+struct TileLoad {
+    static constexpr int N = Tile<TIO, DK>::GRANULES / 256;
+    static constexpr int ROW = DK / kGran<TIO>;
+    quad q[N];
+    __device__ __forceinline__ void load(const Rows<const TIO>& src, int t0, int T, int d, bool whole,
+                                         int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = tid + 256 * i, r = e / ROW, col = (e % ROW) * kGran<TIO>;
+            q[i] = t0 + r < T ? load_granule(src.at(t0 + r), col, d, whole) : quad{0u, 0u, 0u, 0u};
+        }
+    }
+    __device__ __forceinline__ void put(Tile<TIO, DK>& to, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = tid + 256 * i, r = e / ROW, col = (e % ROW) * kGran<TIO>;
+            *reinterpret_cast<quad*>(to.x + r * Tile<TIO, DK>::LD + col) = q[i];
+        }
+    }
+};
+
+// Operand with the tile's token 16 i + c in the lane and features in the slots: slots
+// 0..3 are features 32 j + 4 g + v, 4..7 are 32 j + 16 + 4 g + v (the order in which two
+// result tiles, one above the other, are an operand).
+template <typename TIO, int DK>
+__device__ __forceinline__ Parts<kParts<TIO>> by_token(const Tile<TIO, DK>& t, int i, int j, int lane)
+{
+    const TIO* row = t.x + (16 * i + (lane & 15)) * Tile<TIO, DK>::LD + 32 * j + 4 * (lane >> 4);
+    if constexpr (sizeof(TIO) == 2) {
+        const u32x2 a = *reinterpret_cast<const u32x2*>(row);
+        const u32x2 b = *reinterpret_cast<const u32x2*>(row + 16);
+        return Parts<1>{{u32x4{a.x, a.y, b.x, b.y}}};
+    } else {
+        return split<3>(*reinterpret_cast<const f32x4*>(row), *reinterpret_cast<const f32x4*>(row + 16));
+    }
+}
+
+// Operand with feature 16 m + c in the lane and tokens in the slots: 32 j + 4 g + v and
+// 32 j + 16 + 4 g + v.  (bf16: by the transposing LDS read, see lds_transpose16)
+template <typename TIO, int DK>
+__device__ __forceinline__ Parts<kParts<TIO>> by_feature(const Tile<TIO, DK>& t, int m, int j, int lane)
+{
+    constexpr int LD = Tile<TIO, DK>::LD;
+    const int c = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(TIO) == 2) {
+        auto at = [&](int token) {
+            auto p = (__attribute__((address_space(3))) s16x4*)(t.x + (token + (c >> 2)) * LD + 16 * m +
+                                                                4 * (c & 3));
+            return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+        };
+        const u32x2 a = at(32 * j + 4 * g), b = at(32 * j + 16 + 4 * g);
+        return Parts<1>{{u32x4{a.x, a.y, b.x, b.y}}};
+    } else {
+        const TIO* p = t.x + (32 * j + 4 * g) * LD + 16 * m + c;
+        const f32x4 a = {p[0], p[LD], p[2 * LD], p[3 * LD]};
+        p += 16 * LD;
+        return split<3>(a, f32x4{p[0], p[LD], p[2 * LD], p[3 * LD]});
+    }
+}
+
+// four consecutive features of one token, widened
+template <typename TIO, int DK>
+__device__ __forceinline__ f32x4 token4(const Tile<TIO, DK>& t, int token, int feature)
+{
+    const TIO* p = t.x + token * Tile<TIO, DK>::LD + feature;
+    if constexpr (sizeof(TIO) == 2) return widen4(*reinterpret_cast<const u32x2*>(p));
+    else return *reinterpret_cast<const f32x4*>(p);
+}
+
+// ---- what the preparing kernel leaves for a (head, chunk) -------------------
+// the 6 operands of a lower triangular 64 x 64 matrix that are not zero: row tile i
+// against the token pair of tiles (2 j, 2 j + 1), j <= i / 2; of its transpose, j >= i / 2
+constexpr int kFrags = 6;
+__host__ __device__ constexpr int frag_lower(int i, int j) { return i < 2 ? i : 2 * (i - 1) + j; }
+__host__ __device__ constexpr int frag_upper(int i, int j) { return i < 2 ? 2 * i + j : i + 2; }
+
+struct Frag { u32x4 p[3][64]; };              // parts by lanes, 3 KB
+struct Record {                               // decays of a chunk's tokens
+    double G[kChunk];                         // sums of the log decays, those that forget left out
+    int cuts[kChunk];                         // how many forget, up to and with the token
+    float eta[kChunk];
+    float start[kChunk];                      // decay from the chunk's start through the token
+    float end[kChunk];                        // decay from after the token to the chunk's end
+};
+
+__device__ __forceinline__ float pair_decay(const double* G, const int* cuts, int t, int s)
+{
+    return cuts[t] == cuts[s] ? expf((float)(G[t] - G[s])) : 0.f;
+}
+
+__device__ __forceinline__ void store_frag(Frag& f, int lane, f32x4 a, f32x4 b)
+{
+    const Parts<3> s = split<3>(a, b);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) f.p[k][lane] = s.p[k];
+}
+
+template <int N>
+__device__ __forceinline__ Parts<N> load_frag(const Frag& f, int lane)
+{
+    Parts<N> r;
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.p[k] = f.p[k][lane];
+    return r;
+}
+
+// ---- one element of the I/O type at CL positions ----------------------------
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v)
+{
+    *p = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+}
+
+// result tile i of a chunk (tokens 16 i + 4 g + v, column `col`): from and to rows of d columns
+template <typename TIO>
+__device__ __forceinline__ f32x4 load_cl(const Rows<const TIO>& src, int t0, int T, int i, int g, int col,
+                                         int d)
+{
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int t = t0 + 16 * i + 4 * g + v;
+        if (t < T && col < d) r[v] = load1(src.at(t) + col);
+    }
+    return r;
+}
+
+template <typename TIO>
+__device__ __forceinline__ void store_cl(const Rows<TIO>& dst, int t0, int T, int i, int g, int col, int d,
+                                         f32x4 r)
+{
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int t = t0 + 16 * i + 4 * g + v;
+        if (t < T && col < d) store1(dst.at(t) + col, r[v]);
+    }
+}
+
+// state [dv, dk] fp32, row `col`, features 16 m + 4 g + v
+__device__ __forceinline__ f32x4 load_state(const float* W, int col, int f, int dv, int dk)
+{
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (!W || col >= dv) return r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (f + v < dk) r[v] = W[(size_t)col * dk + f + v];
+    return r;
+}
+
+__device__ __forceinline__ void store_state(float* W, int col, int f, int dv, int dk, f32x4 r)
+{
+    if (!W || col >= dv) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (f + v < dk) W[(size_t)col * dk + f + v] = r[v];
+}
+
+}  // namespace ttt

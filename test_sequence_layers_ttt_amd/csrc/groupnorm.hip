@@ -1,0 +1,659 @@
+// Group norm with an activation over channels-last tensors [N, S, C]:
+//   n = (x - mean) rstd over the S places and the C / G channels of a group,
+//   y = act(n weight + bias),
+// and its gradients:  dv = dy act'(v),  u = dv weight,
+//   dx = rstd (u - mean(u) - n mean(u n)),  dweight = sum of dv n,  dbias = sum of dv.
+//
+// Two forms.  With one place (S = 1: the norm of every head's output of every token) a group
+// is at most 64 lanes' vectors: it stays in registers, every input is read once, and a
+// thread keeps the same channels for all its rows, so weight and bias (and the backward
+// pass's sums) stay in registers too.  Otherwise the places are shared out over the
+// workgroups, each thread with channels of its own: sums per channel first, then a wave per
+// group joins them, then a second read writes the result.
+//
+// Sums run in a fixed order: the same bits on every call.
+#include <algorithm>
+
+#include "block_launch.h"
+#include "device_common.h"
+#include "mfma_common.h"
+#include "ttt.h"
+
+namespace ttt {
+namespace {
+
+// V elements of the I/O type as fp32
+template <typename TIO, int V> struct Vec {
+    RawRow<TIO, V> raw;
+    __device__ __forceinline__ void load(const TIO* p) { raw.load(p); }
+    __device__ __forceinline__ float at(int i) const { return raw.at(i); }
+};
+
+template <typename TIO, int V>
+__device__ __forceinline__ void store_vec(TIO* p, const float (&y)[V])
+{
+    if constexpr (sizeof(TIO) == 4) {
+        if constexpr (V == 4) *reinterpret_cast<f32x4*>(p) = f32x4{y[0], y[1], y[2], y[3]};
+        else if constexpr (V == 2) *reinterpret_cast<f32x2*>(p) = f32x2{y[0], y[1]};
+        else *p = y[0];
+    } else {
+        if constexpr (V == 8)
+            *reinterpret_cast<u32x4*>(p) = pack_bf16x8(f32x4{y[0], y[1], y[2], y[3]}, f32x4{y[4], y[5], y[6], y[7]});
+        else if constexpr (V == 4) *reinterpret_cast<u32x2*>(p) = pack_bf16x4(f32x4{y[0], y[1], y[2], y[3]});
+        else if constexpr (V == 2) *reinterpret_cast<unsigned*>(p) = pack_bf16x2(y[0], y[1]);
+        else *p = (uint16_t)(pack_bf16x2(y[0], 0.f) & 0xffffu);
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act(float v)
+{
+    if constexpr (ACT == TTT_ACT_SILU) return v / (1.f + expf(-v));
+    if constexpr (ACT == TTT_ACT_GELU) return v * (0.5f * erfcf(-0.70710678f * v));
+    return v;
+}
+
+// the derivative
+template <int ACT>
+__device__ __forceinline__ float dact(float v)
+{
+    if constexpr (ACT == TTT_ACT_SILU) {
+        const float y = 1.f / (1.f + expf(-v));
+        return fmaf(v * y, 1.f - y, y);
+    }
+    if constexpr (ACT == TTT_ACT_GELU)
+        return fmaf(v * 0.39894228f, expf(-0.5f * v * v), 0.5f * erfcf(-0.70710678f * v));
+    return 1.f;
+}
+
+// sum over L neighbouring lanes (a power of two), the same bits in each
+template <int L>
+__device__ __forceinline__ float lane_sum(float x)
+{
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) x += __shfl_xor(x, o, 64);
+    return x;
+}
+
+// ---- one place: a group in L lanes, one vector each ------------------------------------
+// slots: rows that a workgroup works on at once (where its 256 threads hold several).
+// block x: 256 threads' worth of channels, y: rows.
+template <int L>
+struct Place {
+    int group, lane, slot;
+    bool in;
+    __device__ __forceinline__ Place(int G, int vectors)
+    {
+        const int per = G * L;     // threads of a row
+        int t = blockIdx.x * 256 + threadIdx.x;
+        slot = 0;
+        if (per < 256) { slot = t / per; t -= slot * per; }
+        group = t / L;
+        lane = t % L;
+        in = group < G && lane < vectors && slot < (per < 256 ? 256 / per : 1);
+    }
+};
+
+template <typename TIO, int V, int L, int ACT>
+__global__ void __launch_bounds__(256) group_row_fwd_kernel(GroupArgs a, int slots)
+{
+    const int per = a.C / a.G, vectors = per / V;
+    const Place<L> p(a.G, vectors);
+    const int ch = p.group * per + p.lane * V;
+    float w[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        w[i] = p.in && a.weight ? a.weight[ch + i] : 1.f;
+        b[i] = p.in && a.bias ? a.bias[ch + i] : 0.f;
+    }
+    const TIO* X = (const TIO*)a.X;
+    TIO* Y = (TIO*)a.Y;
+    const float inv = 1.f / (float)per;
+    const long long step = (long long)gridDim.y * slots;
+    // (every lane goes through the same rows: the sums are over all lanes)
+    for (long long r0 = (long long)blockIdx.y * slots; r0 < a.N; r0 += step) {
+        const long long row = r0 + p.slot;
+        const bool in = p.in && row < a.N;
+        Vec<TIO, V> x;
+        float v[V], s = 0.f;
+        if (in) x.load(X + row * a.C + ch);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += v[i] = in ? x.at(i) : 0.f;
+        const float mean = lane_sum<L>(s) * inv;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] -= mean;
+            s = in ? fmaf(v[i], v[i], s) : 0.f;
+        }
+        const float rstd = 1.f / sqrtf(fmaf(lane_sum<L>(s), inv, a.eps));
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = act<ACT>(fmaf(v[i] * rstd, w[i], b[i]));
+            store_vec<TIO, V>(Y + row * a.C + ch, v);
+            if (p.lane == 0) {
+                a.mean[row * a.G + p.group] = mean;
+                a.rstd[row * a.G + p.group] = rstd;
+            }
+        }
+    }
+}
+
+// the sums for dweight and dbias go to planes [2][C], one for each (block y, slot)
+template <typename TIO, int V, int L, int ACT>
+__global__ void __launch_bounds__(256) group_row_bwd_kernel(GroupBwdArgs a, int slots, float* planes)
+{
+    const int per = a.C / a.G, vectors = per / V;
+    const Place<L> p(a.G, vectors);
+    const int ch = p.group * per + p.lane * V;
+    float w[V], b[V], sw[V], sb[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        w[i] = p.in && a.weight ? a.weight[ch + i] : 1.f;
+        b[i] = p.in && a.bias ? a.bias[ch + i] : 0.f;
+        sw[i] = sb[i] = 0.f;
+    }
+    const TIO* X = (const TIO*)a.X;
+    const TIO* dY = (const TIO*)a.dY;
+    TIO* dX = (TIO*)a.dX;
+    const float inv = 1.f / (float)per;
+    const long long step = (long long)gridDim.y * slots;
+    for (long long r0 = (long long)blockIdx.y * slots; r0 < a.N; r0 += step) {
+        const long long row = r0 + p.slot;
+        const bool in = p.in && row < a.N;
+        Vec<TIO, V> x, dy;
+        float n[V], u[V], s1 = 0.f, s2 = 0.f, mean = 0.f, rstd = 0.f;
+        if (in) {
+            x.load(X + row * a.C + ch);
+            dy.load(dY + row * a.C + ch);
+            mean = a.mean[row * a.G + p.group];
+            rstd = a.rstd[row * a.G + p.group];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            n[i] = u[i] = 0.f;
+            if (in) {
+                n[i] = (x.at(i) - mean) * rstd;
+                const float dv = dy.at(i) * dact<ACT>(fmaf(n[i], w[i], b[i]));
+                sw[i] = fmaf(dv, n[i], sw[i]);
+                sb[i] += dv;
+                u[i] = dv * w[i];
+            }
+            s1 += u[i];
+            s2 = fmaf(u[i], n[i], s2);
+        }
+        s1 = lane_sum<L>(s1) * inv;
+        s2 = lane_sum<L>(s2) * inv;
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) u[i] = rstd * (u[i] - fmaf(n[i], s2, s1));
+            store_vec<TIO, V>(dX + row * a.C + ch, u);
+        }
+    }
+    if (planes && p.in) {
+        float* to = planes + ((size_t)blockIdx.y * slots + p.slot) * 2 * a.C + ch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            to[i] = sw[i];
+            to[a.C + i] = sb[i];
+        }
+    }
+}
+
+// dweight and dbias: column c of all planes [2][C], in fp64, 8 runs of planes a column
+__global__ void __launch_bounds__(256) group_planes_kernel(const float* planes, long long count, int C,
+                                                           float* dweight, float* dbias)
+{
+    __shared__ double part[8][32];
+    const int c = threadIdx.x & 31, k = threadIdx.x >> 5, at = blockIdx.x * 32 + c;
+    double s = 0.0;
+    if (at < 2 * C)
+        for (long long i = k; i < count; i += 8) s += planes[i * 2 * C + at];
+    part[k][c] = s;
+    __syncthreads();
+    if (k == 0 && at < 2 * C) {
+        for (int i = 1; i < 8; ++i) s += part[i][c];
+        if (at < C) { if (dweight) dweight[at] = (float)s; }
+        else if (dbias) dbias[at - C] = (float)s;
+    }
+}
+
+// ---- many places: channels in the threads, places over the workgroups --------------------
+// Workgroup (x: row by row 256 threads' worth of vectors of channels, y: places first .. last).
+struct Slab {
+    long long row;
+    int ch, slot, slots;      // channel, place within a step, places a step
+    bool in;
+    long long first, last;
+    __device__ __forceinline__ Slab(int vectors, int V, long long S, int parts)
+    {
+        const int wide = (vectors + 255) / 256;
+        row = blockIdx.x / wide;
+        int t = threadIdx.x, x = (int)(blockIdx.x % wide) * 256;
+        slots = vectors < 256 ? 256 / vectors : 1;
+        slot = 0;
+        if (vectors < 256) { slot = t / vectors; t -= slot * vectors; }
+        ch = (x + t) * V;
+        in = x + t < vectors && slot < slots;
+        const long long each = (S + parts - 1) / parts;
+        first = each * blockIdx.y;
+        last = first + each < S ? first + each : S;
+    }
+};
+
+// (a, b) of each thread's channels joined over the slots, in LDS, slot after slot
+template <int V, typename JOIN>
+__device__ __forceinline__ void over_slots(const Slab& p, int vectors, float (&s)[V], float (&q)[V],
+                                           JOIN join)
+{
+    __shared__ float ls[256][V + 1], lq[256][V + 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) { ls[threadIdx.x][i] = s[i]; lq[threadIdx.x][i] = q[i]; }
+    __syncthreads();
+    if (p.slot == 0 && p.in)
+        for (int k = 1; k < p.slots; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                join(i, k, ls[threadIdx.x + k * vectors][i], lq[threadIdx.x + k * vectors][i]);
+}
+
+// how many of the places first .. last slot k takes
+__device__ __forceinline__ float taken(const Slab& p, int k)
+{
+    const long long n = p.last - p.first - k;
+    return n > 0 ? (float)((n + p.slots - 1) / p.slots) : 0.f;
+}
+
+// (mean, sum of squares about it) of na and nb values joined
+__device__ __forceinline__ void join_moments(float& na, float& mean, float& m2, float nb, float mb, float qb)
+{
+    if (nb == 0.f) return;
+    const float n = na + nb, d = mb - mean, f = nb / n;
+    mean = fmaf(d, f, mean);
+    m2 += fmaf(d * d, na * f, qb);
+    na = n;
+}
+
+// mean and squares about it of every channel over this workgroup's places; sums are taken of
+// the distance to the channel's first value, which keeps the digits of a far mean
+template <typename TIO, int V>
+__global__ void __launch_bounds__(256) group_moments_kernel(GroupArgs a, int parts, float* planes)
+{
+    const int vectors = a.C / V;
+    const Slab p(vectors, V, a.S, parts);
+    const TIO* X = (const TIO*)a.X + p.row * a.S * a.C;
+    float shift[V], s[V], q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) shift[i] = s[i] = q[i] = 0.f;
+    if (p.in && p.first + p.slot < p.last) {
+        Vec<TIO, V> x;
+        x.load(X + (p.first + p.slot) * a.C + p.ch);
+#pragma unroll
+        for (int i = 0; i < V; ++i) shift[i] = x.at(i);
+#pragma unroll 4
+        for (long long t = p.first + p.slot + p.slots; t < p.last; t += p.slots) {
+            Vec<TIO, V> y;
+            y.load(X + t * a.C + p.ch);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float d = y.at(i) - shift[i];
+                s[i] += d;
+                q[i] = fmaf(d, d, q[i]);
+            }
+        }
+    }
+    const float mine = taken(p, p.slot), inv = mine > 0.f ? 1.f / mine : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float d = s[i] * inv;
+        q[i] = fmaxf(q[i] - s[i] * d, q[i] * 0.f);   // (not below 0; NaN stays)
+        s[i] = shift[i] + d;
+    }
+    float n[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) n[i] = mine;
+    over_slots<V>(p, vectors, s, q, [&](int i, int k, float mb, float qb) {
+        join_moments(n[i], s[i], q[i], taken(p, k), mb, qb);
+    });
+    if (p.slot == 0 && p.in) {
+        float* to = planes + ((size_t)p.row * parts + blockIdx.y) * 2 * a.C + p.ch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            to[i] = s[i];
+            to[a.C + i] = q[i];
+        }
+    }
+}
+
+// one wave per (row, group): mean and rstd from its channels' and parts' moments
+__global__ void __launch_bounds__(64) group_statistics_kernel(GroupArgs a, int parts, const float* planes)
+{
+    const long long row = blockIdx.x / a.G;
+    const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
+    const long long each = (a.S + parts - 1) / parts;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    for (long long e = threadIdx.x; e < (long long)parts * per; e += 64) {
+        const int part = (int)(e / per), ch = group * per + (int)(e % per);
+        const long long have = min(each, a.S - each * part);
+        const float* from = planes + ((size_t)row * parts + part) * 2 * a.C + ch;
+        if (have > 0) join_moments(n, mean, m2, (float)have, from[0], from[a.C]);
+    }
+    for (int o = 1; o < 64; o <<= 1) {
+        const float nb = __shfl_down(n, o, 64), mb = __shfl_down(mean, o, 64), qb = __shfl_down(m2, o, 64);
+        join_moments(n, mean, m2, nb, mb, qb);
+    }
+    if (threadIdx.x == 0) {
+        a.mean[blockIdx.x] = mean;
+        a.rstd[blockIdx.x] = 1.f / sqrtf(m2 / n + a.eps);
+    }
+}
+
+template <typename TIO, int V, int ACT>
+__global__ void __launch_bounds__(256) group_apply_kernel(GroupArgs a, int parts)
+{
+    const Slab p(a.C / V, V, a.S, parts);
+    if (!p.in) return;
+    const long long row = p.row;
+    const TIO* X = (const TIO*)a.X + row * a.S * a.C + p.ch;
+    TIO* Y = (TIO*)a.Y + row * a.S * a.C + p.ch;
+    float mean[V], rstd[V], w[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int ch = p.ch + i;
+        const long long g = row * a.G + ch / (a.C / a.G);
+        mean[i] = a.mean[g];
+        rstd[i] = a.rstd[g];
+        w[i] = a.weight ? a.weight[ch] : 1.f;
+        b[i] = a.bias ? a.bias[ch] : 0.f;
+    }
+#pragma unroll 2
+    for (long long t = p.first + p.slot; t < p.last; t += p.slots) {
+        Vec<TIO, V> x;
+        x.load(X + t * a.C);
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = act<ACT>(fmaf((x.at(i) - mean[i]) * rstd[i], w[i], b[i]));
+        store_vec<TIO, V>(Y + t * a.C, y);
+    }
+}
+
+// sums of dv n and dv of every channel over this workgroup's places, to planes [2][C]
+template <typename TIO, int V, int ACT>
+__global__ void __launch_bounds__(256) group_sums_kernel(GroupBwdArgs a, int parts, float* planes)
+{
+    const int vectors = a.C / V;
+    const Slab p(vectors, V, a.S, parts);
+    const long long row = p.row;
+    const TIO* X = (const TIO*)a.X + row * a.S * a.C + p.ch;
+    const TIO* dY = (const TIO*)a.dY + row * a.S * a.C + p.ch;
+    float s[V], q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+    if (p.in) {
+        float mean[V], rstd[V], w[V], b[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int ch = p.ch + i;
+            const long long g = row * a.G + ch / (a.C / a.G);
+            mean[i] = a.mean[g];
+            rstd[i] = a.rstd[g];
+            w[i] = a.weight ? a.weight[ch] : 1.f;
+            b[i] = a.bias ? a.bias[ch] : 0.f;
+        }
+#pragma unroll 2
+        for (long long t = p.first + p.slot; t < p.last; t += p.slots) {
+            Vec<TIO, V> x, dy;
+            x.load(X + t * a.C);
+            dy.load(dY + t * a.C);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float n = (x.at(i) - mean[i]) * rstd[i];
+                const float dv = dy.at(i) * dact<ACT>(fmaf(n, w[i], b[i]));
+                s[i] = fmaf(dv, n, s[i]);
+                q[i] += dv;
+            }
+        }
+    }
+    over_slots<V>(p, vectors, s, q, [&](int i, int, float sb, float qb) {
+        s[i] += sb;
+        q[i] += qb;
+    });
+    if (p.slot == 0 && p.in) {
+        float* to = planes + ((size_t)row * parts + blockIdx.y) * 2 * a.C + p.ch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            to[i] = s[i];
+            to[a.C + i] = q[i];
+        }
+    }
+}
+
+// one wave per (row, group): means of u and u n
+__global__ void __launch_bounds__(64) group_means_kernel(GroupBwdArgs a, int parts, const float* planes,
+                                                         float* means)
+{
+    const long long row = blockIdx.x / a.G;
+    const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
+    double m1 = 0.0, m2 = 0.0;
+    for (long long e = threadIdx.x; e < (long long)parts * per; e += 64) {
+        const int part = (int)(e / per), ch = group * per + (int)(e % per);
+        const float* from = planes + ((size_t)row * parts + part) * 2 * a.C + ch;
+        const double w = a.weight ? a.weight[ch] : 1.f;
+        m2 += w * from[0];
+        m1 += w * from[a.C];
+    }
+    for (int o = 1; o < 64; o <<= 1) {
+        m1 += __shfl_xor(m1, o, 64);
+        m2 += __shfl_xor(m2, o, 64);
+    }
+    if (threadIdx.x == 0) {
+        const double n = (double)a.S * per;
+        means[2 * (size_t)blockIdx.x] = (float)(m1 / n);
+        means[2 * (size_t)blockIdx.x + 1] = (float)(m2 / n);
+    }
+}
+
+template <typename TIO, int V, int ACT>
+__global__ void __launch_bounds__(256) group_dx_kernel(GroupBwdArgs a, int parts, const float* means)
+{
+    const Slab p(a.C / V, V, a.S, parts);
+    if (!p.in) return;
+    const long long row = p.row, at = row * a.S * a.C + p.ch;
+    const TIO* X = (const TIO*)a.X + at;
+    const TIO* dY = (const TIO*)a.dY + at;
+    TIO* dX = (TIO*)a.dX + at;
+    float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int ch = p.ch + i;
+        const long long g = row * a.G + ch / (a.C / a.G);
+        mean[i] = a.mean[g];
+        rstd[i] = a.rstd[g];
+        m1[i] = means[2 * g];
+        m2[i] = means[2 * g + 1];
+        w[i] = a.weight ? a.weight[ch] : 1.f;
+        b[i] = a.bias ? a.bias[ch] : 0.f;
+    }
+#pragma unroll 2
+    for (long long t = p.first + p.slot; t < p.last; t += p.slots) {
+        Vec<TIO, V> x, dy;
+        x.load(X + t * a.C);
+        dy.load(dY + t * a.C);
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float n = (x.at(i) - mean[i]) * rstd[i];
+            const float u = dy.at(i) * dact<ACT>(fmaf(n, w[i], b[i])) * w[i];
+            y[i] = rstd[i] * (u - fmaf(n, m2[i], m1[i]));
+        }
+        store_vec<TIO, V>(dX + t * a.C, y);
+    }
+}
+
+// ---- launch shapes -----------------------------------------------------------------------
+constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// the largest power of two up to 16 bytes that divides n elements
+int vector_of(int n, bool bf16)
+{
+    int v = bf16 ? 8 : 4;
+    while (n % v) v /= 2;
+    return v;
+}
+
+struct Shape {
+    bool rows;               // the form for one place
+    int V, L, x, y, slots;   // vector, lanes of a group, grid, rows a workgroup holds at once
+    int parts;               // workgroups along the places
+    size_t planes;           // of 2 C floats
+};
+
+Shape shape_of(long long N, long long S, int C, int G, bool bf16)
+{
+    Shape h = {};
+    const int per = C / G;
+    const int v = vector_of(per, bf16);
+    if (S == 1 && per / v <= 64) {
+        h.rows = true;
+        h.V = v;
+        h.L = 1;
+        while (h.L < per / v) h.L *= 2;
+        const long long threads = (long long)G * h.L;
+        h.slots = threads < 256 ? (int)(256 / threads) : 1;
+        h.x = (int)((threads + 255) / 256);
+        // workgroups enough to fill the card several times over, and no more planes than that
+        const long long steps = (N + h.slots - 1) / h.slots;
+        h.y = (int)std::min<long long>(steps, std::max(1, 2048 / h.x));
+        h.planes = (size_t)h.y * h.slots;
+        return h;
+    }
+    h.V = vector_of(C, bf16);
+    const int vectors = C / h.V;
+    h.slots = vectors < 256 ? 256 / vectors : 1;
+    h.x = (vectors + 255) / 256;
+    const long long most = std::max<long long>(1, S / (16ll * h.slots));
+    h.parts = (int)std::min<long long>(most, std::max<long long>(1, 2048 / (N * h.x)));
+    h.planes = (size_t)N * h.parts;
+    return h;
+}
+
+template <typename TIO, int V, int L>
+void row_fwd(const GroupArgs& a, const Shape& h, hipStream_t s)
+{
+    const dim3 grid(h.x, h.y);
+    if (a.act == TTT_ACT_SILU) group_row_fwd_kernel<TIO, V, L, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, h.slots);
+    else if (a.act == TTT_ACT_GELU) group_row_fwd_kernel<TIO, V, L, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, h.slots);
+    else group_row_fwd_kernel<TIO, V, L, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, h.slots);
+}
+
+template <typename TIO, int V, int L>
+void row_bwd(const GroupBwdArgs& a, const Shape& h, float* planes, hipStream_t s)
+{
+    const dim3 grid(h.x, h.y);
+    if (a.act == TTT_ACT_SILU)
+        group_row_bwd_kernel<TIO, V, L, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, h.slots, planes);
+    else if (a.act == TTT_ACT_GELU)
+        group_row_bwd_kernel<TIO, V, L, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, h.slots, planes);
+    else
+        group_row_bwd_kernel<TIO, V, L, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, h.slots, planes);
+}
+
+template <typename TIO, int V, typename DO>
+void lanes_as(int L, DO d)
+{
+    switch (L) {
+    case 1: d(std::integral_constant<int, 1>()); break;
+    case 2: d(std::integral_constant<int, 2>()); break;
+    case 4: d(std::integral_constant<int, 4>()); break;
+    case 8: d(std::integral_constant<int, 8>()); break;
+    case 16: d(std::integral_constant<int, 16>()); break;
+    case 32: d(std::integral_constant<int, 32>()); break;
+    default: d(std::integral_constant<int, 64>());
+    }
+}
+
+template <typename TIO, int V>
+hipError_t fwd_as(const GroupArgs& a, const Shape& h, hipStream_t s)
+{
+    if (h.rows) {
+        lanes_as<TIO, V>(h.L, [&](auto L) { row_fwd<TIO, V, decltype(L)::value>(a, h, s); });
+        return hipGetLastError();
+    }
+    float* planes = (float*)a.workspace;
+    const dim3 grid((unsigned)(h.x * a.N), h.parts);
+    group_moments_kernel<TIO, V><<<grid, 256, 0, s>>>(a, h.parts, planes);
+    group_statistics_kernel<<<(unsigned)(a.N * a.G), 64, 0, s>>>(a, h.parts, planes);
+    if (a.act == TTT_ACT_SILU) group_apply_kernel<TIO, V, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, h.parts);
+    else if (a.act == TTT_ACT_GELU) group_apply_kernel<TIO, V, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, h.parts);
+    else group_apply_kernel<TIO, V, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, h.parts);
+    return hipGetLastError();
+}
+
+template <typename TIO, int V, int ACT>
+void slab_bwd(const GroupBwdArgs& a, const Shape& h, float* planes, float* means, hipStream_t s)
+{
+    const dim3 grid((unsigned)(h.x * a.N), h.parts);
+    group_sums_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, planes);
+    group_means_kernel<<<(unsigned)(a.N * a.G), 64, 0, s>>>(a, h.parts, planes, means);
+    group_dx_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, means);
+}
+
+template <typename TIO, int V>
+hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
+{
+    const bool sums = a.dweight || a.dbias;
+    float* planes = (float*)a.workspace;
+    if (h.rows) {
+        float* to = sums ? planes : nullptr;
+        lanes_as<TIO, V>(h.L, [&](auto L) { row_bwd<TIO, V, decltype(L)::value>(a, h, to, s); });
+    } else {
+        float* means = (float*)((char*)a.workspace + up256(h.planes * 8 * a.C));
+        if (a.act == TTT_ACT_SILU) slab_bwd<TIO, V, TTT_ACT_SILU>(a, h, planes, means, s);
+        else if (a.act == TTT_ACT_GELU) slab_bwd<TIO, V, TTT_ACT_GELU>(a, h, planes, means, s);
+        else slab_bwd<TIO, V, TTT_ACT_NONE>(a, h, planes, means, s);
+    }
+    if (sums)
+        group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 256, 0, s>>>(planes, (long long)h.planes, a.C,
+                                                                            a.dweight, a.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t groupnorm_fwd_workspace(long long N, long long S, int C, int G, bool bf16)
+{
+    const Shape h = shape_of(N, S, C, G, bf16);
+    return h.rows ? 0 : up256(h.planes * 8 * C);
+}
+
+size_t groupnorm_bwd_workspace(long long N, long long S, int C, int G, bool bf16)
+{
+    const Shape h = shape_of(N, S, C, G, bf16);
+    return up256(h.planes * 8 * C) + (h.rows ? 0 : up256((size_t)N * G * 8));
+}
+
+hipError_t launch_groupnorm_fwd(const GroupArgs& a, hipStream_t s)
+{
+    const Shape h = shape_of(a.N, a.S, a.C, a.G, a.bf16);
+    if (a.bf16)
+        return h.V == 8 ? fwd_as<uint16_t, 8>(a, h, s) : h.V == 4 ? fwd_as<uint16_t, 4>(a, h, s)
+             : h.V == 2 ? fwd_as<uint16_t, 2>(a, h, s) : fwd_as<uint16_t, 1>(a, h, s);
+    return h.V == 4 ? fwd_as<float, 4>(a, h, s) : h.V == 2 ? fwd_as<float, 2>(a, h, s) : fwd_as<float, 1>(a, h, s);
+}
+
+hipError_t launch_groupnorm_bwd(const GroupBwdArgs& a, hipStream_t s)
+{
+    if (a.N == 0 || a.S == 0) {
+        if (a.dweight || a.dbias)
+            group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 256, 0, s>>>(nullptr, 0, a.C, a.dweight,
+                                                                                a.dbias);
+        return hipGetLastError();
+    }
+    const Shape h = shape_of(a.N, a.S, a.C, a.G, a.bf16);
+    if (a.bf16)
+        return h.V == 8 ? bwd_as<uint16_t, 8>(a, h, s) : h.V == 4 ? bwd_as<uint16_t, 4>(a, h, s)
+             : h.V == 2 ? bwd_as<uint16_t, 2>(a, h, s) : bwd_as<uint16_t, 1>(a, h, s);
+    return h.V == 4 ? bwd_as<float, 4>(a, h, s) : h.V == 2 ? bwd_as<float, 2>(a, h, s) : bwd_as<float, 1>(a, h, s);
+}
+
+}  // namespace ttt

@@ -17,6 +17,8 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_LAUNCH = 0, -1, -2, -3,
 DTYPE_F32, DTYPE_BF16 = 0, 1
 PLAN_AUTO, PLAN_GENERIC, PLAN_MFMA, PLAN_BIGCHUNK, PLAN_SPLIT = 0, 1, 2, 3, 4
 READ_INCLUSIVE, READ_CHUNK_START = 0, 1
+LAYOUT_BHTD, LAYOUT_BTHD = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 
 # every symbol include/ttt.h declares
 EXPORTS = ("ttt_linear_workspace_bytes", "ttt_linear_workspace_bytes_ex",
@@ -31,6 +33,9 @@ EXPORTS = ("ttt_linear_workspace_bytes", "ttt_linear_workspace_bytes_ex",
            "ttt_gated_workspace_bytes", "ttt_gated_fwd", "ttt_gated_step", "ttt_gated_bwd",
            "ttt_rmsnorm_fwd", "ttt_rmsnorm_q8_fwd", "ttt_rmsnorm_bwd",
            "ttt_rmsnorm_bwd_workspace_bytes", "ttt_clip_grad_norm", "ttt_clip_workspace_bytes",
+           "ttt_delta_fwd", "ttt_delta_workspace_bytes", "ttt_delta_step", "ttt_delta_bwd",
+           "ttt_delta_bwd_workspace_bytes", "ttt_groupnorm_fwd", "ttt_groupnorm_workspace_bytes",
+           "ttt_groupnorm_bwd", "ttt_groupnorm_bwd_workspace_bytes", "ttt_dropout",
            "ttt_status_string", "ttt_plan_name")
 
 
@@ -120,6 +125,24 @@ def lib() -> ctypes.CDLL:
         L.ttt_clip_grad_norm.restype = i
         L.ttt_clip_workspace_bytes.argtypes = []
         L.ttt_clip_workspace_bytes.restype = sz
+        L.ttt_delta_fwd.argtypes = [vp] * 4 + [f] + [vp] * 4 + [i] * 8 + [vp, sz, vp]
+        L.ttt_delta_fwd.restype = i
+        L.ttt_delta_step.argtypes = [vp] * 4 + [f] + [vp] * 3 + [i] * 8 + [vp]
+        L.ttt_delta_step.restype = i
+        L.ttt_delta_bwd.argtypes = [vp] * 4 + [f] + [vp] * 10 + [i] * 8 + [vp, sz, vp]
+        L.ttt_delta_bwd.restype = i
+        L.ttt_groupnorm_fwd.argtypes = [vp] * 3 + [f, i] + [vp] * 3 + [ll, ll, i, i, i, vp, sz, vp]
+        L.ttt_groupnorm_fwd.restype = i
+        L.ttt_groupnorm_bwd.argtypes = [vp] * 3 + [i] + [vp] * 6 + [ll, ll, i, i, i, vp, sz, vp]
+        L.ttt_groupnorm_bwd.restype = i
+        for name in ("ttt_delta_workspace_bytes", "ttt_delta_bwd_workspace_bytes"):
+            getattr(L, name).argtypes = [i] * 7
+            getattr(L, name).restype = sz
+        for name in ("ttt_groupnorm_workspace_bytes", "ttt_groupnorm_bwd_workspace_bytes"):
+            getattr(L, name).argtypes = [ll, ll, i, i, i]
+            getattr(L, name).restype = sz
+        L.ttt_dropout.argtypes = [vp] * 3 + [ll, ctypes.c_double, vp, i, vp]
+        L.ttt_dropout.restype = i
         L.ttt_status_string.argtypes = [i]
         L.ttt_status_string.restype = ctypes.c_char_p
         L.ttt_plan_name.argtypes = [i]
@@ -837,3 +860,272 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, *, outs=None, norm
     if rc != OK:
         raise TTTError(rc, "ttt_clip_grad_norm")
     return outs, norm
+
+
+# ---- gated delta rule, group norm, dropout ----
+
+def _delta_args(K, Q, V, eta, g, W0, layout):
+    """Checks the inputs of a delta call: (B, H, Hk, T, dk, dv, ttt_dtype, device index)."""
+    import torch
+    if layout not in (LAYOUT_BHTD, LAYOUT_BTHD):
+        raise ValueError("layout must be LAYOUT_BHTD or LAYOUT_BTHD, got %r" % (layout,))
+    if K.dim() != 4 or V.dim() != 4:
+        raise ValueError("K and V must have four axes, got %s and %s"
+                         % (tuple(K.shape), tuple(V.shape)))
+    if K.numel() > _INT_MAX or V.numel() > _INT_MAX:       # (else no size is)
+        _fits(*K.shape, *V.shape)
+    io, dev = _first(K, "K")
+    if layout == LAYOUT_BHTD:
+        B, Hk, T, dk = K.shape
+        H, dv = V.shape[1], V.shape[3]
+        values, scalars = (B, H, T, dv), (B, H, T)
+    else:
+        B, T, Hk, dk = K.shape
+        H, dv = V.shape[2:]
+        values, scalars = (B, T, H, dv), (B, T, H)
+    if Hk == 0 or H % Hk:
+        raise ValueError("%d heads of values for %d of keys" % (H, Hk))
+    _match(Q, "Q", K.shape, K.dtype, dev)
+    _match(V, "V", values, K.dtype, dev)
+    if eta is not None:
+        _match(eta, "eta", scalars, torch.float32, dev)
+    if g is not None:
+        _match(g, "g", scalars, torch.float32, dev)
+    if W0 is not None:
+        _match(W0, "W0", (B, H, dv, dk), torch.float32, dev)
+    return B, H, Hk, T, dk, dv, io, dev
+
+
+def delta_workspace_bytes(B, H, Hk, T, dk, dv, io_dtype) -> int:
+    _fits(B, H, Hk, T, dk, dv)
+    return int(lib().ttt_delta_workspace_bytes(B, H, Hk, T, dk, dv, io_dtype))
+
+
+def delta_fwd(K, Q, V, eta, g=None, W0=None, eta_scalar: float = 0.0, *, layout: int = LAYOUT_BHTD,
+              Z=None, W_out=None, workspace=None, stream=None) -> Tuple:
+    """Gated delta rule u_t = v_t - exp(g_t) W_{t-1} k_t, W_t = exp(g_t) W_{t-1} +
+    eta_t u_t k_t^T, z_t = W_t q_t.  K, Q: [B, Hk, T, dk], V: [B, H, T, dv] fp32 or bf16
+    (LAYOUT_BTHD: tokens before heads), H a multiple of Hk; eta: [B, H, T] fp32 or None
+    (then eta_scalar); g: [B, H, T] fp32 <= 0 or None (no decay; -inf starts anew); W0:
+    [B, H, dv, dk] fp32 or None (zero).  Returns (Z, W_T)."""
+    import torch
+    B, H, Hk, T, dk, dv, io, dev = _delta_args(K, Q, V, eta, g, W0, layout)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return delta_fwd(K, Q, V, eta, g, W0, eta_scalar, layout=layout, Z=Z, W_out=W_out,
+                             workspace=workspace)
+    if Z is None:
+        Z = torch.empty_like(V)
+    else:
+        _match(Z, "Z", V.shape, V.dtype, dev)
+    if W_out is None:
+        W_out = torch.empty((B, H, dv, dk), dtype=torch.float32, device=K.device)
+    else:
+        _match(W_out, "W_out", (B, H, dv, dk), torch.float32, dev)
+    L = lib()
+    ws = _scratch(L.ttt_delta_workspace_bytes(B, H, Hk, T, dk, dv, io), K, workspace)
+    rc = L.ttt_delta_fwd(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta), eta_scalar, _ptr(g),
+                         _ptr(W0), Z.data_ptr(), W_out.data_ptr(), B, H, Hk, T, dk, dv, layout, io,
+                         _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_delta_fwd")
+    return Z, W_out
+
+
+def delta_step(K, Q, V, eta, g, W, eta_scalar: float = 0.0, *, layout: int = LAYOUT_BHTD, Z=None,
+               stream=None):
+    """Continue gated delta rules by the n tokens of K, Q, V from the state W [B, H, dv, dk]
+    fp32, which is updated in place; arguments as delta_fwd.  Returns Z."""
+    import torch
+    if W is None:
+        raise ValueError("W is required")
+    B, H, Hk, T, dk, dv, io, dev = _delta_args(K, Q, V, eta, g, W, layout)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return delta_step(K, Q, V, eta, g, W, eta_scalar, layout=layout, Z=Z)
+    if Z is None:
+        Z = torch.empty_like(V)
+    else:
+        _match(Z, "Z", V.shape, V.dtype, dev)
+    rc = lib().ttt_delta_step(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta), eta_scalar,
+                              _ptr(g), W.data_ptr(), Z.data_ptr(), B, H, Hk, T, dk, dv, layout, io,
+                              _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_delta_step")
+    return Z
+
+
+def delta_bwd_workspace_bytes(B, H, Hk, T, dk, dv, io_dtype) -> int:
+    _fits(B, H, Hk, T, dk, dv)
+    return int(lib().ttt_delta_bwd_workspace_bytes(B, H, Hk, T, dk, dv, io_dtype))
+
+
+def delta_bwd(K, Q, V, eta, g, W0, dZ, dW_T=None, eta_scalar: float = 0.0, *,
+              layout: int = LAYOUT_BHTD, dK=None, dQ=None, dV=None, deta=None, dg=None, dW0=None,
+              workspace=None, stream=None) -> Tuple:
+    """Gradients of <dZ, Z> + <dW_T, W_T> through Z, W_T = delta_fwd(K, Q, V, eta, g, W0).
+    dZ: like V; dW_T: [B, H, dv, dk] fp32 or None.  Returns (dK, dQ, dV, deta, dg, dW0): dK
+    and dQ summed over the heads that share them, deta and dg per token in fp32."""
+    import torch
+    B, H, Hk, T, dk, dv, io, dev = _delta_args(K, Q, V, eta, g, W0, layout)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return delta_bwd(K, Q, V, eta, g, W0, dZ, dW_T, eta_scalar, layout=layout, dK=dK, dQ=dQ,
+                             dV=dV, deta=deta, dg=dg, dW0=dW0, workspace=workspace)
+    _match(dZ, "dZ", V.shape, V.dtype, dev)
+    state, scalars = (B, H, dv, dk), V.shape[:3]
+    if dW_T is not None:
+        _match(dW_T, "dW_T", state, torch.float32, dev)
+
+    def output(t, name, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=K.device)
+        _match(t, name, shape, dtype, dev)
+        return t
+
+    dK, dQ = output(dK, "dK", K.shape, K.dtype), output(dQ, "dQ", K.shape, K.dtype)
+    dV = output(dV, "dV", V.shape, V.dtype)
+    deta = output(deta, "deta", scalars, torch.float32)
+    dg = output(dg, "dg", scalars, torch.float32)
+    dW0 = output(dW0, "dW0", state, torch.float32)
+    L = lib()
+    ws = _scratch(L.ttt_delta_bwd_workspace_bytes(B, H, Hk, T, dk, dv, io), K, workspace)
+    rc = L.ttt_delta_bwd(K.data_ptr(), Q.data_ptr(), V.data_ptr(), _ptr(eta), eta_scalar, _ptr(g),
+                         _ptr(W0), dZ.data_ptr(), _ptr(dW_T), dK.data_ptr(), dQ.data_ptr(),
+                         dV.data_ptr(), deta.data_ptr(), dg.data_ptr(), dW0.data_ptr(), B, H, Hk, T,
+                         dk, dv, layout, io, _ptr(ws), 0 if ws is None else ws.numel(),
+                         _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_delta_bwd")
+    return dK, dQ, dV, deta, dg, dW0
+
+
+def _group_args(X, groups, weight, bias):
+    import torch
+    shape = X.shape
+    if len(shape) < 2 or not shape[-1]:
+        raise ValueError("X must be [N, ..., C], got %s" % (tuple(shape),))
+    N, C = shape[0], shape[-1]
+    _fits(C, groups)
+    if groups < 1 or C % groups:
+        raise ValueError("%d channels in %d groups" % (C, groups))
+    io, dev = _first(X, "X")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _match(t, name, (C,), torch.float32, dev)
+    S = 1
+    for n in shape[1:-1]:
+        S *= n
+    return io, dev, N, S, C
+
+
+def groupnorm_workspace_bytes(N, S, C, groups, io_dtype) -> int:
+    _fits(C, groups)
+    return int(lib().ttt_groupnorm_workspace_bytes(N, S, C, groups, io_dtype))
+
+
+def groupnorm_fwd(X, groups: int, weight=None, bias=None, eps: float = 1e-5, act: int = ACT_NONE, *,
+                  Y=None, mean=None, rstd=None, workspace=None, stream=None) -> Tuple:
+    """Group norm with an activation over channels-last X [N, ..., C] fp32 or bf16: over each
+    row's places (the axes between) and the C / groups neighbouring channels of a group,
+    y = act((x - mean) / sqrt(var + eps) * weight + bias).  weight, bias: [C] fp32 or None;
+    act: ACT_NONE, ACT_SILU or ACT_GELU.  [tokens, heads * d] with groups = heads norms every
+    head's output.  Returns (Y, mean, rstd): the statistics are [N, groups] fp32."""
+    import torch
+    io, dev, N, S, C = _group_args(X, groups, weight, bias)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return groupnorm_fwd(X, groups, weight, bias, eps, act, Y=Y, mean=mean, rstd=rstd,
+                                 workspace=workspace)
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _match(Y, "Y", X.shape, X.dtype, dev)
+    if mean is None:
+        mean = torch.empty((N, groups), dtype=torch.float32, device=X.device)
+    else:
+        _match(mean, "mean", (N, groups), torch.float32, dev)
+    if rstd is None:
+        rstd = torch.empty((N, groups), dtype=torch.float32, device=X.device)
+    else:
+        _match(rstd, "rstd", (N, groups), torch.float32, dev)
+    L = lib()
+    ws = _scratch(L.ttt_groupnorm_workspace_bytes(N, S, C, groups, io), X, workspace)
+    rc = L.ttt_groupnorm_fwd(X.data_ptr(), _ptr(weight), _ptr(bias), eps, act, Y.data_ptr(),
+                             mean.data_ptr(), rstd.data_ptr(), N, S, C, groups, io, _ptr(ws),
+                             0 if ws is None else ws.numel(), _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_groupnorm_fwd")
+    return Y, mean, rstd
+
+
+def groupnorm_bwd_workspace_bytes(N, S, C, groups, io_dtype) -> int:
+    _fits(C, groups)
+    return int(lib().ttt_groupnorm_bwd_workspace_bytes(N, S, C, groups, io_dtype))
+
+
+def groupnorm_bwd(X, groups: int, weight, bias, dY, mean, rstd, act: int = ACT_NONE, *, dX=None,
+                  dweight=None, dbias=None, workspace=None, stream=None) -> Tuple:
+    """Gradients through Y, mean, rstd = groupnorm_fwd(X, groups, weight, bias, eps, act).
+    Returns (dX, dweight, dbias), the last two [C] fp32, or None where there is no weight or
+    bias (unless a tensor for it is given)."""
+    import torch
+    io, dev, N, S, C = _group_args(X, groups, weight, bias)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return groupnorm_bwd(X, groups, weight, bias, dY, mean, rstd, act, dX=dX,
+                                 dweight=dweight, dbias=dbias, workspace=workspace)
+    _match(dY, "dY", X.shape, X.dtype, dev)
+    _match(mean, "mean", (N, groups), torch.float32, dev)
+    _match(rstd, "rstd", (N, groups), torch.float32, dev)
+    if dX is None:
+        dX = torch.empty_like(X)
+    else:
+        _match(dX, "dX", X.shape, X.dtype, dev)
+    if dweight is not None:
+        _match(dweight, "dweight", (C,), torch.float32, dev)
+    elif weight is not None:
+        dweight = torch.empty(C, dtype=torch.float32, device=X.device)
+    if dbias is not None:
+        _match(dbias, "dbias", (C,), torch.float32, dev)
+    elif bias is not None:
+        dbias = torch.empty(C, dtype=torch.float32, device=X.device)
+    L = lib()
+    ws = _scratch(L.ttt_groupnorm_bwd_workspace_bytes(N, S, C, groups, io), X, workspace)
+    rc = L.ttt_groupnorm_bwd(X.data_ptr(), _ptr(weight), _ptr(bias), act, mean.data_ptr(),
+                             rstd.data_ptr(), dY.data_ptr(), dX.data_ptr(), _ptr(dweight),
+                             _ptr(dbias), N, S, C, groups, io, _ptr(ws),
+                             0 if ws is None else ws.numel(), _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_groupnorm_bwd")
+    return dX, dweight, dbias
+
+
+def dropout(X, p: float, rng, residual=None, *, Y=None, stream=None):
+    """X / (1 - p) where a counter-based generator keeps an element and 0 elsewhere, plus the
+    residual.  rng: [2] int64 device tensor (seed, first counter), advanced by the caller by
+    (X.numel() + 3) // 4 a call.  The gradient for X is dropout(dY, p, rng) with the same rng.
+    Returns Y."""
+    import torch
+    io, dev = _first(X, "X")
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return dropout(X, p, rng, residual, Y=Y)
+    _match(rng, "rng", (2,), torch.int64, dev)
+    if residual is not None:
+        _match(residual, "residual", X.shape, X.dtype, dev)
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _match(Y, "Y", X.shape, X.dtype, dev)
+    rc = lib().ttt_dropout(X.data_ptr(), _ptr(residual), Y.data_ptr(), X.numel(), p, rng.data_ptr(),
+                           io, _raw_stream(dev))
+    if rc != OK:
+        raise TTTError(rc, "ttt_dropout")
+    return Y
