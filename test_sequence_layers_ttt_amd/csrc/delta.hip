@@ -16,20 +16,32 @@ namespace {
 
 __device__ __forceinline__ double shift_up(double x, int by) { return __shfl_up(x, by, 64); }
 
+// parts of P that the forward scan takes: behind a bf16 Z two are enough (2^-17)
+template <typename TIO> constexpr int kZParts = sizeof(TIO) == 2 ? 2 : 3;
+
 // ---- per chunk: decays, L, S, P -------------------------------------------------
-// One workgroup of four waves per (chunk, head).  S = (I + L eta)^-1 L column tile by
-// column tile: the four 16 x 16 diagonal blocks are inverted by substitution, the tiles
-// below follow from them in order, in fp32 throughout.
+// One workgroup of four waves per (chunk, head).  P's operands (or its transpose's) come out
+// of the products of keys and queries as they lie, with the operands' order chosen for it.
+// S = (I + L eta)^-1 L column tile by column tile: the four 16 x 16 diagonal blocks are
+// inverted by substitution, the tiles below follow from them in order, in fp32 throughout.
+// LDS decides how many workgroups a compute unit holds: S takes the place of the tiles, and
+// the inverted blocks stand in the tiles of L above its diagonal.
 template <typename TIO, int DK, bool BACKWARD>
 __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
 {
     constexpr int LD = kChunk + 4;
-    __shared__ __align__(16) Tile<TIO, DK> tk;
-    __shared__ __align__(16) Tile<TIO, DK> tq;
-    __shared__ __align__(16) float Lm[kChunk * LD], Pm[kChunk * LD], Sm[kChunk * LD], Tm[4 * 16 * 20];
+    struct Inputs { Tile<TIO, DK> k, q; };
+    union Room {
+        Inputs in;
+        float S[kChunk * LD];
+    };
+    __shared__ __align__(16) Room room;
+    __shared__ __align__(16) float Lm[kChunk * LD];
     __shared__ double G[kChunk];
     __shared__ int cuts[kChunk];
     __shared__ __align__(16) float eta[kChunk];
+    const Tile<TIO, DK>&tk = room.in.k, &tq = room.in.q;
+    float* Sm = room.S;
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -37,16 +49,11 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
     const int head = a.head0 + local, b = head / a.f.H, h = head % a.f.H;
     const int hk = h / (a.f.H / a.f.Hk), t0 = chunk * kChunk, T = a.f.T, dk = a.f.dk;
     const bool whole = dk % kGran<TIO> == 0;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    {
-        TileLoad<TIO, DK> lk, lq;
-        const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-        const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-        lk.load(K, t0, T, dk, whole, tid);
-        lq.load(Q, t0, T, dk, whole, tid);
-        lk.put(tk, tid);
-        lq.put(tq, tid);
-    }
+    TileLoad<TIO, DK> lk, lq;
+    lk.load(Rows<const TIO>((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first), t0, T, dk, whole, tid);
+    lq.load(Rows<const TIO>((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first), t0, T, dk, whole, tid);
     const size_t unit = (size_t)local * a.chunks + chunk;
     Record& rec = a.records[unit];
     if (w == 0) {
@@ -70,49 +77,82 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
         rec.start[lane] = n == 0 ? expf((float)x) : 0.f;
         rec.end[lane] = n == nl ? expf((float)(xl - x)) : 0.f;
     }
+    lk.put(room.in.k, tid);
+    lq.put(room.in.q, tid);
     __syncthreads();
 
-    // row tile w of L and P
+    // row tile w of L, and of P: rows s by column t (P's operand as it lies) up to the diagonal,
+    // or rows t by column s from the diagonal on (its transpose's)
+    f32x4 p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+        f32x4 kk = zero;
+        p[i] = zero;
         if (i <= w) {
 #pragma unroll
             for (int j = 0; j < DK / 32; ++j) {
                 const auto s = by_token(tk, i, j, lane);
                 kk = mma(by_token(tk, w, j, lane), s, kk);
-                qk = mma(by_token(tq, w, j, lane), s, qk);
+                if constexpr (!BACKWARD) p[i] = mma(s, by_token(tq, w, j, lane), p[i]);
             }
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const int t = 16 * w + 4 * g + v, s = 16 * i + c;
-                const float e = s <= t ? pair_decay(G, cuts, t, s) : 0.f;
-                kk[v] = s < t ? kk[v] * e : 0.f;
-                qk[v] = s <= t ? qk[v] * e : 0.f;
+                kk[v] = s < t ? kk[v] * pair_decay(G, cuts, t, s) : 0.f;
+                if constexpr (!BACKWARD) {
+                    const int to = 16 * w + c, from = 16 * i + 4 * g + v;
+                    p[i][v] = from <= to ? p[i][v] * pair_decay(G, cuts, to, from) : 0.f;
+                }
+            }
+            put_cl<LD>(Lm + 16 * w * LD, 16 * i, lane, kk);
+        }
+        if constexpr (BACKWARD) {
+            if (i >= w) {
+#pragma unroll
+                for (int j = 0; j < DK / 32; ++j)
+                    p[i] = mma(by_token(tq, i, j, lane), by_token(tk, w, j, lane), p[i]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int t = 16 * i + 4 * g + v, s = 16 * w + c;
+                    p[i][v] = s <= t ? p[i][v] * pair_decay(G, cuts, t, s) : 0.f;
+                }
             }
         }
-        put_cl<LD>(Lm + 16 * w * LD, 16 * i, lane, kk);
-        put_cl<LD>(Pm + 16 * w * LD, 16 * i, lane, qk);
+    }
+    constexpr int NZ = BACKWARD ? 3 : kZParts<TIO>;
+    quad* fp = a.P + unit * NZ * kFragQuads;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (!BACKWARD && j <= w / 2) store_frag<NZ>(fp, frag_lower(w, j), lane, p[2 * j], p[2 * j + 1]);
+        if (BACKWARD && j >= w / 2) store_frag<NZ>(fp, frag_upper(w, j), lane, p[2 * j], p[2 * j + 1]);
     }
     __syncthreads();
 
-    // (I + L eta)^-1 of diagonal block w, column c (the four groups of lanes do the same)
+    // (I + L eta)^-1 of diagonal block w, column c (the four groups of lanes do the same), into
+    // one of the tiles (0, 1), (0, 2), (0, 3), (1, 2)
+    auto inverse_at = [&](int i) { return Lm + (i < 3 ? 16 * (i + 1) : 16 * LD + 32); };
     {
         float x[16];
         const float* L = Lm + 16 * w * LD + 16 * w;
-        float e[16];
+        f32x4 e[4];
 #pragma unroll
-        for (int s = 0; s < 16; ++s) e[s] = eta[16 * w + s];
+        for (int s = 0; s < 4; ++s) e[s] = *reinterpret_cast<const f32x4*>(eta + 16 * w + 4 * s);
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             float y = t == c ? 1.f : 0.f;
 #pragma unroll
-            for (int s = 0; s < t; ++s) y = fmaf(-L[t * LD + s] * e[s], x[s], y);
+            for (int s = 0; s < t; s += 4) {
+                const f32x4 n = *reinterpret_cast<const f32x4*>(L + t * LD + s) * e[s / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (s + i < t) y = fmaf(-n[i], x[s + i], y);
+            }
             x[t] = y;
         }
+        float* to = inverse_at(w);
         if (g == 0)
 #pragma unroll
-            for (int t = 0; t < 16; ++t) Tm[(16 * w + t) * 20 + c] = x[t];
+            for (int t = 0; t < 16; ++t) to[t * LD + c] = x[t];
     }
     __syncthreads();
 
@@ -121,7 +161,7 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
         f32x4 S[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            S[i] = zero;
             if (i >= w) {
                 f32x4 r = cl<LD>(Lm + 16 * i * LD, 16 * w, lane);
 #pragma unroll
@@ -131,139 +171,107 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
                         const f32x4 e = *reinterpret_cast<const f32x4*>(eta + 16 * j + 4 * g);
                         r = mm16(-(n * e), S[j], r);
                     }
-                S[i] = mm16(rl<20>(Tm + 16 * i * 20, 0, lane), r, f32x4{0.f, 0.f, 0.f, 0.f});
+                S[i] = mm16(rl<LD>(inverse_at(i), 0, lane), r, zero);
             }
             put_cl<LD>(Sm + 16 * i * LD, 16 * w, lane, S[i]);
         }
+        if constexpr (BACKWARD) {
+            quad* ft = a.St + unit * 3 * kFragQuads;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (j >= w / 2) store_frag<3>(ft, frag_upper(w, j), lane, S[2 * j], S[2 * j + 1]);
+        }
     }
     __syncthreads();
-
-    Frag* fs = a.S + unit * kFrags;
-    Frag* fp = a.P + unit * kFrags;
-    auto down = [&](const float* M, int i, int j) {   // column 16 i + c over the pair's rows
-        const float* p = M + (32 * j + 4 * g) * LD + 16 * i + c;
-        return f32x4{p[0], p[LD], p[2 * LD], p[3 * LD]};
-    };
+    quad* fs = a.S + unit * 3 * kFragQuads;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (j <= w / 2) {
-            const int f = frag_lower(w, j);
-            store_frag(fs[f], lane, rl<LD>(Sm + 16 * w * LD, 32 * j, lane),
-                       rl<LD>(Sm + 16 * w * LD, 32 * j + 16, lane));
-            if constexpr (!BACKWARD)
-                store_frag(fp[f], lane, rl<LD>(Pm + 16 * w * LD, 32 * j, lane),
-                           rl<LD>(Pm + 16 * w * LD, 32 * j + 16, lane));
-        }
-        if constexpr (BACKWARD) {
-            if (j >= w / 2) {
-                const int f = frag_upper(w, j);
-                store_frag(a.St[unit * kFrags + f], lane, down(Sm, w, j), down(Sm + 16 * LD, w, j));
-                store_frag(fp[f], lane, down(Pm, w, j), down(Pm + 16 * LD, w, j));
-            }
-        }
-    }
+    for (int j = 0; j < 2; ++j)
+        if (j <= w / 2)
+            store_frag<3>(fs, frag_lower(w, j), lane, rl<LD>(Sm + 16 * w * LD, 32 * j, lane),
+                          rl<LD>(Sm + 16 * w * LD, 32 * j + 16, lane));
 }
 
 // ---- the scan over the chunks ------------------------------------------------------
 // One workgroup of four waves per head and 64 columns of values, a wave for 16 of them.
-// Keys and queries of the next chunk are loaded while this one is worked on and go to the
-// other half of the LDS buffer: one barrier a chunk.
+// All that the next chunk needs is loaded to registers while this one is worked on, and then
+// goes to the other LDS buffer: no product waits for memory, one barrier a chunk.
+// Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
 template <typename TIO, int DK, bool SAVE>
 __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
 {
-    constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
-    // the order to which the products behind Z go: its own rounding to bf16 is far above 2^-17
-    constexpr int OZ = sizeof(TIO) == 2 ? 1 : 2, NZ = OZ + 1;
-    __shared__ __align__(16) Tile<TIO, DK> tk[2];
-    __shared__ __align__(16) Tile<TIO, DK> tq[SAVE ? 1 : 2];
+    constexpr int M = DK / 16, J = DK / 32, NZ = SAVE ? 0 : kZParts<TIO>, OZ = kZParts<TIO> - 1;
+    typedef ChunkTiles<TIO, DK, NZ, !SAVE> Tiles;
+    constexpr int NB = kBuffers<Tiles>;
+    __shared__ __align__(16) Tiles tiles[NB];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
     const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
     const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
-    const int col = 64 * (blockIdx.x % parts) + 16 * w + c;
-    const bool works = 64 * (int)(blockIdx.x % parts) + 16 * w < a.dvp;   // (else a wave only helps to load)
-    const bool whole = dk % kGran<TIO> == 0;
+    const int first = 64 * (int)(blockIdx.x % parts), col = first + 16 * w + c;
+    const bool works = first + 16 * w < a.dvp;   // (else a wave only helps to load)
+    const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0, fours = dv % 4 == 0;
     const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
     const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
     const Rows<const TIO> V((const TIO*)a.f.V, b, h, a.f.H, T, dv, a.f.tokens_first);
     const Rows<TIO> Z((TIO*)a.f.Z, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const size_t state = (size_t)head * dv * dk;
+    const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    f32x4 W[M], vn[4];
+    ChunkLoad<TIO, DK, NZ, !SAVE> next;
+    auto fetch = [&](int n) {
+        const size_t unit = unit0 + n;
+        next.load(K, Q, V, a.S + unit * 3 * kFragQuads, a.P + unit * NZ * kFragQuads, a.records + unit,
+                  n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+    };
+    fetch(0);
+    f32x4 W[M];
 #pragma unroll
     for (int m = 0; m < M; ++m)
         W[m] = load_state(a.f.W0 ? a.f.W0 + state : nullptr, col, 16 * m + 4 * g, dv, dk);
-    TileLoad<TIO, DK> lk, lq;
-    lk.load(K, 0, T, dk, whole, tid);
-    lk.put(tk[0], tid);
-    if constexpr (!SAVE) {
-        lq.load(Q, 0, T, dk, whole, tid);
-        lq.put(tq[0], tid);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) vn[i] = load_cl(V, 0, T, i, g, col, dv);
+    next.put(tiles[0], tid);
     __syncthreads();
 
     for (int n = 0; n < a.chunks; ++n) {
-        const int t0 = n * kChunk, next = t0 + kChunk;
-        const size_t unit = (size_t)local * a.chunks + n;
-        const Tile<TIO, DK>& k = tk[n & 1];
-        const Tile<TIO, DK>& q = tq[SAVE ? 0 : n & 1];
-        f32x4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = vn[i];
-        if (n + 1 < a.chunks) {
-            lk.load(K, next, T, dk, whole, tid);
-            if constexpr (!SAVE) lq.load(Q, next, T, dk, whole, tid);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vn[i] = load_cl(V, next, T, i, g, col, dv);
-        }
+        const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
+        if (n + 1 < a.chunks) fetch(n + 1);
         if (works) {
-            const Record& rec = a.records[unit];
-            const Frag* fs = a.S + unit * kFrags;
-            f32x4 start[4], eta[4], end[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                start[i] = *reinterpret_cast<const f32x4*>(rec.start + 16 * i + 4 * g);
-                eta[i] = *reinterpret_cast<const f32x4*>(rec.eta + 16 * i + 4 * g);
-                end[i] = *reinterpret_cast<const f32x4*>(rec.end + 16 * i + 4 * g);
-            }
-            const float all = rec.start[kChunk - 1];
-            Parts<3> S[kFrags];
-#pragma unroll
-            for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(fs[f], lane);
-
             f32x4 r[4], z[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) r[i] = z[i] = zero;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const Parts<3> wp = split<3>(W[2 * j], W[2 * j + 1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    r[i] = mma(by_token(k, i, j, lane), wp, r[i]);
-                    if constexpr (!SAVE) z[i] = mma<OZ>(by_token(q, i, j, lane), wp, z[i]);
+                    r[i] = mma(by_token(t.k, i, j, lane), wp, r[i]);
+                    if constexpr (!SAVE) z[i] = mma<OZ>(wp, by_token(t.q, i, j, lane), z[i]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
+            f32x4 eta[4];
             Parts<3> x[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < 4; ++i) eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const auto v = by_feature(t.v, w, j, lane);
+#pragma unroll
+                for (int i = 2 * j; i < 2 * j + 2; ++i)
+                    r[i] = widen_parts(v, i & 1) - *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g) * r[i];
                 x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j <= i / 2; ++j) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
+                for (int j = 0; j <= i / 2; ++j) r[i] = mma(load_frag<3>(t.s, frag_lower(i, j), lane), x[j], r[i]);
             if constexpr (SAVE) {
-                float* st = a.states + unit * DK * a.dvp + col;
+                float* st = a.states + (unit0 + n) * DK * a.dvp + col;
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st[(size_t)(16 * m + 4 * g + e) * a.dvp] = W[m][e];
-                float* u = a.U + unit * kChunk * a.dvp + col;
+                float* u = a.U + (unit0 + n) * kChunk * a.dvp + col;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -271,33 +279,36 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] *= eta[i];
+            const float all = t.start[kChunk - 1];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                x[j] = split<3>(end[2 * j] * r[2 * j], end[2 * j + 1] * r[2 * j + 1]);
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 ea = *reinterpret_cast<const f32x4*>(t.end + 32 * j + 4 * g);
+                const f32x4 eb = *reinterpret_cast<const f32x4*>(t.end + 32 * j + 16 + 4 * g);
+                x[j] = split<3>(ea * r[2 * j], eb * r[2 * j + 1]);
+            }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 W[m] *= all;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) W[m] = mma(by_feature(k, m, j, lane), x[j], W[m]);
+                for (int j = 0; j < 2; ++j) W[m] = mma(by_feature(t.k, m, j, lane), x[j], W[m]);
             }
             if constexpr (!SAVE) {
-                const Frag* fp = a.P + unit * kFrags;
+                Parts<NZ> u[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) x[j] = split<3>(r[2 * j], r[2 * j + 1]);
+                for (int j = 0; j < 2; ++j) u[j] = split<NZ>(r[2 * j], r[2 * j + 1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    z[i] *= start[i];
+                    z[i] *= t.start[16 * i + c];
 #pragma unroll
                     for (int j = 0; j <= i / 2; ++j)
-                        z[i] = mma<OZ>(load_frag<NZ>(fp[frag_lower(i, j)], lane), x[j], z[i]);
-                    store_cl(Z, t0, T, i, g, col, dv, z[i]);
+                        z[i] = mma<OZ>(u[j], load_frag<NZ>(t.p, frag_lower(i, j), lane), z[i]);
+                    const int token = n * kChunk + 16 * i + c;
+                    if (token < T) store4(Z.at(token), first + 16 * w + 4 * g, dv, fours, z[i]);
                 }
             }
         }
-        if (n + 1 < a.chunks) {
-            lk.put(tk[(n + 1) & 1], tid);
-            if constexpr (!SAVE) lq.put(tq[SAVE ? 0 : (n + 1) & 1], tid);
-        }
+        if constexpr (NB == 1) __syncthreads();
+        if (n + 1 < a.chunks) next.put(tiles[NB == 2 ? (n + 1) & 1 : 0], tid);
         __syncthreads();
     }
     if constexpr (!SAVE)
@@ -420,20 +431,19 @@ constexpr size_t kPassBytes = (size_t)1 << 30;   // of workspace, where one head
 
 struct Plan {
     int chunks, groups;      // groups of heads that share keys, in one pass
-    size_t records, S, P, bytes;
+    size_t S, P, bytes;      // places in the workspace, which begins with the records
 };
 
-Plan fwd_plan(int B, int H, int Hk, int T)
+Plan fwd_plan(int B, int H, int Hk, int T, bool bf16)
 {
     Plan p;
     p.chunks = (T + kChunk - 1) / kChunk;
-    const size_t unit = (size_t)p.chunks * (H / Hk);
-    const size_t one = unit * (sizeof(Record) + 2 * kFrags * sizeof(Frag));
+    const size_t unit = (size_t)p.chunks * (H / Hk), part = kFragQuads * sizeof(quad);
+    const size_t s = 3 * part, z = (bf16 ? 2 : 3) * part, one = unit * (sizeof(Record) + s + z);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
-    p.records = 0;
     p.S = up256(unit * p.groups * sizeof(Record));
-    p.P = p.S + up256(unit * p.groups * kFrags * sizeof(Frag));
-    p.bytes = p.P + up256(unit * p.groups * kFrags * sizeof(Frag));
+    p.P = p.S + up256(unit * p.groups * s);
+    p.bytes = p.P + up256(unit * p.groups * z);
     return p;
 }
 
@@ -463,22 +473,22 @@ hipError_t launch_delta_chain(const DeltaPass& p, bool save, hipStream_t s)
                     : chain_as<float, 128>(p, save, s);
 }
 
-size_t delta_fwd_workspace(int B, int H, int Hk, int T, int, int, bool)
+size_t delta_fwd_workspace(int B, int H, int Hk, int T, int, int, bool bf16)
 {
-    return fwd_plan(B, H, Hk, T).bytes;
+    return fwd_plan(B, H, Hk, T, bf16).bytes;
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
 {
-    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T);
+    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T, a.bf16);
     char* ws = (char*)a.workspace;
     DeltaPass p = {};
     p.f = a;
     p.chunks = plan.chunks;
     p.dvp = (a.dv + 31) / 32 * 32;
-    p.records = (Record*)(ws + plan.records);
-    p.S = (Frag*)(ws + plan.S);
-    p.P = (Frag*)(ws + plan.P);
+    p.records = (Record*)ws;
+    p.S = (quad*)(ws + plan.S);
+    p.P = (quad*)(ws + plan.P);
     const int share = a.H / a.Hk, all = a.B * a.Hk;
     for (int first = 0; first < all; first += plan.groups) {
         p.head0 = first * share;

@@ -27,64 +27,45 @@ template <typename TIO, int DK>
 __global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
 {
     constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
+    typedef ChunkTiles<TIO, DK, 3, true> Tiles;
+    constexpr int NB = kBuffers<Tiles>;
     const DeltaPass& a = q_.p;
-    __shared__ __align__(16) Tile<TIO, DK> tk[2];
-    __shared__ __align__(16) Tile<TIO, DK> tq[2];
+    __shared__ __align__(16) Tiles tiles[NB];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
     const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
     const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
-    const int col = 64 * (blockIdx.x % parts) + 16 * w + c;
-    const bool works = 64 * (int)(blockIdx.x % parts) + 16 * w < a.dvp;
-    const bool whole = dk % kGran<TIO> == 0;
+    const int first = 64 * (int)(blockIdx.x % parts), col = first + 16 * w + c;
+    const bool works = first + 16 * w < a.dvp;
+    const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0;
     const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
     const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
     const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const Rows<TIO> dV((TIO*)q_.a.dV, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const size_t state = (size_t)head * dv * dk;
+    const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    f32x4 D[M], zn[4];
+    ChunkLoad<TIO, DK, 3, true> next;
+    auto fetch = [&](int n) {
+        const size_t unit = unit0 + n;
+        next.load(K, Q, dZ, a.St + unit * 3 * kFragQuads, a.P + unit * 3 * kFragQuads, a.records + unit,
+                  n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+    };
+    const int last = a.chunks - 1;
+    fetch(last);
+    f32x4 D[M];
 #pragma unroll
     for (int m = 0; m < M; ++m)
         D[m] = load_state(q_.a.dW_T ? q_.a.dW_T + state : nullptr, col, 16 * m + 4 * g, dv, dk);
-    const int last = a.chunks - 1;
-    TileLoad<TIO, DK> lk, lq;
-    lk.load(K, last * kChunk, T, dk, whole, tid);
-    lq.load(Q, last * kChunk, T, dk, whole, tid);
-    lk.put(tk[last & 1], tid);
-    lq.put(tq[last & 1], tid);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) zn[i] = load_cl(dZ, last * kChunk, T, i, g, col, dv);
+    next.put(tiles[NB == 2 ? last & 1 : 0], tid);
     __syncthreads();
 
     for (int n = last; n >= 0; --n) {
-        const int t0 = n * kChunk, next = t0 - kChunk;
-        const size_t unit = (size_t)local * a.chunks + n;
-        const Tile<TIO, DK>& k = tk[n & 1];
-        const Tile<TIO, DK>& q = tq[n & 1];
-        f32x4 z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = zn[i];
-        if (n > 0) {
-            lk.load(K, next, T, dk, whole, tid);
-            lq.load(Q, next, T, dk, whole, tid);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) zn[i] = load_cl(dZ, next, T, i, g, col, dv);
-        }
+        const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
+        if (n > 0) fetch(n - 1);
         if (works) {
-            const Record& rec = a.records[unit];
-            f32x4 start[4], eta[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                start[i] = *reinterpret_cast<const f32x4*>(rec.start + 16 * i + 4 * g);
-                eta[i] = *reinterpret_cast<const f32x4*>(rec.eta + 16 * i + 4 * g);
-            }
-            const float all = rec.start[kChunk - 1];
-            const Frag* ft = a.St + unit * kFrags;
-            const Frag* fp = a.P + unit * kFrags;
-
+            const size_t unit = unit0 + n;
             float* out = a.cotangents + unit * DK * a.dvp + col;
 #pragma unroll
             for (int m = 0; m < M; ++m)
@@ -93,24 +74,27 @@ __global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
 
             f32x4 f[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) f[i] = zero;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = mma(by_token(k, i, j, lane), dp, f[i]);
+                for (int i = 0; i < 4; ++i) f[i] = mma(by_token(t.k, i, j, lane), dp, f[i]);
             }
+            Parts<NP> zp[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] *= *reinterpret_cast<const f32x4*>(rec.end + 16 * i + 4 * g);
+            for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const Parts<NP> zp = split<NP>(z[2 * j], z[2 * j + 1]);
+            for (int i = 0; i < 4; ++i) {
+                f[i] *= *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (j >= i / 2) f[i] = mma(load_frag<3>(fp[frag_upper(i, j)], lane), zp, f[i]);
+                for (int j = 0; j < 2; ++j)
+                    if (j >= i / 2) f[i] = mma(load_frag<3>(t.p, frag_upper(i, j), lane), zp[j], f[i]);
             }
-            Parts<3> x[2];
+            f32x4 eta[4];
+            Parts<3> x[2], y[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 x[j] = split<3>(-(eta[2 * j] * f[2 * j]), -(eta[2 * j + 1] * f[2 * j + 1]));
@@ -118,38 +102,36 @@ __global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (j >= i / 2) f[i] = mma(load_frag<3>(ft[frag_upper(i, j)], lane), x[j], f[i]);
+                    if (j >= i / 2) f[i] = mma(load_frag<3>(t.s, frag_upper(i, j), lane), x[j], f[i]);
 
             float* F = a.F + unit * kChunk * a.dvp + col;
+            f32x4 z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) F[(size_t)(16 * i + 4 * g + e) * a.dvp] = f[i][e];
-                f[i] *= eta[i];
-                store_cl(dV, t0, T, i, g, col, dv, f[i]);
-                f[i] *= -start[i];
-                z[i] *= start[i];
+                const f32x4 start = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
+                f[i] *= -(start * eta[i]);
+                z[i] = start * widen_parts(zp[i / 2], i & 1);
             }
-            Parts<3> y[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 x[j] = split<3>(f[2 * j], f[2 * j + 1]);
                 y[j] = split<3>(z[2 * j], z[2 * j + 1]);
             }
+            const float all = t.start[kChunk - 1];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 D[m] *= all;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    D[m] = mma(by_feature(k, m, j, lane), x[j], D[m]);
-                    D[m] = mma(by_feature(q, m, j, lane), y[j], D[m]);
+                    D[m] = mma(by_feature(t.k, m, j, lane), x[j], D[m]);
+                    D[m] = mma(by_feature(t.q, m, j, lane), y[j], D[m]);
                 }
             }
         }
-        if (n > 0) {
-            lk.put(tk[(n - 1) & 1], tid);
-            lq.put(tq[(n - 1) & 1], tid);
-        }
+        if constexpr (NB == 1) __syncthreads();
+        if (n > 0) next.put(tiles[NB == 2 ? (n - 1) & 1 : 0], tid);
         __syncthreads();
     }
 #pragma unroll
@@ -212,6 +194,7 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
         const float* W0 = a.states + unit * DK * dvp;
         const float* D = a.cotangents + unit * DK * dvp;
         const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
+        const Rows<TIO> dV((TIO*)q_.a.dV, b, h, a.f.H, T, dv, a.f.tokens_first);
 
         // rows `row` of a [.., dvp] fp32 plane as an operand over the columns 32 j ..
         auto plane = [&](const float* X, int row, int j, float by) {
@@ -220,20 +203,7 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
                             by * *reinterpret_cast<const f32x4*>(p + 16));
         };
         auto four = [&](int t, int f) {   // of dZ
-            f32x4 x = zero;
-            if (t0 + t >= T) return x;
-            const TIO* p = dZ.at(t0 + t) + f;
-            if (fours) {
-                if (f < dv) {
-                    if constexpr (sizeof(TIO) == 2) x = widen4(*reinterpret_cast<const u32x2*>(p));
-                    else x = *reinterpret_cast<const f32x4*>(p);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (f + e < dv) x[e] = load1(p + e);
-            }
-            return x;
+            return t0 + t < T ? load4(dZ.at(t0 + t), f, dv, fours) : zero;
         };
         auto zrow = [&](int t, int j) {
             return split<NP>(four(t, 32 * j + 4 * g), four(t, 32 * j + 16 + 4 * g));
@@ -252,6 +222,11 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
                 const float* y = F + (size_t)own * dvp + 32 * j + 4 * g;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) de = fmaf(x[e], y[e], fmaf(x[16 + e], y[16 + e], de));
+                if (t0 + own < T) {
+                    const f32x4 a4 = *reinterpret_cast<const f32x4*>(y), b4 = *reinterpret_cast<const f32x4*>(y + 16);
+                    store4(dV.at(t0 + own), 32 * j + 4 * g, dv, fours, eo * a4);
+                    store4(dV.at(t0 + own), 32 * j + 16 + 4 * g, dv, fours, eo * b4);
+                }
             }
             const Parts<3> uo = plane(U, own, j, eo), vo = plane(F, own, j, eo);
             const Parts<NP> zo = zrow(own, j);
@@ -361,22 +336,10 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
     if (t0 + own < T) {
         const Rows<TIO> dQ((TIO*)q_.a.dQ, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
         const Rows<TIO> dK((TIO*)q_.a.dK, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-        auto put = [&](TIO* row, int f, f32x4 x) {
-            if (dk % 4 == 0) {
-                if (f < dk) {
-                    if constexpr (sizeof(TIO) == 2) *reinterpret_cast<u32x2*>(row + f) = pack_bf16x4(x);
-                    else *reinterpret_cast<f32x4*>(row + f) = x;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (f + e < dk) store1(row + f + e, x[e]);
-            }
-        };
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            put(dQ.at(t0 + own), 16 * m + 4 * g, sumq[m]);
-            put(dK.at(t0 + own), 16 * m + 4 * g, sumk[m]);
+            store4(dQ.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, sumq[m]);
+            store4(dK.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, sumk[m]);
         }
     }
 }
@@ -407,7 +370,7 @@ Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
     p.chunks = (T + kChunk - 1) / kChunk;
     p.dvp = (dv + 31) / 32 * 32;
     const size_t unit = (size_t)p.chunks * (H / Hk), DK = delta_padded_dk(dk);
-    const size_t state = 4 * DK * p.dvp, rows = 4 * (size_t)kChunk * p.dvp, frags = kFrags * sizeof(Frag);
+    const size_t state = 4 * DK * p.dvp, rows = 4 * (size_t)kChunk * p.dvp, frags = 3 * kFragQuads * sizeof(quad);
     const size_t one = unit * (sizeof(Record) + 3 * frags + 2 * state + 2 * rows);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
     const size_t units = unit * p.groups;
@@ -441,9 +404,9 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
     p.chunks = plan.chunks;
     p.dvp = plan.dvp;
     p.records = (Record*)ws;
-    p.S = (Frag*)(ws + plan.S);
-    p.St = (Frag*)(ws + plan.St);
-    p.P = (Frag*)(ws + plan.P);
+    p.S = (quad*)(ws + plan.S);
+    p.St = (quad*)(ws + plan.St);
+    p.P = (quad*)(ws + plan.P);
     p.states = (float*)(ws + plan.states);
     p.cotangents = (float*)(ws + plan.cotangents);
     p.U = (float*)(ws + plan.U);

@@ -26,8 +26,6 @@ namespace ttt {
 constexpr int kChunk = 64;
 constexpr float kForget = -1e30f;     // log decays from here down forget everything
 
-typedef uint32_t quad __attribute__((ext_vector_type(4)));
-
 // ---- values as sums of bf16 parts ----------------------------------------
 // An fp32 operand of a product is the exact sum of three bf16 parts (8 + 8 + 8 bits);
 // a bf16 input is one part.  Products of parts are exact in the matrix cores' fp32 sums,
@@ -123,12 +121,13 @@ struct TileLoad {
     static constexpr int N = Tile<TIO, DK>::GRANULES / 256;
     static constexpr int ROW = DK / kGran<TIO>;
     quad q[N];
+    // (columns from `first` of rows of d)
     __device__ __forceinline__ void load(const Rows<const TIO>& src, int t0, int T, int d, bool whole,
-                                         int tid)
+                                         int tid, int first = 0)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = tid + 256 * i, r = e / ROW, col = (e % ROW) * kGran<TIO>;
+            const int e = tid + 256 * i, r = e / ROW, col = first + (e % ROW) * kGran<TIO>;
             q[i] = t0 + r < T ? load_granule(src.at(t0 + r), col, d, whole) : quad{0u, 0u, 0u, 0u};
         }
     }
@@ -197,7 +196,8 @@ constexpr int kFrags = 6;
 __host__ __device__ constexpr int frag_lower(int i, int j) { return i < 2 ? i : 2 * (i - 1) + j; }
 __host__ __device__ constexpr int frag_upper(int i, int j) { return i < 2 ? 2 * i + j : i + 2; }
 
-struct Frag { u32x4 p[3][64]; };              // parts by lanes, 3 KB
+// An operand is its parts, one after the other, 16 bytes for each lane (1 KB a part).
+constexpr int kFragQuads = kFrags * 64;       // of one part of a matrix's operands
 struct Record {                               // decays of a chunk's tokens
     double G[kChunk];                         // sums of the log decays, those that forget left out
     int cuts[kChunk];                         // how many forget, up to and with the token
@@ -211,19 +211,93 @@ __device__ __forceinline__ float pair_decay(const double* G, const int* cuts, in
     return cuts[t] == cuts[s] ? expf((float)(G[t] - G[s])) : 0.f;
 }
 
-__device__ __forceinline__ void store_frag(Frag& f, int lane, f32x4 a, f32x4 b)
+// operand f of N parts each, from result tiles a over b
+template <int N>
+__device__ __forceinline__ void store_frag(quad* to, int f, int lane, f32x4 a, f32x4 b)
 {
-    const Parts<3> s = split<3>(a, b);
+    const Parts<N> s = split<N>(a, b);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) f.p[k][lane] = s.p[k];
+    for (int k = 0; k < N; ++k) to[(f * N + k) * 64 + lane] = __builtin_bit_cast(quad, s.p[k]);
 }
 
 template <int N>
-__device__ __forceinline__ Parts<N> load_frag(const Frag& f, int lane)
+__device__ __forceinline__ Parts<N> load_frag(const quad* from, int f, int lane)
 {
     Parts<N> r;
 #pragma unroll
-    for (int k = 0; k < N; ++k) r.p[k] = f.p[k][lane];
+    for (int k = 0; k < N; ++k) r.p[k] = __builtin_bit_cast(u32x4, from[(f * N + k) * 64 + lane]);
+    return r;
+}
+
+// N quads on their way from memory to LDS, over 256 threads
+template <int N>
+struct LinearLoad {
+    static constexpr int PER = (N + 255) / 256;
+    quad q[PER];
+    __device__ __forceinline__ void load(const quad* from, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (N % 256 == 0 || tid + 256 * i < N) q[i] = from[tid + 256 * i];
+    }
+    __device__ __forceinline__ void put(quad* to, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (N % 256 == 0 || tid + 256 * i < N) to[tid + 256 * i] = q[i];
+    }
+};
+
+// What a scan's workgroup needs of a chunk beside keys and queries: operands of S (3 parts)
+// and P (NP of them), eta, start and end of its tokens, and 64 columns of V or dZ.
+template <typename TIO, int DK, int NP, bool Q>
+struct ChunkTiles {
+    Tile<TIO, DK> k;
+    Tile<TIO, Q ? DK : kGran<TIO>> q;
+    Tile<TIO, 64> v;
+    quad s[3 * kFragQuads], p[NP ? NP * kFragQuads : 1];
+    float eta[kChunk], start[kChunk], end[kChunk];
+};
+
+template <typename TIO, int DK, int NP, bool Q>
+struct ChunkLoad {
+    TileLoad<TIO, DK> k, q;
+    TileLoad<TIO, 64> v;
+    LinearLoad<3 * kFragQuads> s;
+    LinearLoad<NP ? NP * kFragQuads : 1> p;
+    float rec;
+    __device__ __forceinline__ void load(const Rows<const TIO>& K, const Rows<const TIO>& Qr,
+                                         const Rows<const TIO>& V, const quad* S, const quad* P,
+                                         const Record* r, int t0, int T, int dk, int dv, int first,
+                                         bool whole_k, bool whole_v, int tid)
+    {
+        k.load(K, t0, T, dk, whole_k, tid);
+        if constexpr (Q) q.load(Qr, t0, T, dk, whole_k, tid);
+        v.load(V, t0, T, dv, whole_v, tid, first);
+        s.load(S, tid);
+        if constexpr (NP > 0) p.load(P, tid);
+        if (tid < 3 * kChunk) rec = r->eta[tid];   // (eta, start and end lie one after the other)
+    }
+    __device__ __forceinline__ void put(ChunkTiles<TIO, DK, NP, Q>& to, int tid) const
+    {
+        k.put(to.k, tid);
+        if constexpr (Q) q.put(to.q, tid);
+        v.put(to.v, tid);
+        s.put(to.s, tid);
+        if constexpr (NP > 0) p.put(to.p, tid);
+        if (tid < 3 * kChunk) to.eta[tid] = rec;
+    }
+};
+
+// as many buffers of a chunk as LDS holds, up to two
+template <typename TILES> constexpr int kBuffers = 2 * sizeof(TILES) <= 160 * 1024 ? 2 : 1;
+
+template <int N>
+__device__ __forceinline__ f32x4 widen_parts(const Parts<N>& x, bool upper)
+{
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = N - 1; k >= 0; --k) r += widen4(upper ? hi_half(x.p[k]) : lo_half(x.p[k]));
     return r;
 }
 
@@ -236,29 +310,37 @@ __device__ __forceinline__ void store1(uint16_t* p, float v)
     *p = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
 }
 
-// result tile i of a chunk (tokens 16 i + 4 g + v, column `col`): from and to rows of d columns
+// columns f .. f + 3 of a row of d (`fours`: d is a multiple of 4)
 template <typename TIO>
-__device__ __forceinline__ f32x4 load_cl(const Rows<const TIO>& src, int t0, int T, int i, int g, int col,
-                                         int d)
+__device__ __forceinline__ void store4(TIO* row, int f, int d, bool fours, f32x4 x)
 {
-    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (fours) {
+        if (f < d) {
+            if constexpr (sizeof(TIO) == 2) *reinterpret_cast<u32x2*>(row + f) = pack_bf16x4(x);
+            else *reinterpret_cast<f32x4*>(row + f) = x;
+        }
+    } else {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int t = t0 + 16 * i + 4 * g + v;
-        if (t < T && col < d) r[v] = load1(src.at(t) + col);
+        for (int e = 0; e < 4; ++e)
+            if (f + e < d) store1(row + f + e, x[e]);
     }
-    return r;
 }
 
 template <typename TIO>
-__device__ __forceinline__ void store_cl(const Rows<TIO>& dst, int t0, int T, int i, int g, int col, int d,
-                                         f32x4 r)
+__device__ __forceinline__ f32x4 load4(const TIO* row, int f, int d, bool fours)
 {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (fours) {
+        if (f < d) {
+            if constexpr (sizeof(TIO) == 2) x = widen4(*reinterpret_cast<const u32x2*>(row + f));
+            else x = *reinterpret_cast<const f32x4*>(row + f);
+        }
+    } else {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int t = t0 + 16 * i + 4 * g + v;
-        if (t < T && col < d) store1(dst.at(t) + col, r[v]);
+        for (int e = 0; e < 4; ++e)
+            if (f + e < d) x[e] = load1(row + f + e);
     }
+    return x;
 }
 
 // state [dv, dk] fp32, row `col`, features 16 m + 4 g + v

@@ -39,8 +39,8 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s);
 size_t delta_bwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool bf16);
 
 // ---- what the kernels of one pass over some of the heads are given --------------
-struct Frag;
 struct Record;
+typedef uint32_t quad __attribute__((ext_vector_type(4)));
 
 struct DeltaPass {
     DeltaArgs f;
@@ -48,8 +48,7 @@ struct DeltaPass {
     int chunks;              // of 64 tokens
     int dvp;                 // dv up to a multiple of 32
     Record* records;         // [heads][chunks]
-    Frag *S, *P;             // [heads][chunks][6]: of S and P, or of their transposes
-    Frag* St;                // of S's transpose (backward)
+    quad *S, *St, *P;        // operands of S, of its transpose (backward), of P (or its transpose)
     float *states, *cotangents;   // [heads][chunks][DK][dvp]: W^T before a chunk, D^T after it
     float *U, *F;            // [heads][chunks][64][dvp]
 };

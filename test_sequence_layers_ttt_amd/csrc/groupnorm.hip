@@ -45,11 +45,18 @@ __device__ __forceinline__ void store_vec(TIO* p, const float (&y)[V])
     }
 }
 
+// 1 / (1 + exp(-v)) by the hardware's exponential and reciprocal (a last place each, and |v| 2^-24
+// of the exponential for its argument's rounding)
+__device__ __forceinline__ float sigmoid(float v)
+{
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+}
+
 template <int ACT>
 __device__ __forceinline__ float act(float v)
 {
-    if constexpr (ACT == TTT_ACT_SILU) return v / (1.f + expf(-v));
-    if constexpr (ACT == TTT_ACT_GELU) return v * (0.5f * erfcf(-0.70710678f * v));
+    if constexpr (ACT == TTT_ACT_SILU) return v * sigmoid(v);
+    if constexpr (ACT == TTT_ACT_GELU) return v * fmaf(0.5f, erff(0.70710678f * v), 0.5f);
     return v;
 }
 
@@ -58,11 +65,12 @@ template <int ACT>
 __device__ __forceinline__ float dact(float v)
 {
     if constexpr (ACT == TTT_ACT_SILU) {
-        const float y = 1.f / (1.f + expf(-v));
+        const float y = sigmoid(v);
         return fmaf(v * y, 1.f - y, y);
     }
     if constexpr (ACT == TTT_ACT_GELU)
-        return fmaf(v * 0.39894228f, expf(-0.5f * v * v), 0.5f * erfcf(-0.70710678f * v));
+        return fmaf(v * 0.39894228f, __builtin_amdgcn_exp2f(-0.72134752f * v * v),
+                    fmaf(0.5f, erff(0.70710678f * v), 0.5f));
     return 1.f;
 }
 
@@ -70,8 +78,13 @@ __device__ __forceinline__ float dact(float v)
 template <int L>
 __device__ __forceinline__ float lane_sum(float x)
 {
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) x += __shfl_xor(x, o, 64);
+    auto add = [&](int y) { x += __int_as_float(y); };
+    if constexpr (L >= 2) add(__builtin_amdgcn_mov_dpp(__float_as_int(x), kDppQuadXor1, 0xF, 0xF, false));
+    if constexpr (L >= 4) add(__builtin_amdgcn_mov_dpp(__float_as_int(x), kDppQuadXor2, 0xF, 0xF, false));
+    if constexpr (L >= 8) add(__builtin_amdgcn_mov_dpp(__float_as_int(x), kDppRowHalfMirror, 0xF, 0xF, false));
+    if constexpr (L >= 16) add(__builtin_amdgcn_mov_dpp(__float_as_int(x), kDppRowMirror, 0xF, 0xF, false));
+    if constexpr (L >= 32) x += __shfl_xor(x, 16, 64);
+    if constexpr (L >= 64) x += __shfl_xor(x, 32, 64);
     return x;
 }
 
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(256) group_row_fwd_kernel(GroupArgs a, int slo
             v[i] -= mean;
             s = in ? fmaf(v[i], v[i], s) : 0.f;
         }
-        const float rstd = 1.f / sqrtf(fmaf(lane_sum<L>(s), inv, a.eps));
+        const float rstd = __builtin_amdgcn_rsqf(fmaf(lane_sum<L>(s), inv, a.eps));
         if (in) {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = act<ACT>(fmaf(v[i] * rstd, w[i], b[i]));
@@ -200,21 +213,26 @@ __global__ void __launch_bounds__(256) group_row_bwd_kernel(GroupBwdArgs a, int 
     }
 }
 
-// dweight and dbias: column c of all planes [2][C], in fp64, 8 runs of planes a column
-__global__ void __launch_bounds__(256) group_planes_kernel(const float* planes, long long count, int C,
-                                                           float* dweight, float* dbias)
+// dweight and dbias: columns of all planes [2][C] in fp64, 32 runs of planes a column
+__global__ void __launch_bounds__(1024) group_planes_kernel(const float* planes, long long count, int C,
+                                                            float* dweight, float* dbias)
 {
-    __shared__ double part[8][32];
+    __shared__ double part[32][33];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5, at = blockIdx.x * 32 + c;
     double s = 0.0;
-    if (at < 2 * C)
-        for (long long i = k; i < count; i += 8) s += planes[i * 2 * C + at];
+    if (at < 2 * C) {
+#pragma unroll 8
+        for (long long i = k; i < count; i += 32) s += planes[i * 2 * C + at];
+    }
     part[k][c] = s;
     __syncthreads();
-    if (k == 0 && at < 2 * C) {
-        for (int i = 1; i < 8; ++i) s += part[i][c];
-        if (at < C) { if (dweight) dweight[at] = (float)s; }
-        else if (dbias) dbias[at - C] = (float)s;
+    // the columns' 32 sums lie across a half wave now
+    double t = part[c][k];
+    for (int o = 1; o < 32; o <<= 1) t += __shfl_xor(t, o, 64);
+    const int to = blockIdx.x * 32 + k;
+    if (c == 0 && to < 2 * C) {
+        if (to < C) { if (dweight) dweight[to] = (float)t; }
+        else if (dbias) dbias[to - C] = (float)t;
     }
 }
 
@@ -325,26 +343,43 @@ __global__ void __launch_bounds__(256) group_moments_kernel(GroupArgs a, int par
     }
 }
 
-// one wave per (row, group): mean and rstd from its channels' and parts' moments
-__global__ void __launch_bounds__(64) group_statistics_kernel(GroupArgs a, int parts, const float* planes)
+// sum of 256 threads' values, in each
+__device__ __forceinline__ double block_sum(double x, double* room)
 {
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (room[0] + room[1]) + (room[2] + room[3]);
+}
+
+// one workgroup per (row, group): mean and rstd from its channels' and parts' moments, each
+// read twice: the mean first, then the squares about it
+__global__ void __launch_bounds__(256) group_statistics_kernel(GroupArgs a, int parts, const float* planes)
+{
+    __shared__ double room[4];
     const long long row = blockIdx.x / a.G;
     const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
     const long long each = (a.S + parts - 1) / parts;
-    float n = 0.f, mean = 0.f, m2 = 0.f;
-    for (long long e = threadIdx.x; e < (long long)parts * per; e += 64) {
-        const int part = (int)(e / per), ch = group * per + (int)(e % per);
-        const long long have = min(each, a.S - each * part);
-        const float* from = planes + ((size_t)row * parts + part) * 2 * a.C + ch;
-        if (have > 0) join_moments(n, mean, m2, (float)have, from[0], from[a.C]);
+    const float* from = planes + (size_t)row * parts * 2 * a.C + group * per;
+    const int entries = parts * per;
+    const double n = (double)a.S * per;
+    auto have = [&](int part) { return (double)max(0ll, min(each, a.S - each * part)); };
+    double s = 0.0;
+    for (int e = threadIdx.x; e < entries; e += 256)
+        s += have(e / per) * from[(size_t)(e / per) * 2 * a.C + e % per];
+    const double mean = block_sum(s, room) / n;
+    s = 0.0;
+    for (int e = threadIdx.x; e < entries; e += 256) {
+        const double h = have(e / per);
+        const float* p = from + (size_t)(e / per) * 2 * a.C + e % per;
+        const double d = p[0] - mean;
+        if (h > 0.0) s += p[a.C] + h * d * d;
     }
-    for (int o = 1; o < 64; o <<= 1) {
-        const float nb = __shfl_down(n, o, 64), mb = __shfl_down(mean, o, 64), qb = __shfl_down(m2, o, 64);
-        join_moments(n, mean, m2, nb, mb, qb);
-    }
+    s = block_sum(s, room) / n;
     if (threadIdx.x == 0) {
-        a.mean[blockIdx.x] = mean;
-        a.rstd[blockIdx.x] = 1.f / sqrtf(m2 / n + a.eps);
+        a.mean[blockIdx.x] = (float)mean;
+        a.rstd[blockIdx.x] = (float)(1.0 / sqrt(s + (double)a.eps));
     }
 }
 
@@ -428,24 +463,23 @@ __global__ void __launch_bounds__(256) group_sums_kernel(GroupBwdArgs a, int par
     }
 }
 
-// one wave per (row, group): means of u and u n
-__global__ void __launch_bounds__(64) group_means_kernel(GroupBwdArgs a, int parts, const float* planes,
-                                                         float* means)
+// one workgroup per (row, group): means of u and u n
+__global__ void __launch_bounds__(256) group_means_kernel(GroupBwdArgs a, int parts, const float* planes,
+                                                          float* means)
 {
+    __shared__ double room[4];
     const long long row = blockIdx.x / a.G;
     const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
+    const float* from = planes + (size_t)row * parts * 2 * a.C + group * per;
     double m1 = 0.0, m2 = 0.0;
-    for (long long e = threadIdx.x; e < (long long)parts * per; e += 64) {
-        const int part = (int)(e / per), ch = group * per + (int)(e % per);
-        const float* from = planes + ((size_t)row * parts + part) * 2 * a.C + ch;
-        const double w = a.weight ? a.weight[ch] : 1.f;
-        m2 += w * from[0];
-        m1 += w * from[a.C];
+    for (int e = threadIdx.x; e < parts * per; e += 256) {
+        const float* p = from + (size_t)(e / per) * 2 * a.C + e % per;
+        const double w = a.weight ? a.weight[group * per + e % per] : 1.f;
+        m2 += w * p[0];
+        m1 += w * p[a.C];
     }
-    for (int o = 1; o < 64; o <<= 1) {
-        m1 += __shfl_xor(m1, o, 64);
-        m2 += __shfl_xor(m2, o, 64);
-    }
+    m1 = block_sum(m1, room);
+    m2 = block_sum(m2, room);
     if (threadIdx.x == 0) {
         const double n = (double)a.S * per;
         means[2 * (size_t)blockIdx.x] = (float)(m1 / n);
@@ -523,7 +557,7 @@ Shape shape_of(long long N, long long S, int C, int G, bool bf16)
         h.x = (int)((threads + 255) / 256);
         // workgroups enough to fill the card several times over, and no more planes than that
         const long long steps = (N + h.slots - 1) / h.slots;
-        h.y = (int)std::min<long long>(steps, std::max(1, 2048 / h.x));
+        h.y = (int)std::min<long long>(steps, std::max(1, 1024 / h.x));
         h.planes = (size_t)h.y * h.slots;
         return h;
     }
@@ -532,7 +566,7 @@ Shape shape_of(long long N, long long S, int C, int G, bool bf16)
     h.slots = vectors < 256 ? 256 / vectors : 1;
     h.x = (vectors + 255) / 256;
     const long long most = std::max<long long>(1, S / (16ll * h.slots));
-    h.parts = (int)std::min<long long>(most, std::max<long long>(1, 2048 / (N * h.x)));
+    h.parts = (int)std::min<long long>(most, std::max<long long>(1, 1024 / (N * h.x)));
     h.planes = (size_t)N * h.parts;
     return h;
 }
@@ -582,7 +616,7 @@ hipError_t fwd_as(const GroupArgs& a, const Shape& h, hipStream_t s)
     float* planes = (float*)a.workspace;
     const dim3 grid((unsigned)(h.x * a.N), h.parts);
     group_moments_kernel<TIO, V><<<grid, 256, 0, s>>>(a, h.parts, planes);
-    group_statistics_kernel<<<(unsigned)(a.N * a.G), 64, 0, s>>>(a, h.parts, planes);
+    group_statistics_kernel<<<(unsigned)(a.N * a.G), 256, 0, s>>>(a, h.parts, planes);
     if (a.act == TTT_ACT_SILU) group_apply_kernel<TIO, V, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, h.parts);
     else if (a.act == TTT_ACT_GELU) group_apply_kernel<TIO, V, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, h.parts);
     else group_apply_kernel<TIO, V, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, h.parts);
@@ -594,7 +628,7 @@ void slab_bwd(const GroupBwdArgs& a, const Shape& h, float* planes, float* means
 {
     const dim3 grid((unsigned)(h.x * a.N), h.parts);
     group_sums_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, planes);
-    group_means_kernel<<<(unsigned)(a.N * a.G), 64, 0, s>>>(a, h.parts, planes, means);
+    group_means_kernel<<<(unsigned)(a.N * a.G), 256, 0, s>>>(a, h.parts, planes, means);
     group_dx_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, means);
 }
 
@@ -613,7 +647,7 @@ hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
         else slab_bwd<TIO, V, TTT_ACT_NONE>(a, h, planes, means, s);
     }
     if (sums)
-        group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 256, 0, s>>>(planes, (long long)h.planes, a.C,
+        group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 1024, 0, s>>>(planes, (long long)h.planes, a.C,
                                                                             a.dweight, a.dbias);
     return hipGetLastError();
 }
@@ -645,7 +679,7 @@ hipError_t launch_groupnorm_bwd(const GroupBwdArgs& a, hipStream_t s)
 {
     if (a.N == 0 || a.S == 0) {
         if (a.dweight || a.dbias)
-            group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 256, 0, s>>>(nullptr, 0, a.C, a.dweight,
+            group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 1024, 0, s>>>(nullptr, 0, a.C, a.dweight,
                                                                                 a.dbias);
         return hipGetLastError();
     }
