@@ -237,40 +237,74 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
         const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
         if (n + 1 < a.chunks) fetch(n + 1);
         if (works) {
-            f32x4 r[4], z[4];
+            typedef Parts<kParts<TIO>> In;
+            In kt[J][4];
+            Parts<3> S[kFrags], x[2];
+            f32x4 r[4], z[4], v[4], eta[4], start[4], ends[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = z[i] = zero;
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const Parts<3> wp = split<3>(W[2 * j], W[2 * j + 1]);
+                for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    r[i] = mma(by_token(t.k, i, j, lane), wp, r[i]);
-                    if constexpr (!SAVE) z[i] = mma<OZ>(wp, by_token(t.q, i, j, lane), z[i]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
+                ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
             }
-            f32x4 eta[4];
-            Parts<3> x[2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const auto v = by_feature(t.v, w, j, lane);
-#pragma unroll
-                for (int i = 2 * j; i < 2 * j + 2; ++i)
-                    r[i] = widen_parts(v, i & 1) - *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g) * r[i];
-                x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
+                const In p = by_feature(t.v, w, j, lane);
+                v[2 * j] = widen_parts(p, false);
+                v[2 * j + 1] = widen_parts(p, true);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(t.s, f, lane);
+            const float all = t.start[kChunk - 1];
+            reads_before();
+
 #pragma unroll
-                for (int j = 0; j <= i / 2; ++j) r[i] = mma(load_frag<3>(t.s, frag_lower(i, j), lane), x[j], r[i]);
+            for (int i = 0; i < 4; ++i) r[i] = z[i] = zero;
+            Parts<3> wp[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                wp[j] = split<3>(W[2 * j], W[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = mma(kt[j][i], wp[j], r[i]);
+            }
             if constexpr (SAVE) {
                 float* st = a.states + (unit0 + n) * DK * a.dvp + col;
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st[(size_t)(16 * m + 4 * g + e) * a.dvp] = W[m][e];
+            }
+            In kf[M][2];
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
+            reads_before();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
+            In qt[J][4];
+            Parts<NZ ? NZ : 1> P[kFrags], u[2];
+            if constexpr (!SAVE) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qt[j][i] = by_token(t.q, i, j, lane);
+#pragma unroll
+                for (int f = 0; f < kFrags; ++f) P[f] = load_frag<NZ>(t.p, f, lane);
+                reads_before();
+            }
+            if constexpr (SAVE) {
                 float* u = a.U + (unit0 + n) * kChunk * a.dvp + col;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -279,31 +313,38 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] *= eta[i];
-            const float all = t.start[kChunk - 1];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const f32x4 ea = *reinterpret_cast<const f32x4*>(t.end + 32 * j + 4 * g);
-                const f32x4 eb = *reinterpret_cast<const f32x4*>(t.end + 32 * j + 16 + 4 * g);
-                x[j] = split<3>(ea * r[2 * j], eb * r[2 * j + 1]);
-            }
+            for (int j = 0; j < 2; ++j)
+                x[j] = split<3>(ends[2 * j] * r[2 * j], ends[2 * j + 1] * r[2 * j + 1]);
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                W[m] *= all;
+            for (int m = 0; m < M; ++m) W[m] *= all;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) W[m] = mma(by_feature(t.k, m, j, lane), x[j], W[m]);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int m = 0; m < M; ++m) W[m] = mma(kf[m][j], x[j], W[m]);
             if constexpr (!SAVE) {
-                Parts<NZ> u[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) u[j] = split<NZ>(r[2 * j], r[2 * j + 1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    z[i] *= t.start[16 * i + c];
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int j = 0; j <= i / 2; ++j)
-                        z[i] = mma<OZ>(u[j], load_frag<NZ>(t.p, frag_lower(i, j), lane), z[i]);
-                    const int token = n * kChunk + 16 * i + c;
-                    if (token < T) store4(Z.at(token), first + 16 * w + 4 * g, dv, fours, z[i]);
+                    for (int i = 0; i < 4; ++i) z[i] = mma<OZ>(wp[j], qt[j][i], z[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] *= t.start[16 * i + c];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 2 * j; i < 4; ++i) z[i] = mma<OZ>(u[j], P[frag_lower(i, j)], z[i]);
+                const int token = n * kChunk + c;
+                if (fours && first + 64 <= dv && (n + 1) * kChunk <= T) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, true, z[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (token + 16 * i < T)
+                            store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, fours, z[i]);
                 }
             }
         }

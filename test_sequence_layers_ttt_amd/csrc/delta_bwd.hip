@@ -66,69 +66,92 @@ __global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
         if (n > 0) fetch(n - 1);
         if (works) {
             const size_t unit = unit0 + n;
+            typedef Parts<NP> In;
+            In kt[J][4], zp[2];
+            Parts<3> P[kFrags], x[2], y[2];
+            f32x4 f[4], z[4], eta[4], start[4], ends[4];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
+                ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
+#pragma unroll
+            for (int e = 0; e < kFrags; ++e) P[e] = load_frag<3>(t.p, e, lane);
+            const float all = t.start[kChunk - 1];
+            reads_before();
+
             float* out = a.cotangents + unit * DK * a.dvp + col;
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) out[(size_t)(16 * m + 4 * g + e) * a.dvp] = D[m][e];
-
-            f32x4 f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = zero;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = mma(by_token(t.k, i, j, lane), dp, f[i]);
+                for (int i = 0; i < 4; ++i) f[i] = mma(kt[j][i], dp, f[i]);
             }
-            Parts<NP> zp[2];
+            Parts<3> S[kFrags];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
+            for (int e = 0; e < kFrags; ++e) S[e] = load_frag<3>(t.s, e, lane);
+            reads_before();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[i] *= *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
+            for (int i = 0; i < 4; ++i) f[i] *= ends[i];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (j >= i / 2) f[i] = mma(load_frag<3>(t.p, frag_upper(i, j), lane), zp[j], f[i]);
-            }
-            f32x4 eta[4];
-            Parts<3> x[2], y[2];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(P[frag_upper(i, j)], zp[j], f[i]);
+            In kf[M][2];
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
+            reads_before();
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 x[j] = split<3>(-(eta[2 * j] * f[2 * j]), -(eta[2 * j + 1] * f[2 * j + 1]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (j >= i / 2) f[i] = mma(load_frag<3>(t.s, frag_upper(i, j), lane), x[j], f[i]);
+                for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(S[frag_upper(i, j)], x[j], f[i]);
+            In qf[M][2];
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) qf[m][j] = by_feature(t.q, m, j, lane);
+            reads_before();
 
             float* F = a.F + unit * kChunk * a.dvp + col;
-            f32x4 z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) F[(size_t)(16 * i + 4 * g + e) * a.dvp] = f[i][e];
-                const f32x4 start = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
-                f[i] *= -(start * eta[i]);
-                z[i] = start * widen_parts(zp[i / 2], i & 1);
+                f[i] *= -(start[i] * eta[i]);
+                z[i] = start[i] * widen_parts(zp[i / 2], i & 1);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 x[j] = split<3>(f[2 * j], f[2 * j + 1]);
                 y[j] = split<3>(z[2 * j], z[2 * j + 1]);
             }
-            const float all = t.start[kChunk - 1];
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                D[m] *= all;
+            for (int m = 0; m < M; ++m) D[m] *= all;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    D[m] = mma(by_feature(t.k, m, j, lane), x[j], D[m]);
-                    D[m] = mma(by_feature(t.q, m, j, lane), y[j], D[m]);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    D[m] = mma(kf[m][j], x[j], D[m]);
+                    D[m] = mma(qf[m][j], y[j], D[m]);
                 }
-            }
         }
         if constexpr (NB == 1) __syncthreads();
         if (n > 0) next.put(tiles[NB == 2 ? (n - 1) & 1 : 0], tid);

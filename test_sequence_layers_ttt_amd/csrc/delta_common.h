@@ -121,6 +121,16 @@ struct TileLoad {
     static constexpr int N = Tile<TIO, DK>::GRANULES / 256;
     static constexpr int ROW = DK / kGran<TIO>;
     quad q[N];
+    // a tile that lies within the rows and columns
+    __device__ __forceinline__ void load_inside(const Rows<const TIO>& src, int t0, int tid, int first = 0)
+    {
+        const TIO* p = src.at(t0) + ((size_t)(tid / ROW) * src.stride + first + (tid % ROW) * kGran<TIO>);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            q[i] = *reinterpret_cast<const quad*>(p);
+            p += 256 / ROW * src.stride;
+        }
+    }
     // (columns from `first` of rows of d)
     __device__ __forceinline__ void load(const Rows<const TIO>& src, int t0, int T, int d, bool whole,
                                          int tid, int first = 0)
@@ -271,9 +281,15 @@ struct ChunkLoad {
                                          const Record* r, int t0, int T, int dk, int dv, int first,
                                          bool whole_k, bool whole_v, int tid)
     {
-        k.load(K, t0, T, dk, whole_k, tid);
-        if constexpr (Q) q.load(Qr, t0, T, dk, whole_k, tid);
-        v.load(V, t0, T, dv, whole_v, tid, first);
+        if (whole_k && whole_v && dk == DK && first + 64 <= dv && t0 + kChunk <= T) {
+            k.load_inside(K, t0, tid);
+            if constexpr (Q) q.load_inside(Qr, t0, tid);
+            v.load_inside(V, t0, tid, first);
+        } else {
+            k.load(K, t0, T, dk, whole_k, tid);
+            if constexpr (Q) q.load(Qr, t0, T, dk, whole_k, tid);
+            v.load(V, t0, T, dv, whole_v, tid, first);
+        }
         s.load(S, tid);
         if constexpr (NP > 0) p.load(P, tid);
         if (tid < 3 * kChunk) rec = r->eta[tid];   // (eta, start and end lie one after the other)
@@ -288,6 +304,10 @@ struct ChunkLoad {
         if (tid < 3 * kChunk) to.eta[tid] = rec;
     }
 };
+
+// LDS reads stay before it: operands are read a product ahead of the one that takes them (a wave
+// has its SIMD to itself, so nothing else covers a read's latency)
+__device__ __forceinline__ void reads_before() { asm volatile("" ::: "memory"); }
 
 // as many buffers of a chunk as LDS holds, up to two
 template <typename TILES> constexpr int kBuffers = 2 * sizeof(TILES) <= 160 * 1024 ? 2 : 1;
