@@ -37,9 +37,7 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
     };
     __shared__ __align__(16) Room room;
     __shared__ __align__(16) float Lm[kChunk * LD];
-    __shared__ double G[kChunk];
-    __shared__ int cuts[kChunk];
-    __shared__ __align__(16) float eta[kChunk];
+    __shared__ __align__(16) float hi[kChunk], lo[kChunk], eta[kChunk];
     const Tile<TIO, DK>&tk = room.in.k, &tq = room.in.q;
     float* Sm = room.S;
 
@@ -60,22 +58,23 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
         const int t = t0 + lane;
         const Rows<const float> rg(a.f.g, b, h, a.f.H, T, 1, a.f.tokens_first);
         const Rows<const float> re(a.f.eta, b, h, a.f.H, T, 1, a.f.tokens_first);
-        const float gt = a.f.g && t < T ? *rg.at(t) : 0.f;
+        const float gt = a.f.g && t < T ? *rg.at(t) : 0.f;   // (tokens past the end change nothing)
         const float et = t < T ? (a.f.eta ? *re.at(t) : a.f.eta_scalar) : 0.f;
-        int n = gt <= kForget;
         // (sums in fp64: differences of far sums have to keep their own digits)
-        double x = n ? 0.0 : (double)gt;
+        double x = (double)gt * 1.4426950408889634;
+        const bool none = x <= kLeast;
+        if (none) x = kLeast;
         for (int o = 1; o < 64; o <<= 1) {
             const double y = shift_up(x, o);
-            const int m = __shfl_up(n, o, 64);
-            if (lane >= o) { x += y; n += m; }
+            if (lane >= o) x += y;
         }
-        G[lane] = x; cuts[lane] = n; eta[lane] = et;
-        const double xl = __shfl(x, 63, 64);
-        const int nl = __shfl(n, 63, 64);
-        rec.G[lane] = x; rec.cuts[lane] = n; rec.eta[lane] = et;
-        rec.start[lane] = n == 0 ? expf((float)x) : 0.f;
-        rec.end[lane] = n == nl ? expf((float)(xl - x)) : 0.f;
+        const double all = __shfl(x, 63, 64);
+        const float h = (float)x, l = (float)(x - (double)h);
+        hi[lane] = h; lo[lane] = l; eta[lane] = et;
+        rec.hi[lane] = h; rec.lo[lane] = l; rec.eta[lane] = et;
+        rec.start[lane] = __builtin_amdgcn_exp2f(h);
+        rec.end[lane] = __builtin_amdgcn_exp2f((float)(all - x));
+        rec.forgets[lane] = gt * 1.4426950408889634f < -150.f;
     }
     lk.put(room.in.k, tid);
     lq.put(room.in.q, tid);
@@ -84,10 +83,15 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
     // row tile w of L, and of P: rows s by column t (P's operand as it lies) up to the diagonal,
     // or rows t by column s from the diagonal on (its transpose's)
     f32x4 p[4];
+    const f32x4 hw = *reinterpret_cast<const f32x4*>(hi + 16 * w + 4 * g);
+    const f32x4 lw = *reinterpret_cast<const f32x4*>(lo + 16 * w + 4 * g);
+    const float hc = hi[16 * w + c], lc = lo[16 * w + c];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f32x4 kk = zero;
         p[i] = zero;
+        const f32x4 hr = *reinterpret_cast<const f32x4*>(hi + 16 * i + 4 * g);
+        const f32x4 lr = *reinterpret_cast<const f32x4*>(lo + 16 * i + 4 * g);
         if (i <= w) {
 #pragma unroll
             for (int j = 0; j < DK / 32; ++j) {
@@ -95,14 +99,12 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
                 kk = mma(by_token(tk, w, j, lane), s, kk);
                 if constexpr (!BACKWARD) p[i] = mma(s, by_token(tq, w, j, lane), p[i]);
             }
+            const float hs = hi[16 * i + c], ls = lo[16 * i + c];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int t = 16 * w + 4 * g + v, s = 16 * i + c;
-                kk[v] = s < t ? kk[v] * pair_decay(G, cuts, t, s) : 0.f;
-                if constexpr (!BACKWARD) {
-                    const int to = 16 * w + c, from = 16 * i + 4 * g + v;
-                    p[i][v] = from <= to ? p[i][v] * pair_decay(G, cuts, to, from) : 0.f;
-                }
+                kk[v] = 16 * i + c < 16 * w + 4 * g + v ? kk[v] * pair_decay(hw[v], lw[v], hs, ls) : 0.f;
+                if constexpr (!BACKWARD)
+                    p[i][v] = 16 * i + 4 * g + v <= 16 * w + c ? p[i][v] * pair_decay(hc, lc, hr[v], lr[v]) : 0.f;
             }
             put_cl<LD>(Lm + 16 * w * LD, 16 * i, lane, kk);
         }
@@ -112,10 +114,8 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
                 for (int j = 0; j < DK / 32; ++j)
                     p[i] = mma(by_token(tq, i, j, lane), by_token(tk, w, j, lane), p[i]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int t = 16 * i + 4 * g + v, s = 16 * w + c;
-                    p[i][v] = s <= t ? p[i][v] * pair_decay(G, cuts, t, s) : 0.f;
-                }
+                for (int v = 0; v < 4; ++v)
+                    p[i][v] = 16 * w + c <= 16 * i + 4 * g + v ? p[i][v] * pair_decay(hr[v], lr[v], hc, lc) : 0.f;
             }
         }
     }

@@ -20,6 +20,7 @@ namespace {
 struct BwdPass {
     DeltaPass p;
     DeltaBwdArgs a;
+    float *dK, *dQ;          // [heads][chunks][64][DK] where heads share keys, else nullptr
 };
 
 // ---- the scan from the last chunk to the first ---------------------------------------
@@ -163,28 +164,57 @@ __global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
 }
 
 // ---- gradients of a chunk ------------------------------------------------------------
-// One workgroup of four waves per chunk and head of keys, going through the heads of values
-// that share it.  Wave w has the gradients of tokens 16 w .. 16 w + 15, transposed: tokens
+// One workgroup of four waves per chunk and head of values (where heads share keys, dQ and dK
+// go to fp32 planes that another kernel adds up).  Wave w has the gradients of tokens 16 w .. 16 w + 15, transposed: tokens
 // in the lanes, features down the result tiles.  The 64 x 64 products over the columns
 // (dZ u^T and dV u^T, both ways up) come out as operands of what follows, as they lie.
+// The planes that the scans left (U, F, and the states and their gradients) are taken 32
+// columns at a time: each is loaded once, split into parts by the wave that loads it and
+// handed to the others as operands in LDS, while the next 32 columns are on their way.
 template <typename TIO, int DK>
 __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
 {
-    constexpr int NP = kParts<TIO>, M = DK / 16;
+    constexpr int NP = kParts<TIO>, M = DK / 16, MW = (M + 3) / 4;
     const DeltaPass& a = q_.p;
     __shared__ __align__(16) Tile<TIO, DK> tk;
     __shared__ __align__(16) Tile<TIO, DK> tq;
-    __shared__ double G[kChunk], across[4];
-    __shared__ int cuts[kChunk];
-    __shared__ float eta[kChunk], start[kChunk], end[kChunk], dG[kChunk];
+    __shared__ __align__(16) quad fu[4 * 3 * 64], fv[4 * 3 * 64], fz[4 * NP * 64], fw[M * 3 * 64], fd[M * 3 * 64];
+    __shared__ double across[4];
+    __shared__ __align__(16) float hi[kChunk], lo[kChunk];
+    __shared__ float dG[kChunk];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int share = a.f.H / a.f.Hk, chunk = blockIdx.x % a.chunks, group = blockIdx.x / a.chunks;
-    const int key = a.head0 / share + group, b = key / a.f.Hk, hk = key % a.f.Hk;
+    const int chunk = blockIdx.x % a.chunks, local = blockIdx.x / a.chunks, head = a.head0 + local;
+    const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
+    const size_t unit = (size_t)local * a.chunks + chunk;
     const int T = a.f.T, dk = a.f.dk, dv = a.f.dv, dvp = a.dvp, t0 = chunk * kChunk;
-    const int own = 16 * w + c;
-    const bool whole = dk % kGran<TIO> == 0, fours = dv % 4 == 0;
+    const int own = 16 * w + c, steps = dvp / 32;
+    const bool whole = dk % kGran<TIO> == 0, fours = dv % 4 == 0, inside = t0 + own < T;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+
+    // 32 columns on their way: this wave's rows of U, F and dZ, and of the states' tiles w, w + 4
+    f32x4 lu[2], lf[2], lz[2], lw[MW][2], ld[MW][2];
+    const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
+    auto fetch = [&](int j) {
+        const size_t at = 32 * j + 4 * g;
+        const float* u = a.U + (unit * kChunk + own) * dvp + at;
+        const float* f = a.F + (unit * kChunk + own) * dvp + at;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            lu[e] = *reinterpret_cast<const f32x4*>(u + 16 * e);
+            lf[e] = *reinterpret_cast<const f32x4*>(f + 16 * e);
+            lz[e] = inside ? load4(dZ.at(t0 + own), 32 * j + 16 * e + 4 * g, dv, fours) : zero;
+#pragma unroll
+            for (int m = 0; m < MW; ++m)
+                if (w + 4 * m < M) {
+                    const size_t row = (unit * DK + 16 * (w + 4 * m) + c) * dvp + at + 16 * e;
+                    lw[m][e] = *reinterpret_cast<const f32x4*>(a.states + row);
+                    ld[m][e] = *reinterpret_cast<const f32x4*>(a.cotangents + row);
+                }
+        }
+    };
+    fetch(0);
     {
         TileLoad<TIO, DK> lk, lq;
         const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
@@ -194,176 +224,197 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
         lk.put(tk, tid);
         lq.put(tq, tid);
     }
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 sumq[M], sumk[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m) sumq[m] = sumk[m] = zero;
+    const Record& rec = a.records[unit];
+    const Rows<TIO> dV((TIO*)q_.a.dV, b, h, a.f.H, T, dv, a.f.tokens_first);
+    const float eo = rec.eta[own], so = rec.start[own], no = rec.end[own], all = rec.start[kChunk - 1];
 
-    for (int r = 0; r < share; ++r) {
-        const int local = group * share + r, h = hk * share + r;
-        const size_t unit = (size_t)local * a.chunks + chunk;
-        const Record& rec = a.records[unit];
-        __syncthreads();
-        if (tid < kChunk) {
-            G[tid] = rec.G[tid];
-            cuts[tid] = rec.cuts[tid];
-            eta[tid] = rec.eta[tid];
-            start[tid] = rec.start[tid];
-            end[tid] = rec.end[tid];
+    f32x4 p[4], pt[4], l[4], lt[4], aw[M], av[M], ad[M];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pt[i] = l[i] = lt[i] = zero;
+#pragma unroll
+    for (int m = 0; m < M; ++m) aw[m] = av[m] = ad[m] = zero;
+    float de = 0.f, kept = 0.f;
+    for (int j = 0; j < steps; ++j) {
+        f32x4 u[2], v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            u[e] = eo * lu[e];
+            v[e] = eo * lf[e];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) de = fmaf(lu[e][k], lf[e][k], de);
+            if (inside) store4(dV.at(t0 + own), 32 * j + 16 * e + 4 * g, dv, fours, v[e]);
         }
+        const Parts<3> uo = split<3>(u[0], u[1]), vo = split<3>(v[0], v[1]);
+        const Parts<NP> zo = split<NP>(lz[0], lz[1]);
+        __syncthreads();               // (the columns before have been read)
+        if (j == 0 && tid < kChunk) {
+            hi[tid] = rec.hi[tid];
+            lo[tid] = rec.lo[tid];
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            fu[(3 * w + k) * 64 + lane] = __builtin_bit_cast(quad, uo.p[k]);
+            fv[(3 * w + k) * 64 + lane] = __builtin_bit_cast(quad, vo.p[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) fz[(NP * w + k) * 64 + lane] = __builtin_bit_cast(quad, zo.p[k]);
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+            if (w + 4 * m < M) {
+                store_frag<3>(fw, w + 4 * m, lane, lw[m][0], lw[m][1]);
+                store_frag<3>(fd, w + 4 * m, lane, ld[m][0], ld[m][1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) kept = fmaf(lw[m][e][k], ld[m][e][k], kept);
+            }
         __syncthreads();
-        const float* U = a.U + unit * kChunk * dvp;
-        const float* F = a.F + unit * kChunk * dvp;
-        const float* W0 = a.states + unit * DK * dvp;
-        const float* D = a.cotangents + unit * DK * dvp;
-        const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
-        const Rows<TIO> dV((TIO*)q_.a.dV, b, h, a.f.H, T, dv, a.f.tokens_first);
-
-        // rows `row` of a [.., dvp] fp32 plane as an operand over the columns 32 j ..
-        auto plane = [&](const float* X, int row, int j, float by) {
-            const float* p = X + (size_t)row * dvp + 32 * j + 4 * g;
-            return split<3>(by * *reinterpret_cast<const f32x4*>(p),
-                            by * *reinterpret_cast<const f32x4*>(p + 16));
-        };
-        auto four = [&](int t, int f) {   // of dZ
-            return t0 + t < T ? load4(dZ.at(t0 + t), f, dv, fours) : zero;
-        };
-        auto zrow = [&](int t, int j) {
-            return split<NP>(four(t, 32 * j + 4 * g), four(t, 32 * j + 16 + 4 * g));
-        };
-
-        f32x4 p[4], pt[4], l[4], lt[4], aw[M], av[M], ad[M];
+        if (j + 1 < steps) fetch(j + 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = pt[i] = l[i] = lt[i] = zero;
-#pragma unroll
-        for (int m = 0; m < M; ++m) aw[m] = av[m] = ad[m] = zero;
-        float de = 0.f;
-        const float eo = eta[own];
-        for (int j = 0; j < dvp / 32; ++j) {
-            {
-                const float* x = U + (size_t)own * dvp + 32 * j + 4 * g;
-                const float* y = F + (size_t)own * dvp + 32 * j + 4 * g;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) de = fmaf(x[e], y[e], fmaf(x[16 + e], y[16 + e], de));
-                if (t0 + own < T) {
-                    const f32x4 a4 = *reinterpret_cast<const f32x4*>(y), b4 = *reinterpret_cast<const f32x4*>(y + 16);
-                    store4(dV.at(t0 + own), 32 * j + 4 * g, dv, fours, eo * a4);
-                    store4(dV.at(t0 + own), 32 * j + 16 + 4 * g, dv, fours, eo * b4);
-                }
+        for (int i = 0; i < 4; ++i) {
+            if (i <= w) {
+                const Parts<3> x = load_frag<3>(fu, i, lane);
+                pt[i] = mma(x, zo, pt[i]);
+                lt[i] = mma(x, vo, lt[i]);
             }
-            const Parts<3> uo = plane(U, own, j, eo), vo = plane(F, own, j, eo);
-            const Parts<NP> zo = zrow(own, j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 16 * i + c;
-                if (i <= w) {
-                    const Parts<3> u = plane(U, row, j, eta[row]);
-                    pt[i] = mma(u, zo, pt[i]);
-                    lt[i] = mma(u, vo, lt[i]);
-                }
-                if (i >= w) {
-                    p[i] = mma(zrow(row, j), uo, p[i]);
-                    l[i] = mma(plane(F, row, j, eta[row]), uo, l[i]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const Parts<3> s = plane(W0, 16 * m + c, j, 1.f);
-                aw[m] = mma(s, zo, aw[m]);
-                av[m] = mma(s, vo, av[m]);
-                ad[m] = mma(plane(D, 16 * m + c, j, 1.f), uo, ad[m]);
+            if (i >= w) {
+                p[i] = mma(load_frag<NP>(fz, i, lane), uo, p[i]);
+                l[i] = mma(load_frag<3>(fv, i, lane), uo, l[i]);
             }
         }
-        // pt, lt: rows s, column t = own; p, l: rows t, column s = own
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 16 * i + 4 * g + e;
-                const float before = row <= own ? pair_decay(G, cuts, own, row) : 0.f;
-                const float after = row >= own ? pair_decay(G, cuts, row, own) : 0.f;
-                pt[i][e] = row <= own ? pt[i][e] * before : 0.f;
-                lt[i][e] = row < own ? -lt[i][e] * before : 0.f;
-                p[i][e] = row >= own ? p[i][e] * after : 0.f;
-                l[i][e] = row > own ? -l[i][e] * after : 0.f;
-            }
-        float wrote = 0.f;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            aw[m] *= start[own];
-            av[m] *= -start[own];
-            ad[m] *= end[own];
-            const f32x4 k4 = token4(tk, own, 16 * m + 4 * g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wrote = fmaf(k4[e], ad[m][e], wrote);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (2 * j <= w) {
-                const Parts<3> x = split<3>(pt[2 * j], pt[2 * j + 1]), y = split<3>(lt[2 * j], lt[2 * j + 1]);
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const Parts<NP> kf = by_feature(tk, m, j, lane);
-                    aw[m] = mma(kf, x, aw[m]);
-                    av[m] = mma(kf, y, av[m]);
-                }
-            }
-            if (2 * j + 1 >= w) {
-                const Parts<3> x = split<3>(p[2 * j], p[2 * j + 1]), y = split<3>(l[2 * j], l[2 * j + 1]);
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    ad[m] = mma(by_feature(tq, m, j, lane), x, ad[m]);
-                    ad[m] = mma(by_feature(tk, m, j, lane), y, ad[m]);
-                }
-            }
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const f32x4 k4 = token4(tk, own, 16 * m + 4 * g), q4 = token4(tq, own, 16 * m + 4 * g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sum = fmaf(q4[e], aw[m][e], fmaf(k4[e], av[m][e] - ad[m][e], sum));
-            sumq[m] += aw[m];
-            sumk[m] += av[m] + ad[m];
-        }
-        // <D, W'> = start_C <D, W> + sum of k_s.(written part of dK_s)
-        float kept = 0.f;
-        for (int e = tid; e < DK * dvp; e += 256) kept = fmaf(D[e], W0[e], kept);
-        double cross = (double)kept * start[kChunk - 1] + wrote;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) cross += __shfl_xor(cross, o, 64);
-        sum += __shfl_xor(sum, 16, 64);
-        sum += __shfl_xor(sum, 32, 64);
-        de += __shfl_xor(de, 16, 64);
-        de += __shfl_xor(de, 32, 64);
-        if (g == 0) {
-            dG[own] = sum;
-            const Rows<float> o(q_.a.deta, b, h, a.f.H, T, 1, a.f.tokens_first);
-            if (q_.a.deta && t0 + own < T) *o.at(t0 + own) = de;
-        }
-        if (lane == 0) across[w] = cross;
-        __syncthreads();
-        if (w == 0 && q_.a.dg) {
-            double y = dG[lane];
-            for (int o = 1; o < 64; o <<= 1) {
-                const double z = __shfl_down(y, o, 64);
-                if (lane + o < 64) y += z;
-            }
-            y += across[0] + across[1] + across[2] + across[3];
-            const bool forgets = cuts[lane] != (lane ? cuts[lane - 1] : 0);
-            const Rows<float> o(q_.a.dg, b, h, a.f.H, T, 1, a.f.tokens_first);
-            if (t0 + lane < T) *o.at(t0 + lane) = forgets ? 0.f : (float)y;
+            const Parts<3> s = load_frag<3>(fw, m, lane);
+            aw[m] = mma(s, zo, aw[m]);
+            av[m] = mma(s, vo, av[m]);
+            ad[m] = mma(load_frag<3>(fd, m, lane), uo, ad[m]);
         }
     }
-    if (t0 + own < T) {
+    // pt, lt: rows s, column t = own; p, l: rows t, column s = own
+    const float ho = hi[own], loo = lo[own];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 hr = *reinterpret_cast<const f32x4*>(hi + 16 * i + 4 * g);
+        const f32x4 lr = *reinterpret_cast<const f32x4*>(lo + 16 * i + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 16 * i + 4 * g + e;
+            if (i <= w) {
+                const float d = pair_decay(ho, loo, hr[e], lr[e]);
+                pt[i][e] = row <= own ? pt[i][e] * d : 0.f;
+                lt[i][e] = row < own ? -lt[i][e] * d : 0.f;
+            }
+            if (i >= w) {
+                const float d = pair_decay(hr[e], lr[e], ho, loo);
+                p[i][e] = row >= own ? p[i][e] * d : 0.f;
+                l[i][e] = row > own ? -l[i][e] * d : 0.f;
+            }
+        }
+    }
+    float wrote = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        aw[m] *= so;
+        av[m] *= -so;
+        ad[m] *= no;
+        const f32x4 k4 = token4(tk, own, 16 * m + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wrote = fmaf(k4[e], ad[m][e], wrote);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (2 * j <= w) {
+            const Parts<3> x = split<3>(pt[2 * j], pt[2 * j + 1]), y = split<3>(lt[2 * j], lt[2 * j + 1]);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const Parts<NP> kf = by_feature(tk, m, j, lane);
+                aw[m] = mma(kf, x, aw[m]);
+                av[m] = mma(kf, y, av[m]);
+            }
+        }
+        if (2 * j + 1 >= w) {
+            const Parts<3> x = split<3>(p[2 * j], p[2 * j + 1]), y = split<3>(l[2 * j], l[2 * j + 1]);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                ad[m] = mma(by_feature(tq, m, j, lane), x, ad[m]);
+                ad[m] = mma(by_feature(tk, m, j, lane), y, ad[m]);
+            }
+        }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const f32x4 k4 = token4(tk, own, 16 * m + 4 * g), q4 = token4(tq, own, 16 * m + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum = fmaf(q4[e], aw[m][e], fmaf(k4[e], av[m][e] - ad[m][e], sum));
+        av[m] += ad[m];
+    }
+    // <D, W'> = start_C <D, W> + sum of k_s.(written part of dK_s)
+    double cross = (double)kept * all + wrote;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) cross += __shfl_xor(cross, o, 64);
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    de += __shfl_xor(de, 16, 64);
+    de += __shfl_xor(de, 32, 64);
+    if (g == 0) {
+        dG[own] = sum;
+        const Rows<float> o(q_.a.deta, b, h, a.f.H, T, 1, a.f.tokens_first);
+        if (q_.a.deta && inside) *o.at(t0 + own) = de;
+    }
+    if (lane == 0) across[w] = cross;
+    __syncthreads();
+    if (w == 0 && q_.a.dg) {
+        double y = dG[lane];
+        for (int o = 1; o < 64; o <<= 1) {
+            const double z = __shfl_down(y, o, 64);
+            if (lane + o < 64) y += z;
+        }
+        y += across[0] + across[1] + across[2] + across[3];
+        const Rows<float> o(q_.a.dg, b, h, a.f.H, T, 1, a.f.tokens_first);
+        if (t0 + lane < T) *o.at(t0 + lane) = rec.forgets[lane] ? 0.f : (float)y;
+    }
+if (q_.dK) {
+        float* to = q_.dK + (unit * kChunk + own) * DK + 4 * g;
+        float* tq_ = q_.dQ + (unit * kChunk + own) * DK + 4 * g;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            *reinterpret_cast<f32x4*>(to + 16 * m) = av[m];
+            *reinterpret_cast<f32x4*>(tq_ + 16 * m) = aw[m];
+        }
+    } else if (inside) {
         const Rows<TIO> dQ((TIO*)q_.a.dQ, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
         const Rows<TIO> dK((TIO*)q_.a.dK, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            store4(dQ.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, sumq[m]);
-            store4(dK.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, sumk[m]);
+            store4(dQ.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, aw[m]);
+            store4(dK.at(t0 + own), 16 * m + 4 * g, dk, dk % 4 == 0, av[m]);
         }
+    }
+}
+
+// dK and dQ of a chunk of a head of keys: the sum over the heads of values that share it, in
+// their order
+template <typename TIO>
+__global__ void __launch_bounds__(256) delta_shared_kernel(BwdPass q_, int DK)
+{
+    const DeltaPass& a = q_.p;
+    const int share = a.f.H / a.f.Hk, chunk = blockIdx.x % a.chunks, group = blockIdx.x / a.chunks;
+    const int key = a.head0 / share + group, b = key / a.f.Hk, hk = key % a.f.Hk, dk = a.f.dk, T = a.f.T;
+    const Rows<TIO> dK((TIO*)q_.a.dK, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<TIO> dQ((TIO*)q_.a.dQ, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    for (int e = threadIdx.x; e < kChunk * DK / 4; e += 256) {
+        const int row = e / (DK / 4), f = 4 * (e % (DK / 4)), t = chunk * kChunk + row;
+        if (t >= T || f >= dk) continue;
+        f32x4 k = {0.f, 0.f, 0.f, 0.f}, q = k;
+        for (int r = 0; r < share; ++r) {
+            const size_t at = (((size_t)(group * share + r) * a.chunks + chunk) * kChunk + row) * DK + f;
+            k += *reinterpret_cast<const f32x4*>(q_.dK + at);
+            q += *reinterpret_cast<const f32x4*>(q_.dQ + at);
+        }
+        store4(dK.at(t), f, dk, dk % 4 == 0, k);
+        store4(dQ.at(t), f, dk, dk % 4 == 0, q);
     }
 }
 
@@ -374,8 +425,11 @@ hipError_t reverse_and_grads(const BwdPass& q, hipStream_t s)
     delta_reverse_kernel<TIO, DK><<<(unsigned)(p.heads * ((p.dvp + 63) / 64)), 256, 0, s>>>(q);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    delta_grads_kernel<TIO, DK><<<(unsigned)((size_t)p.heads * p.chunks), 256, 0, s>>>(q);
+    e = hipGetLastError();
+    if (e != hipSuccess || !q.dK) return e;
     const size_t groups = p.heads / (p.f.H / p.f.Hk);
-    delta_grads_kernel<TIO, DK><<<(unsigned)(groups * p.chunks), 256, 0, s>>>(q);
+    delta_shared_kernel<TIO><<<(unsigned)(groups * p.chunks), 256, 0, s>>>(q, DK);
     return hipGetLastError();
 }
 
@@ -384,7 +438,7 @@ constexpr size_t kPassBytes = (size_t)4 << 30;
 
 struct Plan {
     int chunks, groups, dvp;
-    size_t S, St, P, states, cotangents, U, F, bytes;
+    size_t S, St, P, states, cotangents, U, F, dK, dQ, bytes;
 };
 
 Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
@@ -394,7 +448,8 @@ Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
     p.dvp = (dv + 31) / 32 * 32;
     const size_t unit = (size_t)p.chunks * (H / Hk), DK = delta_padded_dk(dk);
     const size_t state = 4 * DK * p.dvp, rows = 4 * (size_t)kChunk * p.dvp, frags = 3 * kFragQuads * sizeof(quad);
-    const size_t one = unit * (sizeof(Record) + 3 * frags + 2 * state + 2 * rows);
+    const size_t sums = H > Hk ? 4 * (size_t)kChunk * DK : 0;   // a plane of dK or dQ
+    const size_t one = unit * (sizeof(Record) + 3 * frags + 2 * state + 2 * rows + 2 * sums);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
     const size_t units = unit * p.groups;
     p.S = up256(units * sizeof(Record));
@@ -404,7 +459,9 @@ Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
     p.cotangents = p.states + up256(units * state);
     p.U = p.cotangents + up256(units * state);
     p.F = p.U + up256(units * rows);
-    p.bytes = p.F + up256(units * rows);
+    p.dK = p.F + up256(units * rows);
+    p.dQ = p.dK + up256(units * sums);
+    p.bytes = p.dQ + up256(units * sums);
     return p;
 }
 
@@ -434,6 +491,10 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
     p.cotangents = (float*)(ws + plan.cotangents);
     p.U = (float*)(ws + plan.U);
     p.F = (float*)(ws + plan.F);
+    if (f.H > f.Hk) {
+        q.dK = (float*)(ws + plan.dK);
+        q.dQ = (float*)(ws + plan.dQ);
+    }
     const int share = f.H / f.Hk, all = f.B * f.Hk, DK = delta_padded_dk(f.dk);
     for (int first = 0; first < all; first += plan.groups) {
         p.head0 = first * share;

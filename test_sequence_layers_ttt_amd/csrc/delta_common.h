@@ -209,16 +209,23 @@ __host__ __device__ constexpr int frag_upper(int i, int j) { return i < 2 ? 2 * 
 // An operand is its parts, one after the other, 16 bytes for each lane (1 KB a part).
 constexpr int kFragQuads = kFrags * 64;       // of one part of a matrix's operands
 struct Record {                               // decays of a chunk's tokens
-    double G[kChunk];                         // sums of the log decays, those that forget left out
-    int cuts[kChunk];                         // how many forget, up to and with the token
+    float hi[kChunk], lo[kChunk];             // sums of their binary logarithms, in two parts
     float eta[kChunk];
     float start[kChunk];                      // decay from the chunk's start through the token
     float end[kChunk];                        // decay from after the token to the chunk's end
+    int forgets[kChunk];                      // whether the token's decay leaves nothing
 };
 
-__device__ __forceinline__ float pair_decay(const double* G, const int* cuts, int t, int s)
+// A decay's binary logarithm is taken no lower than this: its power is 0 by far, and sums over a
+// chunk still leave the other tokens' digits alone (64 times this and 2^-27 in 53 bits).
+constexpr double kLeast = -1048576.0;
+
+// product of the decays after s up to t, s <= t: the difference of two sums that may both be far
+// from 0 (two floats each), then the hardware's power of two (a last place, and the argument's
+// rounding: at most 0.4 2^-24 of 1)
+__device__ __forceinline__ float pair_decay(float ht, float lt, float hs, float ls)
 {
-    return cuts[t] == cuts[s] ? expf((float)(G[t] - G[s])) : 0.f;
+    return __builtin_amdgcn_exp2f((ht - hs) + (lt - ls));
 }
 
 // operand f of N parts each, from result tiles a over b
