@@ -58,7 +58,7 @@ KERNEL_SOURCES = {"linear_b16": ["linear_mfma.hip", "linear_coop.hip", "mfma_com
                   "rmsnorm": ["rmsnorm.hip", "mfma_common.h", "device_common.h",
                               "block_launch.h"],
                   "clip": ["clip.hip", "mfma_common.h", "device_common.h", "block_launch.h"],
-                  "delta": ["delta.hip", "delta_bwd.hip", "delta_common.h", "delta_launch.h",
+                  "delta": ["delta.hip", "delta_scan.hip", "delta_bwd.hip", "delta_common.h", "delta_launch.h",
                             "mfma_f32.h", "mfma_common.h", "device_common.h"],
                   "groupnorm": ["groupnorm.hip", "mfma_common.h", "device_common.h",
                                 "block_launch.h"],

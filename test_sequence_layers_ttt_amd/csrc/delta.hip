@@ -1,11 +1,8 @@
 // Gated delta rule: forward pass by chunks of 64 tokens, and the token-by-token form.
 // (delta_common.h has the formulas.)
 //
-// Two kernels.  The first prepares every chunk of every head by itself: decays, K K^T,
-// Q K^T and the triangular solve S.  The second scans the chunks in order: a wave keeps
-// W^T for 16 columns of values in fp32 registers for the whole sequence, since columns
-// never meet; the result tiles of one product are, as they lie in registers, operands of
-// the next, so nothing but keys and queries goes through LDS.
+// The first kernel prepares every chunk of every head by itself: decays, K K^T, Q K^T and the
+// triangular solve S.  The scans over the chunks (delta_scan.hip) take it from there.
 #include <algorithm>
 
 #include "delta_common.h"
@@ -15,9 +12,6 @@ namespace ttt {
 namespace {
 
 __device__ __forceinline__ double shift_up(double x, int by) { return __shfl_up(x, by, 64); }
-
-// parts of P that the forward scan takes: behind a bf16 Z two are enough (2^-17)
-template <typename TIO> constexpr int kZParts = sizeof(TIO) == 2 ? 2 : 3;
 
 // ---- per chunk: decays, L, S, P -------------------------------------------------
 // One workgroup of four waves per (chunk, head).  P's operands (or its transpose's) come out
@@ -191,173 +185,6 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
                           rl<LD>(Sm + 16 * w * LD, 32 * j + 16, lane));
 }
 
-// ---- the scan over the chunks ------------------------------------------------------
-// One workgroup of four waves per head and 64 columns of values, a wave for 16 of them.
-// All that the next chunk needs is loaded to registers while this one is worked on, and then
-// goes to the other LDS buffer: no product waits for memory, one barrier a chunk.
-// Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
-template <typename TIO, int DK, bool SAVE>
-__global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaPass a)
-{
-    constexpr int M = DK / 16, J = DK / 32, NZ = SAVE ? 0 : kZParts<TIO>, OZ = kZParts<TIO> - 1;
-    typedef ChunkTiles<TIO, DK, NZ, !SAVE> Tiles;
-    constexpr int NB = kBuffers<Tiles>;
-    __shared__ __align__(16) Tiles tiles[NB];
-
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
-    const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
-    const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
-    const int first = 64 * (int)(blockIdx.x % parts), col = first + 16 * w + c;
-    const bool works = first + 16 * w < a.dvp;   // (else a wave only helps to load)
-    const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0, fours = dv % 4 == 0;
-    const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-    const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-    const Rows<const TIO> V((const TIO*)a.f.V, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const Rows<TIO> Z((TIO*)a.f.Z, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-
-    ChunkLoad<TIO, DK, NZ, !SAVE> next;
-    auto fetch = [&](int n) {
-        const size_t unit = unit0 + n;
-        next.load(K, Q, V, a.S + unit * 3 * kFragQuads, a.P + unit * NZ * kFragQuads, a.records + unit,
-                  n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
-    };
-    fetch(0);
-    f32x4 W[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-        W[m] = load_state(a.f.W0 ? a.f.W0 + state : nullptr, col, 16 * m + 4 * g, dv, dk);
-    next.put(tiles[0], tid);
-    __syncthreads();
-
-    for (int n = 0; n < a.chunks; ++n) {
-        const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
-        if (n + 1 < a.chunks) fetch(n + 1);
-        if (works) {
-            typedef Parts<kParts<TIO>> In;
-            In kt[J][4];
-            Parts<3> S[kFrags], x[2];
-            f32x4 r[4], z[4], v[4], eta[4], start[4], ends[4];
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
-                start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
-                ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const In p = by_feature(t.v, w, j, lane);
-                v[2 * j] = widen_parts(p, false);
-                v[2 * j + 1] = widen_parts(p, true);
-            }
-#pragma unroll
-            for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(t.s, f, lane);
-            const float all = t.start[kChunk - 1];
-            reads_before();
-
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = z[i] = zero;
-            Parts<3> wp[J];
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                wp[j] = split<3>(W[2 * j], W[2 * j + 1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = mma(kt[j][i], wp[j], r[i]);
-            }
-            if constexpr (SAVE) {
-                float* st = a.states + (unit0 + n) * DK * a.dvp + col;
-#pragma unroll
-                for (int m = 0; m < M; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[(size_t)(16 * m + 4 * g + e) * a.dvp] = W[m][e];
-            }
-            In kf[M][2];
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
-            reads_before();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
-            In qt[J][4];
-            Parts<NZ ? NZ : 1> P[kFrags], u[2];
-            if constexpr (!SAVE) {
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qt[j][i] = by_token(t.q, i, j, lane);
-#pragma unroll
-                for (int f = 0; f < kFrags; ++f) P[f] = load_frag<NZ>(t.p, f, lane);
-                reads_before();
-            }
-            if constexpr (SAVE) {
-                float* u = a.U + (unit0 + n) * kChunk * a.dvp + col;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) u[(size_t)(16 * i + 4 * g + e) * a.dvp] = r[i][e];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] *= eta[i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                x[j] = split<3>(ends[2 * j] * r[2 * j], ends[2 * j + 1] * r[2 * j + 1]);
-#pragma unroll
-            for (int m = 0; m < M; ++m) W[m] *= all;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int m = 0; m < M; ++m) W[m] = mma(kf[m][j], x[j], W[m]);
-            if constexpr (!SAVE) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) u[j] = split<NZ>(r[2 * j], r[2 * j + 1]);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = mma<OZ>(wp[j], qt[j][i], z[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] *= t.start[16 * i + c];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) z[i] = mma<OZ>(u[j], P[frag_lower(i, j)], z[i]);
-                const int token = n * kChunk + c;
-                if (fours && first + 64 <= dv && (n + 1) * kChunk <= T) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, true, z[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (token + 16 * i < T)
-                            store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, fours, z[i]);
-                }
-            }
-        }
-        if constexpr (NB == 1) __syncthreads();
-        if (n + 1 < a.chunks) next.put(tiles[NB == 2 ? (n + 1) & 1 : 0], tid);
-        __syncthreads();
-    }
-    if constexpr (!SAVE)
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-            store_state(a.f.W_out ? a.f.W_out + state : nullptr, col, 16 * m + 4 * g, dv, dk, W[m]);
-}
-
 // ---- token after token ---------------------------------------------------------------
 // 16 lanes hold a row of the state, 4 X features each; a workgroup of 256 threads 16 rows.
 // HBM bounds the decoded token of a large batch (the state in and out).  W k and W q are
@@ -458,33 +285,30 @@ hipError_t prepare_as(const DeltaPass& p, bool backward, hipStream_t s)
     return hipGetLastError();
 }
 
-template <typename TIO, int DK>
-hipError_t chain_as(const DeltaPass& p, bool save, hipStream_t s)
-{
-    const unsigned grid = (unsigned)(p.heads * ((p.dvp + 63) / 64));
-    if (save) delta_chain_kernel<TIO, DK, true><<<grid, 256, 0, s>>>(p);
-    else delta_chain_kernel<TIO, DK, false><<<grid, 256, 0, s>>>(p);
-    return hipGetLastError();
-}
-
 constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr size_t kPassBytes = (size_t)1 << 30;   // of workspace, where one head needs no more
 
 struct Plan {
-    int chunks, groups;      // groups of heads that share keys, in one pass
-    size_t S, P, bytes;      // places in the workspace, which begins with the records
+    int chunks, groups, dvp, segments;   // groups of heads that share keys, in one pass
+    size_t S, P, ends, transitions, bytes;   // places in the workspace, which begins with the records
 };
 
-Plan fwd_plan(int B, int H, int Hk, int T, bool bf16)
+Plan fwd_plan(int B, int H, int Hk, int T, int dk, int dv, bool bf16)
 {
     Plan p;
     p.chunks = (T + kChunk - 1) / kChunk;
-    const size_t unit = (size_t)p.chunks * (H / Hk), part = kFragQuads * sizeof(quad);
+    p.dvp = (dv + 31) / 32 * 32;
+    const size_t share = H / Hk, unit = p.chunks * share, part = kFragQuads * sizeof(quad);
     const size_t s = 3 * part, z = (bf16 ? 2 : 3) * part, one = unit * (sizeof(Record) + s + z);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
-    p.S = up256(unit * p.groups * sizeof(Record));
-    p.P = p.S + up256(unit * p.groups * s);
-    p.bytes = p.P + up256(unit * p.groups * z);
+    const size_t heads = p.groups * share, units = unit * p.groups, DK = delta_padded_dk(dk);
+    p.segments = delta_segments((int)heads, p.chunks, dv, dk, false);
+    const size_t cut = p.segments > 1 ? heads * p.segments * DK * 4 : 0;
+    p.S = up256(units * sizeof(Record));
+    p.P = p.S + up256(units * s);
+    p.ends = p.P + up256(units * z);
+    p.transitions = p.ends + up256(cut * p.dvp);
+    p.bytes = p.transitions + up256(cut * DK);
     return p;
 }
 
@@ -502,40 +326,32 @@ hipError_t launch_delta_prepare(const DeltaPass& p, bool backward, hipStream_t s
                     : prepare_as<float, 128>(p, backward, s);
 }
 
-hipError_t launch_delta_chain(const DeltaPass& p, bool save, hipStream_t s)
+size_t delta_fwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool bf16)
 {
-    const int DK = delta_padded_dk(p.f.dk);
-    if (p.f.bf16)
-        return DK == 32 ? chain_as<uint16_t, 32>(p, save, s)
-             : DK == 64 ? chain_as<uint16_t, 64>(p, save, s)
-                        : chain_as<uint16_t, 128>(p, save, s);
-    return DK == 32 ? chain_as<float, 32>(p, save, s)
-         : DK == 64 ? chain_as<float, 64>(p, save, s)
-                    : chain_as<float, 128>(p, save, s);
-}
-
-size_t delta_fwd_workspace(int B, int H, int Hk, int T, int, int, bool bf16)
-{
-    return fwd_plan(B, H, Hk, T, bf16).bytes;
+    return fwd_plan(B, H, Hk, T, dk, dv, bf16).bytes;
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
 {
-    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T, a.bf16);
+    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T, a.dk, a.dv, a.bf16);
     char* ws = (char*)a.workspace;
     DeltaPass p = {};
     p.f = a;
     p.chunks = plan.chunks;
-    p.dvp = (a.dv + 31) / 32 * 32;
+    p.dvp = plan.dvp;
+    p.segments = plan.segments;
+    p.segment_chunks = (plan.chunks + plan.segments - 1) / plan.segments;
     p.records = (Record*)ws;
     p.S = (quad*)(ws + plan.S);
     p.P = (quad*)(ws + plan.P);
+    p.ends = (float*)(ws + plan.ends);
+    p.transitions = (float*)(ws + plan.transitions);
     const int share = a.H / a.Hk, all = a.B * a.Hk;
     for (int first = 0; first < all; first += plan.groups) {
         p.head0 = first * share;
         p.heads = std::min(plan.groups, all - first) * share;
         hipError_t e = launch_delta_prepare(p, false, s);
-        if (e == hipSuccess) e = launch_delta_chain(p, false, s);
+        if (e == hipSuccess) e = launch_delta_scans(p, nullptr, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -1,9 +1,8 @@
 // Gated delta rule: backward pass by chunks of 64 tokens (delta_common.h has the formulas).
 //
-// The forward scan is run again and keeps every chunk's first state and U; a second scan
-// carries the state's gradient D from the last chunk to the first, a wave for 16 columns of
-// values as in the forward pass; the gradients of keys, queries, step sizes and decays then
-// follow chunk by chunk, all chunks at once.  Every sum has a fixed order: the same bits on
+// The forward scan is run again and keeps every chunk's first state and U, while a second scan
+// carries the state's gradient D from the last chunk to the first; the gradients of keys, queries,
+// step sizes and decays then follow chunk by chunk, all chunks at once.  Every sum has a fixed order: the same bits on
 // every call.
 //
 // The decay's gradient is the product of D and the state across the token, that is of all
@@ -22,146 +21,6 @@ struct BwdPass {
     DeltaBwdArgs a;
     float *dK, *dQ;          // [heads][chunks][64][DK] where heads share keys, else nullptr
 };
-
-// ---- the scan from the last chunk to the first ---------------------------------------
-template <typename TIO, int DK>
-__global__ void __launch_bounds__(256, 1) delta_reverse_kernel(BwdPass q_)
-{
-    constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
-    typedef ChunkTiles<TIO, DK, 3, true> Tiles;
-    constexpr int NB = kBuffers<Tiles>;
-    const DeltaPass& a = q_.p;
-    __shared__ __align__(16) Tiles tiles[NB];
-
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int parts = (a.dvp + 63) / 64, local = blockIdx.x / parts, head = a.head0 + local;
-    const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
-    const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
-    const int first = 64 * (int)(blockIdx.x % parts), col = first + 16 * w + c;
-    const bool works = first + 16 * w < a.dvp;
-    const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0;
-    const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-    const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-    const Rows<const TIO> dZ((const TIO*)q_.a.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
-    const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-
-    ChunkLoad<TIO, DK, 3, true> next;
-    auto fetch = [&](int n) {
-        const size_t unit = unit0 + n;
-        next.load(K, Q, dZ, a.St + unit * 3 * kFragQuads, a.P + unit * 3 * kFragQuads, a.records + unit,
-                  n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
-    };
-    const int last = a.chunks - 1;
-    fetch(last);
-    f32x4 D[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-        D[m] = load_state(q_.a.dW_T ? q_.a.dW_T + state : nullptr, col, 16 * m + 4 * g, dv, dk);
-    next.put(tiles[NB == 2 ? last & 1 : 0], tid);
-    __syncthreads();
-
-    for (int n = last; n >= 0; --n) {
-        const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
-        if (n > 0) fetch(n - 1);
-        if (works) {
-            const size_t unit = unit0 + n;
-            typedef Parts<NP> In;
-            In kt[J][4], zp[2];
-            Parts<3> P[kFrags], x[2], y[2];
-            f32x4 f[4], z[4], eta[4], start[4], ends[4];
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
-                start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
-                ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
-#pragma unroll
-            for (int e = 0; e < kFrags; ++e) P[e] = load_frag<3>(t.p, e, lane);
-            const float all = t.start[kChunk - 1];
-            reads_before();
-
-            float* out = a.cotangents + unit * DK * a.dvp + col;
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) out[(size_t)(16 * m + 4 * g + e) * a.dvp] = D[m][e];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = zero;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = mma(kt[j][i], dp, f[i]);
-            }
-            Parts<3> S[kFrags];
-#pragma unroll
-            for (int e = 0; e < kFrags; ++e) S[e] = load_frag<3>(t.s, e, lane);
-            reads_before();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] *= ends[i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(P[frag_upper(i, j)], zp[j], f[i]);
-            In kf[M][2];
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
-            reads_before();
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                x[j] = split<3>(-(eta[2 * j] * f[2 * j]), -(eta[2 * j + 1] * f[2 * j + 1]));
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(S[frag_upper(i, j)], x[j], f[i]);
-            In qf[M][2];
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) qf[m][j] = by_feature(t.q, m, j, lane);
-            reads_before();
-
-            float* F = a.F + unit * kChunk * a.dvp + col;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) F[(size_t)(16 * i + 4 * g + e) * a.dvp] = f[i][e];
-                f[i] *= -(start[i] * eta[i]);
-                z[i] = start[i] * widen_parts(zp[i / 2], i & 1);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                x[j] = split<3>(f[2 * j], f[2 * j + 1]);
-                y[j] = split<3>(z[2 * j], z[2 * j + 1]);
-            }
-#pragma unroll
-            for (int m = 0; m < M; ++m) D[m] *= all;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    D[m] = mma(kf[m][j], x[j], D[m]);
-                    D[m] = mma(qf[m][j], y[j], D[m]);
-                }
-        }
-        if constexpr (NB == 1) __syncthreads();
-        if (n > 0) next.put(tiles[NB == 2 ? (n - 1) & 1 : 0], tid);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-        store_state(q_.a.dW0 ? q_.a.dW0 + state : nullptr, col, 16 * m + 4 * g, dv, dk, D[m]);
-}
 
 // ---- gradients of a chunk ------------------------------------------------------------
 // One workgroup of four waves per chunk and head of values (where heads share keys, dQ and dK
@@ -419,14 +278,11 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(BwdPass q_, int DK)
 }
 
 template <typename TIO, int DK>
-hipError_t reverse_and_grads(const BwdPass& q, hipStream_t s)
+hipError_t gradients(const BwdPass& q, hipStream_t s)
 {
     const DeltaPass& p = q.p;
-    delta_reverse_kernel<TIO, DK><<<(unsigned)(p.heads * ((p.dvp + 63) / 64)), 256, 0, s>>>(q);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     delta_grads_kernel<TIO, DK><<<(unsigned)((size_t)p.heads * p.chunks), 256, 0, s>>>(q);
-    e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !q.dK) return e;
     const size_t groups = p.heads / (p.f.H / p.f.Hk);
     delta_shared_kernel<TIO><<<(unsigned)(groups * p.chunks), 256, 0, s>>>(q, DK);
@@ -437,8 +293,8 @@ constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr size_t kPassBytes = (size_t)4 << 30;
 
 struct Plan {
-    int chunks, groups, dvp;
-    size_t S, St, P, states, cotangents, U, F, dK, dQ, bytes;
+    int chunks, groups, dvp, segments;
+    size_t S, St, P, states, cotangents, U, F, dK, dQ, ends, ends_back, transitions, bytes;
 };
 
 Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
@@ -461,7 +317,13 @@ Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
     p.F = p.U + up256(units * rows);
     p.dK = p.F + up256(units * rows);
     p.dQ = p.dK + up256(units * sums);
-    p.bytes = p.dQ + up256(units * sums);
+    const size_t heads = (size_t)p.groups * (H / Hk);
+    p.segments = delta_segments((int)heads, p.chunks, dv, dk, true);
+    const size_t cut = p.segments > 1 ? heads * p.segments * DK * 4 : 0;
+    p.ends = p.dQ + up256(units * sums);
+    p.ends_back = p.ends + up256(cut * p.dvp);
+    p.transitions = p.ends_back + up256(cut * p.dvp);
+    p.bytes = p.transitions + up256(cut * DK);
     return p;
 }
 
@@ -483,6 +345,11 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
     p.f = f;
     p.chunks = plan.chunks;
     p.dvp = plan.dvp;
+    p.segments = plan.segments;
+    p.segment_chunks = (plan.chunks + plan.segments - 1) / plan.segments;
+    p.ends = (float*)(ws + plan.ends);
+    p.ends_back = (float*)(ws + plan.ends_back);
+    p.transitions = (float*)(ws + plan.transitions);
     p.records = (Record*)ws;
     p.S = (quad*)(ws + plan.S);
     p.St = (quad*)(ws + plan.St);
@@ -500,16 +367,16 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
         p.head0 = first * share;
         p.heads = std::min(plan.groups, all - first) * share;
         hipError_t e = launch_delta_prepare(p, true, s);
-        if (e == hipSuccess) e = launch_delta_chain(p, true, s);
+        if (e == hipSuccess) e = launch_delta_scans(p, &a, s);
         if (e != hipSuccess) return e;
         if (f.bf16)
-            e = DK == 32 ? reverse_and_grads<uint16_t, 32>(q, s)
-              : DK == 64 ? reverse_and_grads<uint16_t, 64>(q, s)
-                         : reverse_and_grads<uint16_t, 128>(q, s);
+            e = DK == 32 ? gradients<uint16_t, 32>(q, s)
+              : DK == 64 ? gradients<uint16_t, 64>(q, s)
+                         : gradients<uint16_t, 128>(q, s);
         else
-            e = DK == 32 ? reverse_and_grads<float, 32>(q, s)
-              : DK == 64 ? reverse_and_grads<float, 64>(q, s)
-                         : reverse_and_grads<float, 128>(q, s);
+            e = DK == 32 ? gradients<float, 32>(q, s)
+              : DK == 64 ? gradients<float, 64>(q, s)
+                         : gradients<float, 128>(q, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -71,6 +71,8 @@ __device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32
 }
 
 template <typename TIO> constexpr int kParts = sizeof(TIO) == 2 ? 1 : 3;
+// parts of P that the forward scan takes: behind a bf16 Z two are enough (2^-17)
+template <typename TIO> constexpr int kZParts = sizeof(TIO) == 2 ? 2 : 3;
 
 // ---- token tensors ---------------------------------------------------------
 // rows of one (batch, head) of [B, H, T, d] or [B, T, H, d]

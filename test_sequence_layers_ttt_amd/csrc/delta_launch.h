@@ -51,11 +51,15 @@ struct DeltaPass {
     quad *S, *St, *P;        // operands of S, of its transpose (backward), of P (or its transpose)
     float *states, *cotangents;   // [heads][chunks][DK][dvp]: W^T before a chunk, D^T after it
     float *U, *F;            // [heads][chunks][64][dvp]
+    int segments, segment_chunks;
+    float *ends, *ends_back; // [heads][segments][DK][dvp]: states and their gradients past a segment
+    float* transitions;      // [heads][segments][DK][DK]
 };
 // decays, S and P (transposed: S, its transpose and P's) of every chunk
 hipError_t launch_delta_prepare(const DeltaPass& p, bool backward, hipStream_t s);
-// the scan over the chunks; `save` keeps states and U instead of writing Z and W_out
-hipError_t launch_delta_chain(const DeltaPass& p, bool save, hipStream_t s);
+// the scan over the chunks; with `o` both scans of a backward pass, which keep states, U, D and F
+hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s);
+int delta_segments(int heads, int chunks, int dv, int dk, bool backward);
 // features of a head as the kernels hold them
 inline int delta_padded_dk(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : 128; }
 

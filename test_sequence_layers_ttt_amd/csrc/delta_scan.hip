@@ -1,0 +1,518 @@
+// The gated delta rule's scans over the chunks: forward, and from the last chunk to the first.
+// (delta_common.h has the formulas.)
+//
+// One workgroup of four waves per head and 64 columns of values; a wave keeps W^T (or D^T) for
+// 16 of them in fp32 registers, since columns never meet: the result tiles of one product are,
+// as they lie in registers, operands of the next, and only what all waves need goes through
+// LDS.  All that the next chunk needs is loaded to registers while this one is worked on, and
+// then goes to the other LDS buffer: no product waits for memory, one barrier a chunk.  What
+// bounds a chunk (3.3 us with 64 features) is one wave's own instructions: some 650 of the
+// vector units, most of them splitting operands into parts, and 120 matrix products.
+//
+// The reverse scan needs nothing of the forward one, so in a backward pass both run at once.
+// Where there are too few heads for the card, each sequence is cut into segments.  First the
+// segments' ends are found from a start of zero, together with what becomes of a unit matrix
+// (the segment's transition: V = 0, the features' unit vectors as rows of the state); a chain of
+// small products then gives every segment its start; and all segments run again from there.
+#include <algorithm>
+
+#include "delta_common.h"
+
+namespace ttt {
+namespace {
+
+// what a scan leaves: Z, or states and U (or D and F) for the gradients, or its last state alone
+enum { kRead, kSave, kEnd };
+
+template <int N>
+__device__ __forceinline__ void store_plane(float* X, int ld, int col, int g, const f32x4 (&x)[N])
+{
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) X[(size_t)(16 * m + 4 * g + e) * ld + col] = x[m][e];
+}
+
+template <int N>
+__device__ __forceinline__ void load_plane(const float* X, int ld, int col, int g, f32x4 (&x)[N])
+{
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[m][e] = X[(size_t)(16 * m + 4 * g + e) * ld + col];
+}
+
+// a workgroup's share: 64 columns from `first` of one head's segment
+struct Share {
+    int local, segment, first;
+};
+
+// Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
+template <typename TIO, int DK, int KEEP>
+struct Forward {
+    static constexpr int NZ = KEEP == kRead ? kZParts<TIO> : 0;
+    typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead> Tiles;
+    static constexpr int NB = kBuffers<Tiles>;
+
+    // `unit`: V = 0 and a unit matrix for the start, columns are features
+    static __device__ __forceinline__ void run(const DeltaPass& a, Tiles* tiles, Share s, bool unit)
+    {
+        constexpr int M = DK / 16, J = DK / 32, OZ = kZParts<TIO> - 1;
+        const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int local = s.local, head = a.head0 + local, first = s.first;
+        const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
+        const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
+        const int col = first + 16 * w + c;
+        const bool works = first + 16 * w < (unit ? DK : a.dvp);   // (else a wave only helps to load)
+        const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0, fours = dv % 4 == 0;
+        const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> V((const TIO*)a.f.V, b, h, a.f.H, T, dv, a.f.tokens_first);
+        const Rows<TIO> Z((TIO*)a.f.Z, b, h, a.f.H, T, dv, a.f.tokens_first);
+        const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const int begin = s.segment * a.segment_chunks;
+        const int stop = begin + a.segment_chunks < a.chunks ? begin + a.segment_chunks : a.chunks;
+
+        ChunkLoad<TIO, DK, NZ, KEEP == kRead> next;
+        auto fetch = [&](int n) {
+            const size_t at = unit0 + n;
+            next.load(K, Q, V, a.S + at * 3 * kFragQuads, a.P + at * NZ * kFragQuads, a.records + at,
+                      n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+        };
+        fetch(begin);
+        f32x4 W[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) W[m] = zero;
+        if (unit) {
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) W[m][e] = 16 * m + 4 * g + e == col ? 1.f : 0.f;
+        } else if (s.segment == 0) {
+            if (a.f.W0)
+#pragma unroll
+                for (int m = 0; m < M; ++m) W[m] = load_state(a.f.W0 + state, col, 16 * m + 4 * g, dv, dk);
+        } else if (KEEP != kEnd && works) {
+            load_plane(a.ends + ((size_t)local * a.segments + s.segment - 1) * DK * a.dvp, a.dvp, col, g, W);
+        }
+        next.put(tiles[0], tid);
+        __syncthreads();
+
+        for (int n = begin; n < stop; ++n) {
+            const Tiles& t = tiles[NB == 2 ? (n - begin) & 1 : 0];
+            if (n + 1 < stop) fetch(n + 1);
+            if (works) {
+                typedef Parts<kParts<TIO>> In;
+                In kt[J][4];
+                Parts<3> S[kFrags], x[2];
+                f32x4 r[4], z[4], v[4], eta[4], start[4], ends[4];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                    start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
+                    ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const In p = by_feature(t.v, w, j, lane);
+                    v[2 * j] = unit ? zero : widen_parts(p, false);
+                    v[2 * j + 1] = unit ? zero : widen_parts(p, true);
+                }
+#pragma unroll
+                for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(t.s, f, lane);
+                const float all = t.start[kChunk - 1];
+                reads_before();
+
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = z[i] = zero;
+                Parts<3> wp[J];
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    wp[j] = split<3>(W[2 * j], W[2 * j + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = mma(kt[j][i], wp[j], r[i]);
+                }
+                if constexpr (KEEP == kSave) store_plane(a.states + (unit0 + n) * DK * a.dvp, a.dvp, col, g, W);
+                In kf[M][2];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
+                reads_before();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 2 * j; i < 4; ++i) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
+                In qt[J][4];
+                Parts<NZ ? NZ : 1> P[kFrags], u[2];
+                if constexpr (KEEP == kRead) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qt[j][i] = by_token(t.q, i, j, lane);
+#pragma unroll
+                    for (int f = 0; f < kFrags; ++f) P[f] = load_frag<NZ>(t.p, f, lane);
+                    reads_before();
+                }
+                if constexpr (KEEP == kSave) store_plane(a.U + (unit0 + n) * kChunk * a.dvp, a.dvp, col, g, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] *= eta[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    x[j] = split<3>(ends[2 * j] * r[2 * j], ends[2 * j + 1] * r[2 * j + 1]);
+#pragma unroll
+                for (int m = 0; m < M; ++m) W[m] *= all;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int m = 0; m < M; ++m) W[m] = mma(kf[m][j], x[j], W[m]);
+                if constexpr (KEEP == kRead) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) u[j] = split<NZ>(r[2 * j], r[2 * j + 1]);
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[i] = mma<OZ>(wp[j], qt[j][i], z[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] *= t.start[16 * i + c];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 2 * j; i < 4; ++i) z[i] = mma<OZ>(u[j], P[frag_lower(i, j)], z[i]);
+                    const int token = n * kChunk + c;
+                    if (fours && first + 64 <= dv && (n + 1) * kChunk <= T) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, true, z[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (token + 16 * i < T)
+                                store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, fours, z[i]);
+                    }
+                }
+            }
+            if constexpr (NB == 1) __syncthreads();
+            if (n + 1 < stop) next.put(tiles[NB == 2 ? (n + 1 - begin) & 1 : 0], tid);
+            __syncthreads();
+        }
+        if constexpr (KEEP == kEnd) {
+            if (!works) return;
+            const size_t at = (size_t)local * a.segments + s.segment;
+            if (unit) store_plane(a.transitions + at * DK * DK, DK, col, g, W);
+            else store_plane(a.ends + at * DK * a.dvp, a.dvp, col, g, W);
+        }
+        if constexpr (KEEP == kRead) {
+            if (stop == a.chunks && a.f.W_out)
+#pragma unroll
+                for (int m = 0; m < M; ++m) store_state(a.f.W_out + state, col, 16 * m + 4 * g, dv, dk, W[m]);
+        }
+    }
+};
+
+template <typename TIO, int DK, int KEEP>
+struct Reverse {
+    typedef ChunkTiles<TIO, DK, 3, true> Tiles;
+    static constexpr int NB = kBuffers<Tiles>;
+
+    static __device__ __forceinline__ void run(const DeltaPass& a, const DeltaBwdArgs& o, Tiles* tiles, Share s)
+    {
+        constexpr int NP = kParts<TIO>, M = DK / 16, J = DK / 32;
+        const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int local = s.local, head = a.head0 + local, first = s.first;
+        const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
+        const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
+        const int col = first + 16 * w + c;
+        const bool works = first + 16 * w < a.dvp;
+        const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0;
+        const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+        const Rows<const TIO> dZ((const TIO*)o.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
+        const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        const int begin = s.segment * a.segment_chunks;
+        const int last = (begin + a.segment_chunks < a.chunks ? begin + a.segment_chunks : a.chunks) - 1;
+
+        ChunkLoad<TIO, DK, 3, true> next;
+        auto fetch = [&](int n) {
+            const size_t at = unit0 + n;
+            next.load(K, Q, dZ, a.St + at * 3 * kFragQuads, a.P + at * 3 * kFragQuads, a.records + at,
+                      n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+        };
+        fetch(last);
+        f32x4 D[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) D[m] = zero;
+        if (last == a.chunks - 1) {
+            if (o.dW_T)
+#pragma unroll
+                for (int m = 0; m < M; ++m) D[m] = load_state(o.dW_T + state, col, 16 * m + 4 * g, dv, dk);
+        } else if (KEEP != kEnd && works) {
+            load_plane(a.ends_back + ((size_t)local * a.segments + s.segment + 1) * DK * a.dvp, a.dvp, col, g, D);
+        }
+        next.put(tiles[NB == 2 ? last & 1 : 0], tid);
+        __syncthreads();
+
+        for (int n = last; n >= begin; --n) {
+            const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
+            if (n > begin) fetch(n - 1);
+            if (works) {
+                const size_t unit = unit0 + n;
+                typedef Parts<NP> In;
+                In kt[J][4], zp[2];
+                Parts<3> P[kFrags], x[2], y[2];
+                f32x4 f[4], z[4], eta[4], start[4], ends[4];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                    start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
+                    ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
+#pragma unroll
+                for (int e = 0; e < kFrags; ++e) P[e] = load_frag<3>(t.p, e, lane);
+                const float all = t.start[kChunk - 1];
+                reads_before();
+
+                if constexpr (KEEP == kSave) store_plane(a.cotangents + unit * DK * a.dvp, a.dvp, col, g, D);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = zero;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = mma(kt[j][i], dp, f[i]);
+                }
+                Parts<3> S[kFrags];
+#pragma unroll
+                for (int e = 0; e < kFrags; ++e) S[e] = load_frag<3>(t.s, e, lane);
+                reads_before();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] *= ends[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(P[frag_upper(i, j)], zp[j], f[i]);
+                In kf[M][2];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
+                reads_before();
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    x[j] = split<3>(-(eta[2 * j] * f[2 * j]), -(eta[2 * j + 1] * f[2 * j + 1]));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(S[frag_upper(i, j)], x[j], f[i]);
+                In qf[M][2];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) qf[m][j] = by_feature(t.q, m, j, lane);
+                reads_before();
+
+                if constexpr (KEEP == kSave) store_plane(a.F + unit * kChunk * a.dvp, a.dvp, col, g, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[i] *= -(start[i] * eta[i]);
+                    z[i] = start[i] * widen_parts(zp[i / 2], i & 1);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[j] = split<3>(f[2 * j], f[2 * j + 1]);
+                    y[j] = split<3>(z[2 * j], z[2 * j + 1]);
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m) D[m] *= all;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        D[m] = mma(kf[m][j], x[j], D[m]);
+                        D[m] = mma(qf[m][j], y[j], D[m]);
+                    }
+            }
+            if constexpr (NB == 1) __syncthreads();
+            if (n > begin) next.put(tiles[NB == 2 ? (n - 1) & 1 : 0], tid);
+            __syncthreads();
+        }
+        if constexpr (KEEP == kEnd) {
+            if (works) store_plane(a.ends_back + ((size_t)local * a.segments + s.segment) * DK * a.dvp, a.dvp, col, g, D);
+        } else if (begin == 0 && o.dW0) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) store_state(o.dW0 + state, col, 16 * m + 4 * g, dv, dk, D[m]);
+        }
+    }
+};
+
+// One launch of all shares of a kind.  Forward alone: kRead over all segments, or the ends of
+// all but the last and the transitions of all but the first and last.  With the backward pass:
+// kSave of both scans, or all three kinds of ends.
+template <typename TIO, int DK, int KEEP>
+__global__ void __launch_bounds__(256, 1) delta_scan_kernel(DeltaPass a)
+{
+    typedef typename Forward<TIO, DK, KEEP>::Tiles Tiles;
+    __shared__ __align__(16) Tiles tiles[kBuffers<Tiles>];
+    const int parts = (a.dvp + 63) / 64, wide = (DK + 63) / 64;
+    const int ends = KEEP == kEnd ? (a.segments - 1) * parts : a.segments * parts;
+    const int each = ends + (KEEP == kEnd ? (a.segments - 2) * wide : 0);
+    const int local = blockIdx.x / each;
+    int k = blockIdx.x % each;
+    const bool unit = k >= ends;
+    if (unit) k -= ends;
+    const Share s = {local, unit ? 1 + k / wide : k / parts, 64 * (unit ? k % wide : k % parts)};
+    Forward<TIO, DK, KEEP>::run(a, tiles, s, unit);
+}
+
+template <typename TIO, int DK, int KEEP>
+__global__ void __launch_bounds__(256, 1) delta_scans_kernel(DeltaPass a, DeltaBwdArgs o)
+{
+    typedef typename Forward<TIO, DK, KEEP>::Tiles There;
+    typedef typename Reverse<TIO, DK, KEEP>::Tiles Back;
+    constexpr size_t room = kBuffers<There> * sizeof(There) > kBuffers<Back> * sizeof(Back)
+                                ? kBuffers<There> * sizeof(There) : kBuffers<Back> * sizeof(Back);
+    __shared__ __align__(16) char tiles[room];
+    const int parts = (a.dvp + 63) / 64, wide = (DK + 63) / 64;
+    const int ends = KEEP == kEnd ? (a.segments - 1) * parts : a.segments * parts;
+    const int each = 2 * ends + (KEEP == kEnd ? (a.segments - 2) * wide : 0);
+    const int local = blockIdx.x / each;
+    int k = blockIdx.x % each;
+    if (k < ends) {
+        const Share s = {local, k / parts + (KEEP == kEnd ? 1 : 0), 64 * (k % parts)};
+        Reverse<TIO, DK, KEEP>::run(a, o, (Back*)tiles, s);
+        return;
+    }
+    k -= ends;
+    const bool unit = k >= ends;
+    if (unit) k -= ends;
+    const Share s = {local, unit ? 1 + k / wide : k / parts, 64 * (unit ? k % wide : k % parts)};
+    Forward<TIO, DK, KEEP>::run(a, (There*)tiles, s, unit);
+}
+
+// The segments' ends, one after the other: with X^T_s the state that segment s - 1 leaves (its end
+// from the true start) and A the transition as it was stored, X^T_(s+1) = A X^T_s + end_s; backward
+// by A^T.  One wave for 16 columns of a head.
+template <int DK>
+__global__ void __launch_bounds__(64) delta_join_kernel(DeltaPass a)
+{
+    constexpr int M = DK / 16, J = DK / 32;
+    const int lane = threadIdx.x, c = lane & 15, g = lane >> 4, parts = a.dvp / 16;
+    const bool back = blockIdx.x >= (unsigned)(a.heads * parts);
+    const int id = blockIdx.x % (a.heads * parts), local = id / parts, col = 16 * (id % parts) + c;
+    const size_t plane = (size_t)DK * a.dvp;
+    float* ends = (back ? a.ends_back : a.ends) + (size_t)local * a.segments * plane;
+    f32x4 X[M];
+    load_plane(ends + (back ? (a.segments - 1) * plane : 0), a.dvp, col, g, X);
+    for (int k = 1; k < a.segments - 1; ++k) {
+        const int s = back ? a.segments - 1 - k : k;
+        const float* A = a.transitions + ((size_t)local * a.segments + s) * DK * DK;
+        Parts<3> x[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[j] = split<3>(X[2 * j], X[2 * j + 1]);
+        load_plane(ends + s * plane, a.dvp, col, g, X);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                f32x4 p, q;
+                if (back) {
+                    const float* at = A + (size_t)(32 * j + 4 * g) * DK + 16 * m + c;
+                    p = f32x4{at[0], at[DK], at[2 * DK], at[3 * DK]};
+                    at += 16 * DK;
+                    q = f32x4{at[0], at[DK], at[2 * DK], at[3 * DK]};
+                } else {
+                    const float* at = A + (size_t)(16 * m + c) * DK + 32 * j + 4 * g;
+                    p = *reinterpret_cast<const f32x4*>(at);
+                    q = *reinterpret_cast<const f32x4*>(at + 16);
+                }
+                X[m] = mma(split<3>(p, q), x[j], X[m]);
+            }
+        store_plane(ends + s * plane, a.dvp, col, g, X);
+    }
+}
+
+template <typename TIO, int DK, int KEEP>
+hipError_t launch(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
+{
+    const size_t parts = (p.dvp + 63) / 64, wide = (DK + 63) / 64;
+    const size_t ends = (KEEP == kEnd ? p.segments - 1 : p.segments) * parts;
+    const size_t units = KEEP == kEnd ? (p.segments - 2) * wide : 0;
+    if constexpr (KEEP != kSave) {
+        if (!o) {
+            delta_scan_kernel<TIO, DK, KEEP><<<(unsigned)(p.heads * (ends + units)), 256, 0, s>>>(p);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (KEEP != kRead)
+        delta_scans_kernel<TIO, DK, KEEP><<<(unsigned)(p.heads * (2 * ends + units)), 256, 0, s>>>(p, *o);
+    return hipGetLastError();
+}
+
+template <typename TIO, int DK>
+hipError_t scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
+{
+    if (p.segments > 1) {
+        hipError_t e = launch<TIO, DK, kEnd>(p, o, s);
+        if (e != hipSuccess) return e;
+        const unsigned grid = (unsigned)(p.heads * (p.dvp / 16)) * (o ? 2 : 1);
+        delta_join_kernel<DK><<<grid, 64, 0, s>>>(p);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return o ? launch<TIO, DK, kSave>(p, o, s) : launch<TIO, DK, kRead>(p, o, s);
+}
+
+}  // namespace
+
+hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
+{
+    const int DK = delta_padded_dk(p.f.dk);
+    if (p.f.bf16)
+        return DK == 32 ? scans<uint16_t, 32>(p, o, s)
+             : DK == 64 ? scans<uint16_t, 64>(p, o, s) : scans<uint16_t, 128>(p, o, s);
+    return DK == 32 ? scans<float, 32>(p, o, s)
+         : DK == 64 ? scans<float, 64>(p, o, s) : scans<float, 128>(p, o, s);
+}
+
+// Segments of a sequence.  A share's time goes with its chunks and with how often the compute
+// units are filled: one workgroup fits a unit (two where ends are found alone).  The ends and the
+// second run cost 2 / segments of the sequence where they fit at once, so cutting pays from few
+// heads on (measured figures at the kernels' top).
+int delta_segments(int heads, int chunks, int dv, int dk, bool backward)
+{
+    const long long parts = (dv + 63) / 64, wide = (delta_padded_dk(dk) + 63) / 64, cus = 256;
+    auto rounds = [&](long long shares) { return (heads * shares + cus - 1) / cus; };
+    const long long sides = backward ? 2 : 1;
+    long long best = rounds(sides * parts) * chunks;
+    int segments = 1;
+    for (int n = 3; n <= 32 && chunks / n >= 4; ++n) {
+        const long long each = (chunks + n - 1) / n;
+        if ((chunks + each - 1) / each != n) continue;   // (no empty segments)
+        const long long ends = rounds(sides * (n - 1) * parts + (n - 2) * wide), run = rounds(sides * n * parts);
+        // the chain of joins: about two chunks' time a segment
+        const long long cost = (ends + run) * each + 2 * n;
+        if (cost < best) { best = cost; segments = n; }
+    }
+    return segments;
+}
+
+}  // namespace ttt

@@ -102,6 +102,18 @@ def test_forward(dev, shape, io, layout):
     check_fwd(c, *ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, layout=layout))
 
 
+# few heads and many tokens: sequences in segments
+LONG = [(1, 1, 1, 2000, 64, 64), (1, 2, 2, 2600, 128, 128), (2, 1, 1, 1601, 32, 83), (1, 1, 1, 3000, 50, 200)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", LONG)
+def test_long_sequences_of_few_heads(dev, shape, io):
+    c = Case(dev, *shape, io, ttt.LAYOUT_BTHD, seed=sum(shape), forget=(700, 1500))
+    check_fwd(c, *ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, layout=c.layout))
+    check_bwd(c, ttt.delta_bwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW, layout=c.layout))
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("forget", [(0,), (63,), (64,), (10, 11, 64, 65, 140), tuple(range(0, 150, 3)), (149,)])
 def test_forward_forgets(dev, io, forget):
