@@ -289,7 +289,8 @@ constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr size_t kPassBytes = (size_t)1 << 30;   // of workspace, where one head needs no more
 
 struct Plan {
-    int chunks, groups, dvp, segments;   // groups of heads that share keys, in one pass
+    DeltaCut cut;
+    int chunks, groups, dvp;   // groups of heads that share keys, in one pass
     size_t S, P, ends, transitions, bytes;   // places in the workspace, which begins with the records
 };
 
@@ -302,8 +303,8 @@ Plan fwd_plan(int B, int H, int Hk, int T, int dk, int dv, bool bf16)
     const size_t s = 3 * part, z = (bf16 ? 2 : 3) * part, one = unit * (sizeof(Record) + s + z);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
     const size_t heads = p.groups * share, units = unit * p.groups, DK = delta_padded_dk(dk);
-    p.segments = delta_segments((int)heads, p.chunks, dv, dk, false);
-    const size_t cut = p.segments > 1 ? heads * p.segments * DK * 4 : 0;
+    p.cut = delta_cut((int)heads, p.chunks, dv, dk, false);
+    const size_t cut = p.cut.segments > 1 ? heads * p.cut.segments * DK * 4 : 0;
     p.S = up256(units * sizeof(Record));
     p.P = p.S + up256(units * s);
     p.ends = p.P + up256(units * z);
@@ -339,8 +340,7 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
     p.f = a;
     p.chunks = plan.chunks;
     p.dvp = plan.dvp;
-    p.segments = plan.segments;
-    p.segment_chunks = (plan.chunks + plan.segments - 1) / plan.segments;
+    p.cut = plan.cut;
     p.records = (Record*)ws;
     p.S = (quad*)(ws + plan.S);
     p.P = (quad*)(ws + plan.P);

@@ -293,7 +293,8 @@ constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr size_t kPassBytes = (size_t)4 << 30;
 
 struct Plan {
-    int chunks, groups, dvp, segments;
+    DeltaCut cut;
+    int chunks, groups, dvp;
     size_t S, St, P, states, cotangents, U, F, dK, dQ, ends, ends_back, transitions, bytes;
 };
 
@@ -318,8 +319,8 @@ Plan bwd_plan(int B, int H, int Hk, int T, int dk, int dv)
     p.dK = p.F + up256(units * rows);
     p.dQ = p.dK + up256(units * sums);
     const size_t heads = (size_t)p.groups * (H / Hk);
-    p.segments = delta_segments((int)heads, p.chunks, dv, dk, true);
-    const size_t cut = p.segments > 1 ? heads * p.segments * DK * 4 : 0;
+    p.cut = delta_cut((int)heads, p.chunks, dv, dk, true);
+    const size_t cut = p.cut.segments > 1 ? heads * p.cut.segments * DK * 4 : 0;
     p.ends = p.dQ + up256(units * sums);
     p.ends_back = p.ends + up256(cut * p.dvp);
     p.transitions = p.ends_back + up256(cut * p.dvp);
@@ -345,8 +346,7 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
     p.f = f;
     p.chunks = plan.chunks;
     p.dvp = plan.dvp;
-    p.segments = plan.segments;
-    p.segment_chunks = (plan.chunks + plan.segments - 1) / plan.segments;
+    p.cut = plan.cut;
     p.ends = (float*)(ws + plan.ends);
     p.ends_back = (float*)(ws + plan.ends_back);
     p.transitions = (float*)(ws + plan.transitions);

@@ -117,10 +117,10 @@ struct Tile {
     TIO x[kChunk * LD];
 };
 
-// a tile on its way from memory: each of 256 threads holds its granules
-template <typename TIO, int DK>
+// a tile on its way from memory: each of N threads holds its granules
+template <typename TIO, int DK, int THREADS = 256>
 struct TileLoad {
-    static constexpr int N = Tile<TIO, DK>::GRANULES / 256;
+    static constexpr int N = Tile<TIO, DK>::GRANULES / THREADS;
     static constexpr int ROW = DK / kGran<TIO>;
     quad q[N];
     // a tile that lies within the rows and columns
@@ -130,7 +130,7 @@ struct TileLoad {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             q[i] = *reinterpret_cast<const quad*>(p);
-            p += 256 / ROW * src.stride;
+            p += THREADS / ROW * src.stride;
         }
     }
     // (columns from `first` of rows of d)
@@ -139,7 +139,7 @@ struct TileLoad {
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = tid + 256 * i, r = e / ROW, col = first + (e % ROW) * kGran<TIO>;
+            const int e = tid + THREADS * i, r = e / ROW, col = first + (e % ROW) * kGran<TIO>;
             q[i] = t0 + r < T ? load_granule(src.at(t0 + r), col, d, whole) : quad{0u, 0u, 0u, 0u};
         }
     }
@@ -147,7 +147,7 @@ struct TileLoad {
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = tid + 256 * i, r = e / ROW, col = (e % ROW) * kGran<TIO>;
+            const int e = tid + THREADS * i, r = e / ROW, col = (e % ROW) * kGran<TIO>;
             *reinterpret_cast<quad*>(to.x + r * Tile<TIO, DK>::LD + col) = q[i];
         }
     }
@@ -248,49 +248,54 @@ __device__ __forceinline__ Parts<N> load_frag(const quad* from, int f, int lane)
     return r;
 }
 
-// N quads on their way from memory to LDS, over 256 threads
-template <int N>
+// N quads on their way from memory to LDS
+template <int N, int THREADS>
 struct LinearLoad {
-    static constexpr int PER = (N + 255) / 256;
+    static constexpr int PER = (N + THREADS - 1) / THREADS;
     quad q[PER];
     __device__ __forceinline__ void load(const quad* from, int tid)
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (N % 256 == 0 || tid + 256 * i < N) q[i] = from[tid + 256 * i];
+            if (N % THREADS == 0 || tid + THREADS * i < N) q[i] = from[tid + THREADS * i];
     }
     __device__ __forceinline__ void put(quad* to, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (N % 256 == 0 || tid + 256 * i < N) to[tid + 256 * i] = q[i];
+            if (N % THREADS == 0 || tid + THREADS * i < N) to[tid + THREADS * i] = q[i];
     }
 };
 
-// What a scan's workgroup needs of a chunk beside keys and queries: operands of S (3 parts)
-// and P (NP of them), eta, start and end of its tokens, and 64 columns of V or dZ.
-template <typename TIO, int DK, int NP, bool Q>
+// A scan's workgroup of four waves: all compute, 16 columns of values each, and load as well
+// (CW = 4), or two compute and two load (CW = 2).
+template <int CW> constexpr int kLoaders = CW == 4 ? 256 : 128;
+
+// What it needs of a chunk: keys, queries, its columns of V or dZ, operands of S (3 parts) and
+// P (NP of them), eta, start and end of the tokens.
+template <typename TIO, int DK, int NP, bool Q, int CW>
 struct ChunkTiles {
     Tile<TIO, DK> k;
     Tile<TIO, Q ? DK : kGran<TIO>> q;
-    Tile<TIO, 64> v;
+    Tile<TIO, 16 * CW> v;
     quad s[3 * kFragQuads], p[NP ? NP * kFragQuads : 1];
     float eta[kChunk], start[kChunk], end[kChunk];
 };
 
-template <typename TIO, int DK, int NP, bool Q>
+// the same on its way, in the loading waves' registers
+template <typename TIO, int DK, int NP, bool Q, int CW>
 struct ChunkLoad {
-    TileLoad<TIO, DK> k, q;
-    TileLoad<TIO, 64> v;
-    LinearLoad<3 * kFragQuads> s;
-    LinearLoad<NP ? NP * kFragQuads : 1> p;
-    float rec;
+    TileLoad<TIO, DK, kLoaders<CW>> k, q;
+    TileLoad<TIO, 16 * CW, kLoaders<CW>> v;
+    LinearLoad<3 * kFragQuads, kLoaders<CW>> s;
+    LinearLoad<NP ? NP * kFragQuads : 1, kLoaders<CW>> p;
+    LinearLoad<3 * kChunk / 4, kLoaders<CW>> rec;
     __device__ __forceinline__ void load(const Rows<const TIO>& K, const Rows<const TIO>& Qr,
                                          const Rows<const TIO>& V, const quad* S, const quad* P,
                                          const Record* r, int t0, int T, int dk, int dv, int first,
                                          bool whole_k, bool whole_v, int tid)
     {
-        if (whole_k && whole_v && dk == DK && first + 64 <= dv && t0 + kChunk <= T) {
+        if (whole_k && whole_v && dk == DK && first + 16 * CW <= dv && t0 + kChunk <= T) {
             k.load_inside(K, t0, tid);
             if constexpr (Q) q.load_inside(Qr, t0, tid);
             v.load_inside(V, t0, tid, first);
@@ -301,16 +306,16 @@ struct ChunkLoad {
         }
         s.load(S, tid);
         if constexpr (NP > 0) p.load(P, tid);
-        if (tid < 3 * kChunk) rec = r->eta[tid];   // (eta, start and end lie one after the other)
+        rec.load(reinterpret_cast<const quad*>(r->eta), tid);   // (eta, start and end: one after the other)
     }
-    __device__ __forceinline__ void put(ChunkTiles<TIO, DK, NP, Q>& to, int tid) const
+    __device__ __forceinline__ void put(ChunkTiles<TIO, DK, NP, Q, CW>& to, int tid) const
     {
         k.put(to.k, tid);
         if constexpr (Q) q.put(to.q, tid);
         v.put(to.v, tid);
         s.put(to.s, tid);
         if constexpr (NP > 0) p.put(to.p, tid);
-        if (tid < 3 * kChunk) to.eta[tid] = rec;
+        rec.put(reinterpret_cast<quad*>(to.eta), tid);
     }
 };
 

@@ -42,6 +42,12 @@ size_t delta_bwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool bf1
 struct Record;
 typedef uint32_t quad __attribute__((ext_vector_type(4)));
 
+// segments of a sequence, chunks of each, 32 columns a workgroup (or 64)
+struct DeltaCut {
+    int segments, chunks;
+    bool narrow;
+};
+
 struct DeltaPass {
     DeltaArgs f;
     int head0, heads;        // heads of values, counted through the batch: whole groups
@@ -51,7 +57,7 @@ struct DeltaPass {
     quad *S, *St, *P;        // operands of S, of its transpose (backward), of P (or its transpose)
     float *states, *cotangents;   // [heads][chunks][DK][dvp]: W^T before a chunk, D^T after it
     float *U, *F;            // [heads][chunks][64][dvp]
-    int segments, segment_chunks;
+    DeltaCut cut;
     float *ends, *ends_back; // [heads][segments][DK][dvp]: states and their gradients past a segment
     float* transitions;      // [heads][segments][DK][DK]
 };
@@ -59,7 +65,7 @@ struct DeltaPass {
 hipError_t launch_delta_prepare(const DeltaPass& p, bool backward, hipStream_t s);
 // the scan over the chunks; with `o` both scans of a backward pass, which keep states, U, D and F
 hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s);
-int delta_segments(int heads, int chunks, int dv, int dk, bool backward);
+DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward);
 // features of a head as the kernels hold them
 inline int delta_padded_dk(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : 128; }
 

@@ -42,16 +42,16 @@ __device__ __forceinline__ void load_plane(const float* X, int ld, int col, int 
         for (int e = 0; e < 4; ++e) x[m][e] = X[(size_t)(16 * m + 4 * g + e) * ld + col];
 }
 
-// a workgroup's share: 64 columns from `first` of one head's segment
+// a workgroup's share: 16 CW columns from `first` of one head's segment
 struct Share {
     int local, segment, first;
 };
 
 // Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
-template <typename TIO, int DK, int KEEP>
+template <typename TIO, int DK, int KEEP, int CW>
 struct Forward {
     static constexpr int NZ = KEEP == kRead ? kZParts<TIO> : 0;
-    typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead> Tiles;
+    typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
 
     // `unit`: V = 0 and a unit matrix for the start, columns are features
@@ -64,7 +64,7 @@ struct Forward {
         const int b = head / a.f.H, h = head % a.f.H, hk = h / (a.f.H / a.f.Hk);
         const int T = a.f.T, dk = a.f.dk, dv = a.f.dv;
         const int col = first + 16 * w + c;
-        const bool works = first + 16 * w < (unit ? DK : a.dvp);   // (else a wave only helps to load)
+        const bool works = first + 16 * w < (unit ? DK : a.dvp);
         const bool whole_k = dk % kGran<TIO> == 0, whole_v = dv % kGran<TIO> == 0, fours = dv % 4 == 0;
         const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
         const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
@@ -72,16 +72,31 @@ struct Forward {
         const Rows<TIO> Z((TIO*)a.f.Z, b, h, a.f.H, T, dv, a.f.tokens_first);
         const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        const int begin = s.segment * a.segment_chunks;
-        const int stop = begin + a.segment_chunks < a.chunks ? begin + a.segment_chunks : a.chunks;
+        const int begin = s.segment * a.cut.chunks;
+        const int stop = begin + a.cut.chunks < a.chunks ? begin + a.cut.chunks : a.chunks;
 
-        ChunkLoad<TIO, DK, NZ, KEEP == kRead> next;
+        const int id = CW == 4 ? tid : tid - 128;
+        ChunkLoad<TIO, DK, NZ, KEEP == kRead, CW> next;
         auto fetch = [&](int n) {
             const size_t at = unit0 + n;
             next.load(K, Q, V, a.S + at * 3 * kFragQuads, a.P + at * NZ * kFragQuads, a.records + at,
-                      n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+                      n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
         };
-        fetch(begin);
+        auto put = [&](int n) { next.put(tiles[NB == 2 ? (n - begin) & 1 : 0], id); };
+        if (CW == 2 && w >= 2) {
+            fetch(begin);
+            put(begin);
+            if (begin + 1 < stop) fetch(begin + 1);
+            __syncthreads();
+            for (int n = begin; n < stop; ++n) {
+                if constexpr (NB == 1) __syncthreads();
+                if (n + 1 < stop) put(n + 1);
+                if (n + 2 < stop) fetch(n + 2);
+                __syncthreads();
+            }
+            return;
+        }
+        if constexpr (CW == 4) fetch(begin);
         f32x4 W[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) W[m] = zero;
@@ -95,19 +110,19 @@ struct Forward {
 #pragma unroll
                 for (int m = 0; m < M; ++m) W[m] = load_state(a.f.W0 + state, col, 16 * m + 4 * g, dv, dk);
         } else if (KEEP != kEnd && works) {
-            load_plane(a.ends + ((size_t)local * a.segments + s.segment - 1) * DK * a.dvp, a.dvp, col, g, W);
+            load_plane(a.ends + ((size_t)local * a.cut.segments + s.segment - 1) * DK * a.dvp, a.dvp, col, g, W);
         }
-        next.put(tiles[0], tid);
+        if constexpr (CW == 4) put(begin);
         __syncthreads();
 
         for (int n = begin; n < stop; ++n) {
             const Tiles& t = tiles[NB == 2 ? (n - begin) & 1 : 0];
-            if (n + 1 < stop) fetch(n + 1);
+            if (CW == 4 && n + 1 < stop) fetch(n + 1);
             if (works) {
                 typedef Parts<kParts<TIO>> In;
-                In kt[J][4];
+                In kt[J][4], vp[2];
                 Parts<3> S[kFrags], x[2];
-                f32x4 r[4], z[4], v[4], eta[4], start[4], ends[4];
+                f32x4 r[4], z[4], eta[4], start[4], ends[4];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -120,9 +135,7 @@ struct Forward {
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const In p = by_feature(t.v, w, j, lane);
-                    v[2 * j] = unit ? zero : widen_parts(p, false);
-                    v[2 * j + 1] = unit ? zero : widen_parts(p, true);
+                    vp[j] = by_feature(t.v, w, j, lane);
                 }
 #pragma unroll
                 for (int f = 0; f < kFrags; ++f) S[f] = load_frag<3>(t.s, f, lane);
@@ -146,7 +159,10 @@ struct Forward {
                     for (int j = 0; j < 2; ++j) kf[m][j] = by_feature(t.k, m, j, lane);
                 reads_before();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] = v[i] - start[i] * r[i];
+                for (int i = 0; i < 4; ++i) {
+                    r[i] *= -start[i];
+                    if (!unit) r[i] += widen_parts(vp[i / 2], i & 1);
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     x[j] = split<3>(-(eta[2 * j] * r[2 * j]), -(eta[2 * j + 1] * r[2 * j + 1]));
@@ -191,7 +207,7 @@ struct Forward {
 #pragma unroll
                         for (int i = 2 * j; i < 4; ++i) z[i] = mma<OZ>(u[j], P[frag_lower(i, j)], z[i]);
                     const int token = n * kChunk + c;
-                    if (fours && first + 64 <= dv && (n + 1) * kChunk <= T) {
+                    if (fours && first + 16 * CW <= dv && (n + 1) * kChunk <= T) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             store4(Z.at(token + 16 * i), first + 16 * w + 4 * g, dv, true, z[i]);
@@ -204,12 +220,12 @@ struct Forward {
                 }
             }
             if constexpr (NB == 1) __syncthreads();
-            if (n + 1 < stop) next.put(tiles[NB == 2 ? (n + 1 - begin) & 1 : 0], tid);
+            if (CW == 4 && n + 1 < stop) put(n + 1);
             __syncthreads();
         }
         if constexpr (KEEP == kEnd) {
             if (!works) return;
-            const size_t at = (size_t)local * a.segments + s.segment;
+            const size_t at = (size_t)local * a.cut.segments + s.segment;
             if (unit) store_plane(a.transitions + at * DK * DK, DK, col, g, W);
             else store_plane(a.ends + at * DK * a.dvp, a.dvp, col, g, W);
         }
@@ -221,9 +237,9 @@ struct Forward {
     }
 };
 
-template <typename TIO, int DK, int KEEP>
+template <typename TIO, int DK, int KEEP, int CW>
 struct Reverse {
-    typedef ChunkTiles<TIO, DK, 3, true> Tiles;
+    typedef ChunkTiles<TIO, DK, 3, true, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
 
     static __device__ __forceinline__ void run(const DeltaPass& a, const DeltaBwdArgs& o, Tiles* tiles, Share s)
@@ -242,16 +258,31 @@ struct Reverse {
         const Rows<const TIO> dZ((const TIO*)o.dZ, b, h, a.f.H, T, dv, a.f.tokens_first);
         const size_t state = (size_t)head * dv * dk, unit0 = (size_t)local * a.chunks;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        const int begin = s.segment * a.segment_chunks;
-        const int last = (begin + a.segment_chunks < a.chunks ? begin + a.segment_chunks : a.chunks) - 1;
+        const int begin = s.segment * a.cut.chunks;
+        const int last = (begin + a.cut.chunks < a.chunks ? begin + a.cut.chunks : a.chunks) - 1;
 
-        ChunkLoad<TIO, DK, 3, true> next;
+        const int id = CW == 4 ? tid : tid - 128;
+        ChunkLoad<TIO, DK, 3, true, CW> next;
         auto fetch = [&](int n) {
             const size_t at = unit0 + n;
             next.load(K, Q, dZ, a.St + at * 3 * kFragQuads, a.P + at * 3 * kFragQuads, a.records + at,
-                      n * kChunk, T, dk, dv, first, whole_k, whole_v, tid);
+                      n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
         };
-        fetch(last);
+        auto put = [&](int n) { next.put(tiles[NB == 2 ? n & 1 : 0], id); };
+        if (CW == 2 && w >= 2) {
+            fetch(last);
+            put(last);
+            if (last > begin) fetch(last - 1);
+            __syncthreads();
+            for (int n = last; n >= begin; --n) {
+                if constexpr (NB == 1) __syncthreads();
+                if (n > begin) put(n - 1);
+                if (n > begin + 1) fetch(n - 2);
+                __syncthreads();
+            }
+            return;
+        }
+        if constexpr (CW == 4) fetch(last);
         f32x4 D[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) D[m] = zero;
@@ -260,14 +291,14 @@ struct Reverse {
 #pragma unroll
                 for (int m = 0; m < M; ++m) D[m] = load_state(o.dW_T + state, col, 16 * m + 4 * g, dv, dk);
         } else if (KEEP != kEnd && works) {
-            load_plane(a.ends_back + ((size_t)local * a.segments + s.segment + 1) * DK * a.dvp, a.dvp, col, g, D);
+            load_plane(a.ends_back + ((size_t)local * a.cut.segments + s.segment + 1) * DK * a.dvp, a.dvp, col, g, D);
         }
-        next.put(tiles[NB == 2 ? last & 1 : 0], tid);
+        if constexpr (CW == 4) put(last);
         __syncthreads();
 
         for (int n = last; n >= begin; --n) {
             const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
-            if (n > begin) fetch(n - 1);
+            if (CW == 4 && n > begin) fetch(n - 1);
             if (works) {
                 const size_t unit = unit0 + n;
                 typedef Parts<NP> In;
@@ -352,11 +383,11 @@ struct Reverse {
                     }
             }
             if constexpr (NB == 1) __syncthreads();
-            if (n > begin) next.put(tiles[NB == 2 ? (n - 1) & 1 : 0], tid);
+            if (CW == 4 && n > begin) put(n - 1);
             __syncthreads();
         }
         if constexpr (KEEP == kEnd) {
-            if (works) store_plane(a.ends_back + ((size_t)local * a.segments + s.segment) * DK * a.dvp, a.dvp, col, g, D);
+            if (works) store_plane(a.ends_back + ((size_t)local * a.cut.segments + s.segment) * DK * a.dvp, a.dvp, col, g, D);
         } else if (begin == 0 && o.dW0) {
 #pragma unroll
             for (int m = 0; m < M; ++m) store_state(o.dW0 + state, col, 16 * m + 4 * g, dv, dk, D[m]);
@@ -364,48 +395,55 @@ struct Reverse {
     }
 };
 
-// One launch of all shares of a kind.  Forward alone: kRead over all segments, or the ends of
-// all but the last and the transitions of all but the first and last.  With the backward pass:
-// kSave of both scans, or all three kinds of ends.
-template <typename TIO, int DK, int KEEP>
-__global__ void __launch_bounds__(256, 1) delta_scan_kernel(DeltaPass a)
+// column parts of a head's segment, the transition's among them
+template <int CW>
+__host__ __device__ __forceinline__ int widest(const DeltaPass& a, int DK)
 {
-    typedef typename Forward<TIO, DK, KEEP>::Tiles Tiles;
-    __shared__ __align__(16) Tiles tiles[kBuffers<Tiles>];
-    const int parts = (a.dvp + 63) / 64, wide = (DK + 63) / 64;
-    const int ends = KEEP == kEnd ? (a.segments - 1) * parts : a.segments * parts;
-    const int each = ends + (KEEP == kEnd ? (a.segments - 2) * wide : 0);
-    const int local = blockIdx.x / each;
-    int k = blockIdx.x % each;
-    const bool unit = k >= ends;
-    if (unit) k -= ends;
-    const Share s = {local, unit ? 1 + k / wide : k / parts, 64 * (unit ? k % wide : k % parts)};
-    Forward<TIO, DK, KEEP>::run(a, tiles, s, unit);
+    return ((a.cut.segments > 1 && DK > a.dvp ? DK : a.dvp) + 16 * CW - 1) / (16 * CW);
 }
 
-template <typename TIO, int DK, int KEEP>
+// One launch of all shares of a kind, the column parts of a segment on one XCD (they share its
+// keys and operands in L2).  Forward alone: kRead over all segments, or the ends of
+// all but the last and the transitions of all but the first and last.  With the backward pass:
+// kSave of both scans, or all three kinds of ends.
+template <typename TIO, int DK, int KEEP, int CW>
+__global__ void __launch_bounds__(256, 1) delta_scan_kernel(DeltaPass a)
+{
+    typedef typename Forward<TIO, DK, KEEP, CW>::Tiles Tiles;
+    __shared__ __align__(16) Tiles tiles[kBuffers<Tiles>];
+    const int ends = KEEP == kEnd ? a.cut.segments - 1 : a.cut.segments;
+    const int each = ends + (KEEP == kEnd ? a.cut.segments - 2 : 0);
+    int id, part;
+    xcd_unit_part(blockIdx.x, widest<CW>(a, DK), id, part);
+    const int local = id / each, k = id % each;
+    const bool unit = k >= ends;
+    const Share s = {local, unit ? 1 + k - ends : k, 16 * CW * part};
+    if (local >= a.heads || s.first >= (unit ? DK : a.dvp)) return;
+    Forward<TIO, DK, KEEP, CW>::run(a, tiles, s, unit);
+}
+
+template <typename TIO, int DK, int KEEP, int CW>
 __global__ void __launch_bounds__(256, 1) delta_scans_kernel(DeltaPass a, DeltaBwdArgs o)
 {
-    typedef typename Forward<TIO, DK, KEEP>::Tiles There;
-    typedef typename Reverse<TIO, DK, KEEP>::Tiles Back;
+    typedef typename Forward<TIO, DK, KEEP, CW>::Tiles There;
+    typedef typename Reverse<TIO, DK, KEEP, CW>::Tiles Back;
     constexpr size_t room = kBuffers<There> * sizeof(There) > kBuffers<Back> * sizeof(Back)
                                 ? kBuffers<There> * sizeof(There) : kBuffers<Back> * sizeof(Back);
     __shared__ __align__(16) char tiles[room];
-    const int parts = (a.dvp + 63) / 64, wide = (DK + 63) / 64;
-    const int ends = KEEP == kEnd ? (a.segments - 1) * parts : a.segments * parts;
-    const int each = 2 * ends + (KEEP == kEnd ? (a.segments - 2) * wide : 0);
-    const int local = blockIdx.x / each;
-    int k = blockIdx.x % each;
-    if (k < ends) {
-        const Share s = {local, k / parts + (KEEP == kEnd ? 1 : 0), 64 * (k % parts)};
-        Reverse<TIO, DK, KEEP>::run(a, o, (Back*)tiles, s);
+    const int ends = KEEP == kEnd ? a.cut.segments - 1 : a.cut.segments;
+    const int each = 2 * ends + (KEEP == kEnd ? a.cut.segments - 2 : 0);
+    int id, part;
+    xcd_unit_part(blockIdx.x, widest<CW>(a, DK), id, part);
+    const int local = id / each, k = id % each;
+    const bool back = k < ends, unit = k >= 2 * ends;
+    const Share s = {local, back ? k + (KEEP == kEnd ? 1 : 0) : unit ? 1 + k - 2 * ends : k - ends,
+                     16 * CW * part};
+    if (local >= a.heads || s.first >= (unit ? DK : a.dvp)) return;
+    if (back) {
+        Reverse<TIO, DK, KEEP, CW>::run(a, o, (Back*)tiles, s);
         return;
     }
-    k -= ends;
-    const bool unit = k >= ends;
-    if (unit) k -= ends;
-    const Share s = {local, unit ? 1 + k / wide : k / parts, 64 * (unit ? k % wide : k % parts)};
-    Forward<TIO, DK, KEEP>::run(a, (There*)tiles, s, unit);
+    Forward<TIO, DK, KEEP, CW>::run(a, (There*)tiles, s, unit);
 }
 
 // The segments' ends, one after the other: with X^T_s the state that segment s - 1 leaves (its end
@@ -419,12 +457,12 @@ __global__ void __launch_bounds__(64) delta_join_kernel(DeltaPass a)
     const bool back = blockIdx.x >= (unsigned)(a.heads * parts);
     const int id = blockIdx.x % (a.heads * parts), local = id / parts, col = 16 * (id % parts) + c;
     const size_t plane = (size_t)DK * a.dvp;
-    float* ends = (back ? a.ends_back : a.ends) + (size_t)local * a.segments * plane;
+    float* ends = (back ? a.ends_back : a.ends) + (size_t)local * a.cut.segments * plane;
     f32x4 X[M];
-    load_plane(ends + (back ? (a.segments - 1) * plane : 0), a.dvp, col, g, X);
-    for (int k = 1; k < a.segments - 1; ++k) {
-        const int s = back ? a.segments - 1 - k : k;
-        const float* A = a.transitions + ((size_t)local * a.segments + s) * DK * DK;
+    load_plane(ends + (back ? (a.cut.segments - 1) * plane : 0), a.dvp, col, g, X);
+    for (int k = 1; k < a.cut.segments - 1; ++k) {
+        const int s = back ? a.cut.segments - 1 - k : k;
+        const float* A = a.transitions + ((size_t)local * a.cut.segments + s) * DK * DK;
         Parts<3> x[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) x[j] = split<3>(X[2 * j], X[2 * j + 1]);
@@ -450,35 +488,41 @@ __global__ void __launch_bounds__(64) delta_join_kernel(DeltaPass a)
     }
 }
 
-template <typename TIO, int DK, int KEEP>
+template <typename TIO, int DK, int KEEP, int CW>
 hipError_t launch(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
 {
-    const size_t parts = (p.dvp + 63) / 64, wide = (DK + 63) / 64;
-    const size_t ends = (KEEP == kEnd ? p.segments - 1 : p.segments) * parts;
-    const size_t units = KEEP == kEnd ? (p.segments - 2) * wide : 0;
+    const size_t ends = KEEP == kEnd ? p.cut.segments - 1 : p.cut.segments;
+    const size_t each = (o ? 2 : 1) * ends + (KEEP == kEnd ? p.cut.segments - 2 : 0);
+    const unsigned grid = (unsigned)((p.heads * each + 7) / 8 * 8 * widest<CW>(p, DK));
     if constexpr (KEEP != kSave) {
         if (!o) {
-            delta_scan_kernel<TIO, DK, KEEP><<<(unsigned)(p.heads * (ends + units)), 256, 0, s>>>(p);
+            delta_scan_kernel<TIO, DK, KEEP, CW><<<grid, 256, 0, s>>>(p);
             return hipGetLastError();
         }
     }
     if constexpr (KEEP != kRead)
-        delta_scans_kernel<TIO, DK, KEEP><<<(unsigned)(p.heads * (2 * ends + units)), 256, 0, s>>>(p, *o);
+        delta_scans_kernel<TIO, DK, KEEP, CW><<<grid, 256, 0, s>>>(p, *o);
     return hipGetLastError();
 }
 
-template <typename TIO, int DK>
-hipError_t scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
+template <typename TIO, int DK, int CW>
+hipError_t scans_as(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
 {
-    if (p.segments > 1) {
-        hipError_t e = launch<TIO, DK, kEnd>(p, o, s);
+    if (p.cut.segments > 1) {
+        hipError_t e = launch<TIO, DK, kEnd, CW>(p, o, s);
         if (e != hipSuccess) return e;
         const unsigned grid = (unsigned)(p.heads * (p.dvp / 16)) * (o ? 2 : 1);
         delta_join_kernel<DK><<<grid, 64, 0, s>>>(p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return o ? launch<TIO, DK, kSave>(p, o, s) : launch<TIO, DK, kRead>(p, o, s);
+    return o ? launch<TIO, DK, kSave, CW>(p, o, s) : launch<TIO, DK, kRead, CW>(p, o, s);
+}
+
+template <typename TIO, int DK>
+hipError_t scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
+{
+    return p.cut.narrow ? scans_as<TIO, DK, 2>(p, o, s) : scans_as<TIO, DK, 4>(p, o, s);
 }
 
 }  // namespace
@@ -493,26 +537,37 @@ hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStre
          : DK == 64 ? scans<float, 64>(p, o, s) : scans<float, 128>(p, o, s);
 }
 
-// Segments of a sequence.  A share's time goes with its chunks and with how often the compute
-// units are filled: one workgroup fits a unit (two where ends are found alone).  The ends and the
-// second run cost 2 / segments of the sequence where they fit at once, so cutting pays from few
-// heads on (measured figures at the kernels' top).
-int delta_segments(int heads, int chunks, int dv, int dk, bool backward)
+// How a sequence is cut: into how many segments, and whether a workgroup takes 32 columns or 64.
+// A round of workgroups over the 256 compute units takes its chunks times (8 x 12 heads of 64
+// features, us a chunk) 4.0 with 64 columns and 2.6 with 32, where the workgroup's waves meet less
+// in LDS; where only ends are found 2.3 and 1.8.  The ends and the second run cost 2 / segments of
+// the sequence where they fit at once, so segments pay from few heads on (1 x 32 heads of 64
+// features, 32768 tokens: 2.05 ms whole, 0.82 ms in 8 segments).
+DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward)
 {
-    const long long parts = (dv + 63) / 64, wide = (delta_padded_dk(dk) + 63) / 64, cus = 256;
+    const long long sides = backward ? 2 : 1, cus = 256;
     auto rounds = [&](long long shares) { return (heads * shares + cus - 1) / cus; };
-    const long long sides = backward ? 2 : 1;
-    long long best = rounds(sides * parts) * chunks;
-    int segments = 1;
-    for (int n = 3; n <= 32 && chunks / n >= 4; ++n) {
-        const long long each = (chunks + n - 1) / n;
-        if ((chunks + each - 1) / each != n) continue;   // (no empty segments)
-        const long long ends = rounds(sides * (n - 1) * parts + (n - 2) * wide), run = rounds(sides * n * parts);
-        // the chain of joins: about two chunks' time a segment
-        const long long cost = (ends + run) * each + 2 * n;
-        if (cost < best) { best = cost; segments = n; }
+    DeltaCut best = {1, chunks, false};
+    long long least = -1;
+    for (int narrow = 0; narrow < 2; ++narrow) {
+        const int columns = narrow ? 32 : 64;
+        const long long parts = (dv + columns - 1) / columns;
+        const long long wide = (delta_padded_dk(dk) + columns - 1) / columns;
+        for (int n = 1; n <= 32 && (n == 1 || chunks / n >= 4); ++n) {
+            if (n == 2) continue;                      // (the ends alone are half of it then)
+            const int each = (chunks + n - 1) / n;
+            if ((chunks + each - 1) / each != n) continue;   // (no empty segments)
+            long long cost = rounds(sides * n * parts) * (narrow ? 26 : 40) * each;
+            // the ends, and joins of about a chunk's time
+            if (n > 1)
+                cost += rounds(sides * (n - 1) * parts + (n - 2) * wide) * (narrow ? 18 : 23) * each + 40 * n;
+            if (least < 0 || cost < least) {
+                least = cost;
+                best = {n, each, narrow != 0};
+            }
+        }
     }
-    return segments;
+    return best;
 }
 
 }  // namespace ttt
