@@ -186,14 +186,14 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
 }
 
 // ---- token after token ---------------------------------------------------------------
-// 16 lanes hold a row of the state, 4 X features each; a workgroup of 256 threads 16 rows.
+// 16 lanes hold R rows of the state, 4 X features of each; a workgroup of 256 threads 16 R rows.
 // HBM bounds the decoded token of a large batch (the state in and out).  W k and W q are
 // summed at once: z = exp(g) W q + eta u (k.q).
-template <typename TIO, int X>
+template <typename TIO, int X, int R>
 __global__ void __launch_bounds__(256) delta_step_kernel(DeltaArgs a, int parts)
 {
     const int tid = threadIdx.x, c = tid & 15;
-    const int head = blockIdx.x / parts, row = (blockIdx.x % parts) * 16 + (tid >> 4);
+    const int head = blockIdx.x / parts, row0 = (blockIdx.x % parts) * 16 * R + (tid >> 4);
     const int b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk), T = a.T, dk = a.dk, dv = a.dv;
     const Rows<const TIO> K((const TIO*)a.K, b, hk, a.Hk, T, dk, a.tokens_first);
     const Rows<const TIO> Q((const TIO*)a.Q, b, hk, a.Hk, T, dk, a.tokens_first);
@@ -201,79 +201,60 @@ __global__ void __launch_bounds__(256) delta_step_kernel(DeltaArgs a, int parts)
     const Rows<TIO> Z((TIO*)a.Z, b, h, a.H, T, dv, a.tokens_first);
     const Rows<const float> rg(a.g, b, h, a.H, T, 1, a.tokens_first);
     const Rows<const float> re(a.eta, b, h, a.H, T, 1, a.tokens_first);
-    const bool in = row < dv, fours = dk % 4 == 0;
-    const size_t state = ((size_t)head * dv + (in ? row : 0)) * dk;
+    const bool fours = dk % 4 == 0;
+    const size_t state = ((size_t)head * dv + row0) * dk;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    f32x4 W[X];
+    f32x4 W[R][X];
 #pragma unroll
-    for (int x = 0; x < X; ++x) {
-        const int f = 64 * x + 4 * c;
-        W[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (a.W0 && in) {
-            if (fours) {
-                if (f < dk) W[x] = *reinterpret_cast<const f32x4*>(a.W0 + state + f);
-            } else {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (f + v < dk) W[x][v] = a.W0[state + f + v];
-            }
-        }
-    }
-    auto four = [&](const TIO* p, int f) {
-        f32x4 r = {0.f, 0.f, 0.f, 0.f};
-        if (fours) {
-            if (f < dk) {
-                if constexpr (sizeof(TIO) == 2) r = widen4(*reinterpret_cast<const u32x2*>(p + f));
-                else r = *reinterpret_cast<const f32x4*>(p + f);
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                if (f + v < dk) r[v] = load1(p + f + v);
-        }
-        return r;
-    };
+        for (int x = 0; x < X; ++x)
+            W[r][x] = a.W0 && row0 + 16 * r < dv
+                          ? load4(a.W0 + state + (size_t)(16 * r) * dk, 64 * x + 4 * c, dk, fours) : zero;
     for (int t = 0; t < T; ++t) {
         f32x4 k[X], q[X];
+        float v[R];
 #pragma unroll
         for (int x = 0; x < X; ++x) {
-            k[x] = four(K.at(t), 64 * x + 4 * c);
-            q[x] = four(Q.at(t), 64 * x + 4 * c);
+            k[x] = load4(K.at(t), 64 * x + 4 * c, dk, fours);
+            q[x] = load4(Q.at(t), 64 * x + 4 * c, dk, fours);
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] = row0 + 16 * r < dv ? load1(V.at(t) + row0 + 16 * r) : 0.f;
         const float gt = a.g ? *rg.at(t) : 0.f, eta = a.eta ? *re.at(t) : a.eta_scalar;
-        const float v = in ? load1(V.at(t) + row) : 0.f;
         const float decay = gt <= kForget ? 0.f : expf(gt);
-        float sum[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < X; ++x) {
-            W[x] *= decay;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum[0] = fmaf(W[x][e], k[x][e], sum[0]);
-                sum[1] = fmaf(W[x][e], q[x][e], sum[1]);
-                sum[2] = fmaf(k[x][e], q[x][e], sum[2]);
-            }
-        }
-        row_sum16_n(sum);
-        const float u = eta * (v - sum[0]);
+        float sum[2 * R + 1] = {};
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) W[x][e] = fmaf(u, k[x][e], W[x][e]);
-        if (in && c == 0) store1(Z.at(t) + row, fmaf(u, sum[2], sum[1]));
-    }
-    if (a.W_out && in)
+            for (int e = 0; e < 4; ++e) {
+                sum[2 * R] = fmaf(k[x][e], q[x][e], sum[2 * R]);
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
-            const int f = 64 * x + 4 * c;
-            if (fours) {
-                if (f < dk) *reinterpret_cast<f32x4*>(a.W_out + state + f) = W[x];
-            } else {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (f + v < dk) a.W_out[state + f + v] = W[x][v];
+                for (int r = 0; r < R; ++r) {
+                    W[r][x][e] *= decay;
+                    sum[2 * r] = fmaf(W[r][x][e], k[x][e], sum[2 * r]);
+                    sum[2 * r + 1] = fmaf(W[r][x][e], q[x][e], sum[2 * r + 1]);
+                }
             }
+        row_sum16_n(sum);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float u = eta * (v[r] - sum[2 * r]);
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) W[r][x][e] = fmaf(u, k[x][e], W[r][x][e]);
+            if (row0 + 16 * r < dv && c == 0) store1(Z.at(t) + row0 + 16 * r, fmaf(u, sum[2 * R], sum[2 * r + 1]));
         }
+    }
+    if (a.W_out)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+                if (row0 + 16 * r < dv)
+                    store4(a.W_out + state + (size_t)(16 * r) * dk, 64 * x + 4 * c, dk, fours, W[r][x]);
 }
 
 template <typename TIO, int DK>
@@ -357,17 +338,26 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
     return hipSuccess;
 }
 
+template <typename TIO>
+static void step_as(const DeltaArgs& a, hipStream_t s)
+{
+    // four rows a lane where the card is full of workgroups all the same
+    const bool four = (long long)a.B * a.H * a.dv >= 65536;
+    const int parts = (a.dv + (four ? 63 : 15)) / (four ? 64 : 16);
+    const unsigned grid = (unsigned)(a.B * a.H * parts);
+    if (a.dk <= 64) {
+        if (four) delta_step_kernel<TIO, 1, 4><<<grid, 256, 0, s>>>(a, parts);
+        else delta_step_kernel<TIO, 1, 1><<<grid, 256, 0, s>>>(a, parts);
+    } else {
+        if (four) delta_step_kernel<TIO, 2, 4><<<grid, 256, 0, s>>>(a, parts);
+        else delta_step_kernel<TIO, 2, 1><<<grid, 256, 0, s>>>(a, parts);
+    }
+}
+
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t s)
 {
-    const int parts = (a.dv + 15) / 16;
-    const unsigned grid = (unsigned)(a.B * a.H * parts);
-    if (a.bf16) {
-        if (a.dk <= 64) delta_step_kernel<uint16_t, 1><<<grid, 256, 0, s>>>(a, parts);
-        else delta_step_kernel<uint16_t, 2><<<grid, 256, 0, s>>>(a, parts);
-    } else {
-        if (a.dk <= 64) delta_step_kernel<float, 1><<<grid, 256, 0, s>>>(a, parts);
-        else delta_step_kernel<float, 2><<<grid, 256, 0, s>>>(a, parts);
-    }
+    if (a.bf16) step_as<uint16_t>(a, s);
+    else step_as<float>(a, s);
     return hipGetLastError();
 }
 

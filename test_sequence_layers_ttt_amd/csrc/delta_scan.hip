@@ -407,7 +407,8 @@ __host__ __device__ __forceinline__ int widest(const DeltaPass& a, int DK)
 // all but the last and the transitions of all but the first and last.  With the backward pass:
 // kSave of both scans, or all three kinds of ends.
 template <typename TIO, int DK, int KEEP, int CW>
-__global__ void __launch_bounds__(256, 1) delta_scan_kernel(DeltaPass a)
+__global__ void __launch_bounds__(256, KEEP == kEnd && DK <= 64 && sizeof(TIO) == 2 ? 2 : 1)
+delta_scan_kernel(DeltaPass a)
 {
     typedef typename Forward<TIO, DK, KEEP, CW>::Tiles Tiles;
     __shared__ __align__(16) Tiles tiles[kBuffers<Tiles>];
@@ -448,43 +449,76 @@ __global__ void __launch_bounds__(256, 1) delta_scans_kernel(DeltaPass a, DeltaB
 
 // The segments' ends, one after the other: with X^T_s the state that segment s - 1 leaves (its end
 // from the true start) and A the transition as it was stored, X^T_(s+1) = A X^T_s + end_s; backward
-// by A^T.  One wave for 16 columns of a head.
+// by A^T.  One workgroup for 16 columns of a head: a wave has every fourth tile of features, the
+// columns go round by LDS, and the next transition is on its way while this one is multiplied.
 template <int DK>
-__global__ void __launch_bounds__(64) delta_join_kernel(DeltaPass a)
+__global__ void __launch_bounds__(256) delta_join_kernel(DeltaPass a)
 {
-    constexpr int M = DK / 16, J = DK / 32;
-    const int lane = threadIdx.x, c = lane & 15, g = lane >> 4, parts = a.dvp / 16;
+    constexpr int M = DK / 16, J = DK / 32, MW = (M + 3) / 4, LD = 17;
+    __shared__ float X[DK * LD];
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4, parts = a.dvp / 16;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), segments = a.cut.segments;
     const bool back = blockIdx.x >= (unsigned)(a.heads * parts);
     const int id = blockIdx.x % (a.heads * parts), local = id / parts, col = 16 * (id % parts) + c;
     const size_t plane = (size_t)DK * a.dvp;
-    float* ends = (back ? a.ends_back : a.ends) + (size_t)local * a.cut.segments * plane;
-    f32x4 X[M];
-    load_plane(ends + (back ? (a.cut.segments - 1) * plane : 0), a.dvp, col, g, X);
-    for (int k = 1; k < a.cut.segments - 1; ++k) {
-        const int s = back ? a.cut.segments - 1 - k : k;
-        const float* A = a.transitions + ((size_t)local * a.cut.segments + s) * DK * DK;
+    float* ends = (back ? a.ends_back : a.ends) + (size_t)local * segments * plane;
+    f32x4 A[MW][J][2], E[MW];
+    auto at = [&](int k) { return back ? segments - 1 - k : k; };
+    auto fetch = [&](int s) {
+        const float* T = a.transitions + ((size_t)local * segments + s) * DK * DK;
+#pragma unroll
+        for (int i = 0; i < MW; ++i) {
+            const int m = w + 4 * i;
+            if (m >= M) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[i][e] = ends[s * plane + (size_t)(16 * m + 4 * g + e) * a.dvp + col];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int f = 32 * j + 16 * h + 4 * g;
+                    if (back) {
+                        const float* p = T + (size_t)f * DK + 16 * m + c;
+                        A[i][j][h] = f32x4{p[0], p[DK], p[2 * DK], p[3 * DK]};
+                    } else {
+                        A[i][j][h] = *reinterpret_cast<const f32x4*>(T + (size_t)(16 * m + c) * DK + f);
+                    }
+                }
+        }
+    };
+    for (int e = tid; e < DK * 16; e += 256)
+        X[e / 16 * LD + e % 16] = ends[at(0) * plane + (size_t)(e / 16) * a.dvp + 16 * (id % parts) + e % 16];
+    fetch(at(1));
+    for (int k = 1; k < segments - 1; ++k) {
+        __syncthreads();
         Parts<3> x[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) x[j] = split<3>(X[2 * j], X[2 * j + 1]);
-        load_plane(ends + s * plane, a.dvp, col, g, X);
+        for (int j = 0; j < J; ++j) {
+            const float* p = X + (32 * j + 4 * g) * LD + c;
+            const f32x4 lo = {p[0], p[LD], p[2 * LD], p[3 * LD]};
+            p += 16 * LD;
+            x[j] = split<3>(lo, f32x4{p[0], p[LD], p[2 * LD], p[3 * LD]});
+        }
+        f32x4 y[MW];
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+        for (int i = 0; i < MW; ++i) {
+            y[i] = E[i];
+            if (w + 4 * i >= M) continue;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                f32x4 p, q;
-                if (back) {
-                    const float* at = A + (size_t)(32 * j + 4 * g) * DK + 16 * m + c;
-                    p = f32x4{at[0], at[DK], at[2 * DK], at[3 * DK]};
-                    at += 16 * DK;
-                    q = f32x4{at[0], at[DK], at[2 * DK], at[3 * DK]};
-                } else {
-                    const float* at = A + (size_t)(16 * m + c) * DK + 32 * j + 4 * g;
-                    p = *reinterpret_cast<const f32x4*>(at);
-                    q = *reinterpret_cast<const f32x4*>(at + 16);
-                }
-                X[m] = mma(split<3>(p, q), x[j], X[m]);
+            for (int j = 0; j < J; ++j) y[i] = mma(split<3>(A[i][j][0], A[i][j][1]), x[j], y[i]);
+        }
+        if (k + 1 < segments - 1) fetch(at(k + 1));
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MW; ++i) {
+            const int m = w + 4 * i;
+            if (m >= M) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                X[(16 * m + 4 * g + e) * LD + c] = y[i][e];
+                ends[at(k) * plane + (size_t)(16 * m + 4 * g + e) * a.dvp + col] = y[i][e];
             }
-        store_plane(ends + s * plane, a.dvp, col, g, X);
+        }
     }
 }
 
@@ -512,7 +546,7 @@ hipError_t scans_as(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
         hipError_t e = launch<TIO, DK, kEnd, CW>(p, o, s);
         if (e != hipSuccess) return e;
         const unsigned grid = (unsigned)(p.heads * (p.dvp / 16)) * (o ? 2 : 1);
-        delta_join_kernel<DK><<<grid, 64, 0, s>>>(p);
+        delta_join_kernel<DK><<<grid, 256, 0, s>>>(p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

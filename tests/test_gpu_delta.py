@@ -167,7 +167,7 @@ def test_forward_in_place_state_and_same_bits(dev):
 @pytest.mark.parametrize("layout", [ttt.LAYOUT_BHTD, ttt.LAYOUT_BTHD])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(2, 3, 1, 64, 64), (1, 4, 2, 128, 128), (1, 2, 1, 50, 83), (2, 1, 1, 3, 256),
-                                   (1, 2, 1, 100, 5)])
+                                   (1, 2, 1, 100, 5), (100, 8, 4, 64, 83), (60, 10, 1, 18, 130), (40, 8, 2, 128, 256)])
 def test_step_continues(dev, shape, io, layout):
     B, H, share, dk, dv = shape
     T = 7
