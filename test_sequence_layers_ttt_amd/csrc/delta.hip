@@ -113,12 +113,20 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
             }
         }
     }
-    constexpr int NZ = BACKWARD ? 3 : kZParts<TIO>;
-    quad* fp = a.P + unit * NZ * kFragQuads;
+    // (backward with wide workgroups: three parts of each operand)
+    const bool parts = BACKWARD && !a.cut.narrow;
+    const size_t each = parts ? 3 * kFragQuads : kHalfQuads;
+    f32x4* fp = a.P + unit * each;
+    if (parts) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (!BACKWARD && j <= w / 2) store_frag<NZ>(fp, frag_lower(w, j), lane, p[2 * j], p[2 * j + 1]);
-        if (BACKWARD && j >= w / 2) store_frag<NZ>(fp, frag_upper(w, j), lane, p[2 * j], p[2 * j + 1]);
+        for (int j = 0; j < 2; ++j)
+            if (j >= w / 2) store_frag<3>((quad*)fp, frag_upper(w, j), lane, p[2 * j], p[2 * j + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!BACKWARD && i <= w) fp[64 * half_lower(w, i) + lane] = p[i];
+            if (BACKWARD && i >= w) fp[64 * half_upper(w, i) + lane] = p[i];
+        }
     }
     __syncthreads();
 
@@ -170,19 +178,30 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
             put_cl<LD>(Sm + 16 * i * LD, 16 * w, lane, S[i]);
         }
         if constexpr (BACKWARD) {
-            quad* ft = a.St + unit * 3 * kFragQuads;
+            f32x4* ft = a.St + unit * each;
+            if (parts) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j >= w / 2) store_frag<3>(ft, frag_upper(w, j), lane, S[2 * j], S[2 * j + 1]);
+                for (int j = 0; j < 2; ++j)
+                    if (j >= w / 2) store_frag<3>((quad*)ft, frag_upper(w, j), lane, S[2 * j], S[2 * j + 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i >= w) ft[64 * half_upper(w, i) + lane] = S[i];
+            }
         }
     }
     __syncthreads();
-    quad* fs = a.S + unit * 3 * kFragQuads;
+    f32x4* fs = a.S + unit * each;
+    auto row = [&](int i) { return rl<LD>(Sm + 16 * w * LD, 16 * i, lane); };
+    if (parts) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (j <= w / 2)
-            store_frag<3>(fs, frag_lower(w, j), lane, rl<LD>(Sm + 16 * w * LD, 32 * j, lane),
-                          rl<LD>(Sm + 16 * w * LD, 32 * j + 16, lane));
+        for (int j = 0; j < 2; ++j)
+            if (j <= w / 2) store_frag<3>((quad*)fs, frag_lower(w, j), lane, row(2 * j), row(2 * j + 1));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i <= w) fs[64 * half_lower(w, i) + lane] = row(i);
+    }
 }
 
 // ---- token after token ---------------------------------------------------------------
@@ -275,20 +294,20 @@ struct Plan {
     size_t S, P, ends, transitions, bytes;   // places in the workspace, which begins with the records
 };
 
-Plan fwd_plan(int B, int H, int Hk, int T, int dk, int dv, bool bf16)
+Plan fwd_plan(int B, int H, int Hk, int T, int dk, int dv)
 {
     Plan p;
     p.chunks = (T + kChunk - 1) / kChunk;
     p.dvp = (dv + 31) / 32 * 32;
-    const size_t share = H / Hk, unit = p.chunks * share, part = kFragQuads * sizeof(quad);
-    const size_t s = 3 * part, z = (bf16 ? 2 : 3) * part, one = unit * (sizeof(Record) + s + z);
+    const size_t share = H / Hk, unit = p.chunks * share, half = kHalfQuads * sizeof(f32x4);
+    const size_t one = unit * (sizeof(Record) + 2 * half);
     p.groups = (int)std::min<size_t>((size_t)B * Hk, std::max<size_t>(1, kPassBytes / one));
     const size_t heads = p.groups * share, units = unit * p.groups, DK = delta_padded_dk(dk);
     p.cut = delta_cut((int)heads, p.chunks, dv, dk, false);
     const size_t cut = p.cut.segments > 1 ? heads * p.cut.segments * DK * 4 : 0;
     p.S = up256(units * sizeof(Record));
-    p.P = p.S + up256(units * s);
-    p.ends = p.P + up256(units * z);
+    p.P = p.S + up256(units * half);
+    p.ends = p.P + up256(units * half);
     p.transitions = p.ends + up256(cut * p.dvp);
     p.bytes = p.transitions + up256(cut * DK);
     return p;
@@ -308,14 +327,14 @@ hipError_t launch_delta_prepare(const DeltaPass& p, bool backward, hipStream_t s
                     : prepare_as<float, 128>(p, backward, s);
 }
 
-size_t delta_fwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool bf16)
+size_t delta_fwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool)
 {
-    return fwd_plan(B, H, Hk, T, dk, dv, bf16).bytes;
+    return fwd_plan(B, H, Hk, T, dk, dv).bytes;
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
 {
-    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T, a.dk, a.dv, a.bf16);
+    const Plan plan = fwd_plan(a.B, a.H, a.Hk, a.T, a.dk, a.dv);
     char* ws = (char*)a.workspace;
     DeltaPass p = {};
     p.f = a;
@@ -323,8 +342,8 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s)
     p.dvp = plan.dvp;
     p.cut = plan.cut;
     p.records = (Record*)ws;
-    p.S = (quad*)(ws + plan.S);
-    p.P = (quad*)(ws + plan.P);
+    p.S = (f32x4*)(ws + plan.S);
+    p.P = (f32x4*)(ws + plan.P);
     p.ends = (float*)(ws + plan.ends);
     p.transitions = (float*)(ws + plan.transitions);
     const int share = a.H / a.Hk, all = a.B * a.Hk;

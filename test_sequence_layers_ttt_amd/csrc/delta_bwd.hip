@@ -351,9 +351,9 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t s)
     p.ends_back = (float*)(ws + plan.ends_back);
     p.transitions = (float*)(ws + plan.transitions);
     p.records = (Record*)ws;
-    p.S = (quad*)(ws + plan.S);
-    p.St = (quad*)(ws + plan.St);
-    p.P = (quad*)(ws + plan.P);
+    p.S = (f32x4*)(ws + plan.S);
+    p.St = (f32x4*)(ws + plan.St);
+    p.P = (f32x4*)(ws + plan.P);
     p.states = (float*)(ws + plan.states);
     p.cotangents = (float*)(ws + plan.cotangents);
     p.U = (float*)(ws + plan.U);

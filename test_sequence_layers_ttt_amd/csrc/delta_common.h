@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "delta_launch.h"
 #include "device_common.h"
 #include "mfma_common.h"
@@ -202,11 +204,20 @@ __device__ __forceinline__ f32x4 token4(const Tile<TIO, DK>& t, int token, int f
 }
 
 // ---- what the preparing kernel leaves for a (head, chunk) -------------------
-// the 6 operands of a lower triangular 64 x 64 matrix that are not zero: row tile i
-// against the token pair of tiles (2 j, 2 j + 1), j <= i / 2; of its transpose, j >= i / 2
+// A lower triangular 64 x 64 matrix as the row operands of products: 6 operands that are not
+// zero, row tile i against the token pair of tiles (2 j, 2 j + 1), j <= i / 2; of its transpose
+// j >= i / 2.
 constexpr int kFrags = 6;
 __host__ __device__ constexpr int frag_lower(int i, int j) { return i < 2 ? i : 2 * (i - 1) + j; }
 __host__ __device__ constexpr int frag_upper(int i, int j) { return i < 2 ? 2 * i + j : i + 2; }
+
+// In memory it is the 10 tiles that are not zero, fp32, 16 bytes for each lane as the operand
+// takes them (row c, columns 4 g ..); on the way into LDS each is split into parts and becomes
+// half of an operand.  The two halves beyond the diagonal are zero from the start.  Where the
+// waves that load also compute, it is the operands' three parts instead.
+constexpr int kHalves = 10, kHalfQuads = kHalves * 64;
+__host__ __device__ constexpr int half_lower(int i, int j) { return i * (i + 1) / 2 + j; }
+__host__ __device__ constexpr int half_upper(int i, int j) { return 4 * i - i * (i - 1) / 2 + j - i; }
 
 // An operand is its parts, one after the other, 16 bytes for each lane (1 KB a part).
 constexpr int kFragQuads = kFrags * 64;       // of one part of a matrix's operands
@@ -267,9 +278,57 @@ struct LinearLoad {
     }
 };
 
-// A scan's workgroup of four waves: all compute, 16 columns of values each, and load as well
-// (CW = 4), or two compute and two load (CW = 2).
-template <int CW> constexpr int kLoaders = CW == 4 ? 256 : 128;
+// a triangular matrix on its way from memory into N parts in LDS
+template <int THREADS>
+struct HalvesLoad {
+    static constexpr int PER = (kHalfQuads + THREADS - 1) / THREADS;
+    f32x4 q[PER];
+    __device__ __forceinline__ void load(const f32x4* from, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (kHalfQuads % THREADS == 0 || tid + THREADS * i < kHalfQuads) q[i] = from[tid + THREADS * i];
+    }
+    template <int N, bool UPPER>
+    __device__ __forceinline__ void put(quad* to, int tid) const
+    {
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int h = w + THREADS / 64 * i;
+            if (kHalfQuads % THREADS != 0 && h >= kHalves) continue;
+            // the half's place among 12, of which two are zero
+            const int p = UPPER ? h + (h >= 4) + (h >= 9) : h + (h >= 1) + (h >= 6);
+            u32x2* at = reinterpret_cast<u32x2*>(to) + p / 2 * (N * 128) + (p & 1) + 2 * lane;
+            f32x4 x = q[i];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const u32x2 b = pack_bf16x4(x);
+                at[k * 128] = b;
+                if (k + 1 < N) x -= widen4(b);
+            }
+        }
+    }
+};
+
+// the two halves that no load writes
+template <int N, bool UPPER>
+__device__ __forceinline__ void zero_halves(quad* to, int tid, int threads)
+{
+    for (int e = tid; e < 2 * N * 64; e += threads) {
+        const int p = e < N * 64 ? (UPPER ? 4 : 1) : (UPPER ? 10 : 7), k = e % (N * 64);
+        reinterpret_cast<u32x2*>(to)[(size_t)(p / 2 * N * 64 + k) * 2 + (p & 1)] = u32x2{0u, 0u};
+    }
+}
+
+// A scan's workgroup: CW waves that compute, 16 columns of values each, and as many that load;
+// four waves that do both where registers do not allow eight, and in the backward pass (BACK), whose
+// triangular operands then come in parts from memory (both scans at 8 x 12 x 2048 tokens of 64
+// features 145 us so, 188 us with waves apart; forward 277 and 257 us a run at 1 x 32 x 32768).
+template <typename TIO, int DK, int CW, bool BACK>
+constexpr bool kApart = CW == 2 || (!BACK && sizeof(TIO) == 2 && DK <= 64);
+template <typename TIO, int DK, int CW, bool BACK>
+constexpr int kScanThreads = 64 * CW * (kApart<TIO, DK, CW, BACK> ? 2 : 1);
 
 // What it needs of a chunk: keys, queries, its columns of V or dZ, operands of S (3 parts) and
 // P (NP of them), eta, start and end of the tokens.
@@ -283,15 +342,14 @@ struct ChunkTiles {
 };
 
 // the same on its way, in the loading waves' registers
-template <typename TIO, int DK, int NP, bool Q, int CW>
+template <typename TIO, int DK, int NP, bool Q, bool UPPER, int CW, bool PARTS>
 struct ChunkLoad {
-    TileLoad<TIO, DK, kLoaders<CW>> k, q;
-    TileLoad<TIO, 16 * CW, kLoaders<CW>> v;
-    LinearLoad<3 * kFragQuads, kLoaders<CW>> s;
-    LinearLoad<NP ? NP * kFragQuads : 1, kLoaders<CW>> p;
-    LinearLoad<3 * kChunk / 4, kLoaders<CW>> rec;
+    TileLoad<TIO, DK, 64 * CW> k, q;
+    TileLoad<TIO, 16 * CW, 64 * CW> v;
+    typename std::conditional<PARTS, LinearLoad<3 * kFragQuads, 64 * CW>, HalvesLoad<64 * CW>>::type s, p;
+    LinearLoad<3 * kChunk / 4, 64 * CW> rec;
     __device__ __forceinline__ void load(const Rows<const TIO>& K, const Rows<const TIO>& Qr,
-                                         const Rows<const TIO>& V, const quad* S, const quad* P,
+                                         const Rows<const TIO>& V, const f32x4* S, const f32x4* P,
                                          const Record* r, int t0, int T, int dk, int dv, int first,
                                          bool whole_k, bool whole_v, int tid)
     {
@@ -304,8 +362,13 @@ struct ChunkLoad {
             if constexpr (Q) q.load(Qr, t0, T, dk, whole_k, tid);
             v.load(V, t0, T, dv, whole_v, tid, first);
         }
-        s.load(S, tid);
-        if constexpr (NP > 0) p.load(P, tid);
+        if constexpr (PARTS) {
+            s.load(reinterpret_cast<const quad*>(S), tid);
+            if constexpr (NP > 0) p.load(reinterpret_cast<const quad*>(P), tid);
+        } else {
+            s.load(S, tid);
+            if constexpr (NP > 0) p.load(P, tid);
+        }
         rec.load(reinterpret_cast<const quad*>(r->eta), tid);   // (eta, start and end: one after the other)
     }
     __device__ __forceinline__ void put(ChunkTiles<TIO, DK, NP, Q, CW>& to, int tid) const
@@ -313,8 +376,13 @@ struct ChunkLoad {
         k.put(to.k, tid);
         if constexpr (Q) q.put(to.q, tid);
         v.put(to.v, tid);
-        s.put(to.s, tid);
-        if constexpr (NP > 0) p.put(to.p, tid);
+        if constexpr (PARTS) {
+            s.put(to.s, tid);
+            if constexpr (NP > 0) p.put(to.p, tid);
+        } else {
+            s.template put<3, UPPER>(to.s, tid);
+            if constexpr (NP > 0) p.template put<NP, UPPER>(to.p, tid);
+        }
         rec.put(reinterpret_cast<quad*>(to.eta), tid);
     }
 };

@@ -41,6 +41,7 @@ size_t delta_bwd_workspace(int B, int H, int Hk, int T, int dk, int dv, bool bf1
 // ---- what the kernels of one pass over some of the heads are given --------------
 struct Record;
 typedef uint32_t quad __attribute__((ext_vector_type(4)));
+typedef float float4x __attribute__((ext_vector_type(4)));
 
 // segments of a sequence, chunks of each, 32 columns a workgroup (or 64)
 struct DeltaCut {
@@ -54,7 +55,8 @@ struct DeltaPass {
     int chunks;              // of 64 tokens
     int dvp;                 // dv up to a multiple of 32
     Record* records;         // [heads][chunks]
-    quad *S, *St, *P;        // operands of S, of its transpose (backward), of P (or its transpose)
+    // S, its transpose (backward) and P (or its transpose): tiles, or operands in parts
+    float4x *S, *St, *P;
     float *states, *cotangents;   // [heads][chunks][DK][dvp]: W^T before a chunk, D^T after it
     float *U, *F;            // [heads][chunks][64][dvp]
     DeltaCut cut;

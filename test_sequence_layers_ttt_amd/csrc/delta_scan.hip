@@ -48,11 +48,13 @@ struct Share {
 };
 
 // Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
-template <typename TIO, int DK, int KEEP, int CW>
+template <typename TIO, int DK, int KEEP, int CW, bool BACK>
 struct Forward {
     static constexpr int NZ = KEEP == kRead ? kZParts<TIO> : 0;
     typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
+    static constexpr bool APART = kApart<TIO, DK, CW, BACK>, PARTS = BACK && CW == 4;
+    static constexpr size_t LOWER = PARTS ? 3 * kFragQuads : kHalfQuads;   // of 16 bytes, a chunk's S
 
     // `unit`: V = 0 and a unit matrix for the start, columns are features
     static __device__ __forceinline__ void run(const DeltaPass& a, Tiles* tiles, Share s, bool unit)
@@ -75,28 +77,33 @@ struct Forward {
         const int begin = s.segment * a.cut.chunks;
         const int stop = begin + a.cut.chunks < a.chunks ? begin + a.cut.chunks : a.chunks;
 
-        const int id = CW == 4 ? tid : tid - 128;
-        ChunkLoad<TIO, DK, NZ, KEEP == kRead, CW> next;
-        auto fetch = [&](int n) {
+        for (int e = 0; !PARTS && e < NB; ++e) {
+            zero_halves<3, false>(tiles[e].s, tid, kScanThreads<TIO, DK, CW, BACK>);
+            if constexpr (NZ > 0) zero_halves<NZ, false>(tiles[e].p, tid, kScanThreads<TIO, DK, CW, BACK>);
+        }
+        const int id = APART ? tid - 64 * CW : tid;
+        typedef ChunkLoad<TIO, DK, NZ, KEEP == kRead, false, CW, PARTS> Load;
+        auto fetch = [&](Load& l, int n) {
             const size_t at = unit0 + n;
-            next.load(K, Q, V, a.S + at * 3 * kFragQuads, a.P + at * NZ * kFragQuads, a.records + at,
-                      n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
+            l.load(K, Q, V, a.S + at * LOWER, a.P + at * kHalfQuads, a.records + at,
+                   n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
         };
-        auto put = [&](int n) { next.put(tiles[NB == 2 ? (n - begin) & 1 : 0], id); };
-        if (CW == 2 && w >= 2) {
-            fetch(begin);
-            put(begin);
-            if (begin + 1 < stop) fetch(begin + 1);
+        auto put = [&](const Load& l, int n) { l.put(tiles[NB == 2 ? (n - begin) & 1 : 0], id); };
+        Load next;
+        if (APART && w >= CW) {
+            fetch(next, begin);
+            put(next, begin);
+            if (begin + 1 < stop) fetch(next, begin + 1);
             __syncthreads();
             for (int n = begin; n < stop; ++n) {
                 if constexpr (NB == 1) __syncthreads();
-                if (n + 1 < stop) put(n + 1);
-                if (n + 2 < stop) fetch(n + 2);
+                if (n + 1 < stop) put(next, n + 1);
+                if (n + 2 < stop) fetch(next, n + 2);
                 __syncthreads();
             }
             return;
         }
-        if constexpr (CW == 4) fetch(begin);
+        if constexpr (!APART) fetch(next, begin);
         f32x4 W[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) W[m] = zero;
@@ -112,12 +119,12 @@ struct Forward {
         } else if (KEEP != kEnd && works) {
             load_plane(a.ends + ((size_t)local * a.cut.segments + s.segment - 1) * DK * a.dvp, a.dvp, col, g, W);
         }
-        if constexpr (CW == 4) put(begin);
+        if constexpr (!APART) put(next, begin);
         __syncthreads();
 
         for (int n = begin; n < stop; ++n) {
             const Tiles& t = tiles[NB == 2 ? (n - begin) & 1 : 0];
-            if (CW == 4 && n + 1 < stop) fetch(n + 1);
+            if (!APART && n + 1 < stop) fetch(next, n + 1);
             if (works) {
                 typedef Parts<kParts<TIO>> In;
                 In kt[J][4], vp[2];
@@ -129,9 +136,7 @@ struct Forward {
                     for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
                     start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
-                    ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -152,6 +157,8 @@ struct Forward {
                     for (int i = 0; i < 4; ++i) r[i] = mma(kt[j][i], wp[j], r[i]);
                 }
                 if constexpr (KEEP == kSave) store_plane(a.states + (unit0 + n) * DK * a.dvp, a.dvp, col, g, W);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
                 In kf[M][2];
 #pragma unroll
                 for (int m = 0; m < M; ++m)
@@ -170,6 +177,8 @@ struct Forward {
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 2 * j; i < 4; ++i) r[i] = mma(S[frag_lower(i, j)], x[j], r[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
                 In qt[J][4];
                 Parts<NZ ? NZ : 1> P[kFrags], u[2];
                 if constexpr (KEEP == kRead) {
@@ -220,7 +229,7 @@ struct Forward {
                 }
             }
             if constexpr (NB == 1) __syncthreads();
-            if (CW == 4 && n + 1 < stop) put(n + 1);
+            if (!APART && n + 1 < stop) put(next, n + 1);
             __syncthreads();
         }
         if constexpr (KEEP == kEnd) {
@@ -241,6 +250,8 @@ template <typename TIO, int DK, int KEEP, int CW>
 struct Reverse {
     typedef ChunkTiles<TIO, DK, 3, true, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
+    static constexpr bool APART = kApart<TIO, DK, CW, true>, PARTS = CW == 4;
+    static constexpr size_t UPPER = PARTS ? 3 * kFragQuads : kHalfQuads;
 
     static __device__ __forceinline__ void run(const DeltaPass& a, const DeltaBwdArgs& o, Tiles* tiles, Share s)
     {
@@ -261,28 +272,33 @@ struct Reverse {
         const int begin = s.segment * a.cut.chunks;
         const int last = (begin + a.cut.chunks < a.chunks ? begin + a.cut.chunks : a.chunks) - 1;
 
-        const int id = CW == 4 ? tid : tid - 128;
-        ChunkLoad<TIO, DK, 3, true, CW> next;
-        auto fetch = [&](int n) {
+        for (int e = 0; !PARTS && e < NB; ++e) {
+            zero_halves<3, true>(tiles[e].s, tid, kScanThreads<TIO, DK, CW, true>);
+            zero_halves<3, true>(tiles[e].p, tid, kScanThreads<TIO, DK, CW, true>);
+        }
+        const int id = APART ? tid - 64 * CW : tid;
+        typedef ChunkLoad<TIO, DK, 3, true, true, CW, PARTS> Load;
+        auto fetch = [&](Load& l, int n) {
             const size_t at = unit0 + n;
-            next.load(K, Q, dZ, a.St + at * 3 * kFragQuads, a.P + at * 3 * kFragQuads, a.records + at,
-                      n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
+            l.load(K, Q, dZ, a.St + at * UPPER, a.P + at * UPPER, a.records + at,
+                   n * kChunk, T, dk, dv, first, whole_k, whole_v, id);
         };
-        auto put = [&](int n) { next.put(tiles[NB == 2 ? n & 1 : 0], id); };
-        if (CW == 2 && w >= 2) {
-            fetch(last);
-            put(last);
-            if (last > begin) fetch(last - 1);
+        auto put = [&](const Load& l, int n) { l.put(tiles[NB == 2 ? n & 1 : 0], id); };
+        Load next;
+        if (APART && w >= CW) {
+            fetch(next, last);
+            put(next, last);
+            if (last > begin) fetch(next, last - 1);
             __syncthreads();
             for (int n = last; n >= begin; --n) {
                 if constexpr (NB == 1) __syncthreads();
-                if (n > begin) put(n - 1);
-                if (n > begin + 1) fetch(n - 2);
+                if (n > begin) put(next, n - 1);
+                if (n > begin + 1) fetch(next, n - 2);
                 __syncthreads();
             }
             return;
         }
-        if constexpr (CW == 4) fetch(last);
+        if constexpr (!APART) fetch(next, last);
         f32x4 D[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) D[m] = zero;
@@ -293,54 +309,53 @@ struct Reverse {
         } else if (KEEP != kEnd && works) {
             load_plane(a.ends_back + ((size_t)local * a.cut.segments + s.segment + 1) * DK * a.dvp, a.dvp, col, g, D);
         }
-        if constexpr (CW == 4) put(last);
+        if constexpr (!APART) put(next, last);
         __syncthreads();
 
         for (int n = last; n >= begin; --n) {
             const Tiles& t = tiles[NB == 2 ? n & 1 : 0];
-            if (CW == 4 && n > begin) fetch(n - 1);
+            if (!APART && n > begin) fetch(next, n - 1);
             if (works) {
                 const size_t unit = unit0 + n;
                 typedef Parts<NP> In;
                 In kt[J][4], zp[2];
-                Parts<3> P[kFrags], x[2], y[2];
-                f32x4 f[4], z[4], eta[4], start[4], ends[4];
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
-                    start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
-                    ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
-                }
+                Parts<3> P[kFrags], S[kFrags], x[2];
+                f32x4 f[4], kd[4], z[4], eta[4], start[4], ends[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) zp[j] = by_feature(t.v, w, j, lane);
 #pragma unroll
                 for (int e = 0; e < kFrags; ++e) P[e] = load_frag<3>(t.p, e, lane);
                 const float all = t.start[kChunk - 1];
                 reads_before();
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kt[j][i] = by_token(t.k, i, j, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ends[i] = *reinterpret_cast<const f32x4*>(t.end + 16 * i + 4 * g);
+                    eta[i] = *reinterpret_cast<const f32x4*>(t.eta + 16 * i + 4 * g);
+                }
+                reads_before();
 
                 if constexpr (KEEP == kSave) store_plane(a.cotangents + unit * DK * a.dvp, a.dvp, col, g, D);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = zero;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = mma(kt[j][i], dp, f[i]);
-                }
-                Parts<3> S[kFrags];
-#pragma unroll
-                for (int e = 0; e < kFrags; ++e) S[e] = load_frag<3>(t.s, e, lane);
-                reads_before();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] *= ends[i];
+                for (int i = 0; i < 4; ++i) f[i] = kd[i] = zero;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(P[frag_upper(i, j)], zp[j], f[i]);
+#pragma unroll
+                for (int e = 0; e < kFrags; ++e) S[e] = load_frag<3>(t.s, e, lane);
+                reads_before();
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const Parts<3> dp = split<3>(D[2 * j], D[2 * j + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kd[i] = mma(kt[j][i], dp, kd[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] += ends[i] * kd[i];
                 In kf[M][2];
 #pragma unroll
                 for (int m = 0; m < M; ++m)
@@ -354,6 +369,8 @@ struct Reverse {
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 0; i < 2 * j + 2; ++i) f[i] = mma(S[frag_upper(i, j)], x[j], f[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) start[i] = *reinterpret_cast<const f32x4*>(t.start + 16 * i + 4 * g);
                 In qf[M][2];
 #pragma unroll
                 for (int m = 0; m < M; ++m)
@@ -363,27 +380,26 @@ struct Reverse {
 
                 if constexpr (KEEP == kSave) store_plane(a.F + unit * kChunk * a.dvp, a.dvp, col, g, f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i] *= -(start[i] * eta[i]);
-                    z[i] = start[i] * widen_parts(zp[i / 2], i & 1);
-                }
+                for (int i = 0; i < 4; ++i) f[i] *= -(start[i] * eta[i]);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    x[j] = split<3>(f[2 * j], f[2 * j + 1]);
-                    y[j] = split<3>(z[2 * j], z[2 * j + 1]);
-                }
+                for (int j = 0; j < 2; ++j) x[j] = split<3>(f[2 * j], f[2 * j + 1]);
 #pragma unroll
                 for (int m = 0; m < M; ++m) D[m] *= all;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        D[m] = mma(kf[m][j], x[j], D[m]);
-                        D[m] = mma(qf[m][j], y[j], D[m]);
-                    }
+                    for (int m = 0; m < M; ++m) D[m] = mma(kf[m][j], x[j], D[m]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = start[i] * widen_parts(zp[i / 2], i & 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) x[j] = split<3>(z[2 * j], z[2 * j + 1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int m = 0; m < M; ++m) D[m] = mma(qf[m][j], x[j], D[m]);
             }
             if constexpr (NB == 1) __syncthreads();
-            if (CW == 4 && n > begin) put(n - 1);
+            if (!APART && n > begin) put(next, n - 1);
             __syncthreads();
         }
         if constexpr (KEEP == kEnd) {
@@ -407,10 +423,10 @@ __host__ __device__ __forceinline__ int widest(const DeltaPass& a, int DK)
 // all but the last and the transitions of all but the first and last.  With the backward pass:
 // kSave of both scans, or all three kinds of ends.
 template <typename TIO, int DK, int KEEP, int CW>
-__global__ void __launch_bounds__(256, KEEP == kEnd && DK <= 64 && sizeof(TIO) == 2 ? 2 : 1)
+__global__ void __launch_bounds__((kScanThreads<TIO, DK, CW, false>), KEEP == kEnd && CW == 2 && DK <= 64 && sizeof(TIO) == 2 ? 2 : 1)
 delta_scan_kernel(DeltaPass a)
 {
-    typedef typename Forward<TIO, DK, KEEP, CW>::Tiles Tiles;
+    typedef typename Forward<TIO, DK, KEEP, CW, false>::Tiles Tiles;
     __shared__ __align__(16) Tiles tiles[kBuffers<Tiles>];
     const int ends = KEEP == kEnd ? a.cut.segments - 1 : a.cut.segments;
     const int each = ends + (KEEP == kEnd ? a.cut.segments - 2 : 0);
@@ -420,13 +436,13 @@ delta_scan_kernel(DeltaPass a)
     const bool unit = k >= ends;
     const Share s = {local, unit ? 1 + k - ends : k, 16 * CW * part};
     if (local >= a.heads || s.first >= (unit ? DK : a.dvp)) return;
-    Forward<TIO, DK, KEEP, CW>::run(a, tiles, s, unit);
+    Forward<TIO, DK, KEEP, CW, false>::run(a, tiles, s, unit);
 }
 
 template <typename TIO, int DK, int KEEP, int CW>
-__global__ void __launch_bounds__(256, 1) delta_scans_kernel(DeltaPass a, DeltaBwdArgs o)
+__global__ void __launch_bounds__((kScanThreads<TIO, DK, CW, true>), 1) delta_scans_kernel(DeltaPass a, DeltaBwdArgs o)
 {
-    typedef typename Forward<TIO, DK, KEEP, CW>::Tiles There;
+    typedef typename Forward<TIO, DK, KEEP, CW, true>::Tiles There;
     typedef typename Reverse<TIO, DK, KEEP, CW>::Tiles Back;
     constexpr size_t room = kBuffers<There> * sizeof(There) > kBuffers<Back> * sizeof(Back)
                                 ? kBuffers<There> * sizeof(There) : kBuffers<Back> * sizeof(Back);
@@ -444,7 +460,7 @@ __global__ void __launch_bounds__(256, 1) delta_scans_kernel(DeltaPass a, DeltaB
         Reverse<TIO, DK, KEEP, CW>::run(a, o, (Back*)tiles, s);
         return;
     }
-    Forward<TIO, DK, KEEP, CW>::run(a, (There*)tiles, s, unit);
+    Forward<TIO, DK, KEEP, CW, true>::run(a, (There*)tiles, s, unit);
 }
 
 // The segments' ends, one after the other: with X^T_s the state that segment s - 1 leaves (its end
@@ -530,12 +546,12 @@ hipError_t launch(const DeltaPass& p, const DeltaBwdArgs* o, hipStream_t s)
     const unsigned grid = (unsigned)((p.heads * each + 7) / 8 * 8 * widest<CW>(p, DK));
     if constexpr (KEEP != kSave) {
         if (!o) {
-            delta_scan_kernel<TIO, DK, KEEP, CW><<<grid, 256, 0, s>>>(p);
+            delta_scan_kernel<TIO, DK, KEEP, CW><<<grid, kScanThreads<TIO, DK, CW, false>, 0, s>>>(p);
             return hipGetLastError();
         }
     }
     if constexpr (KEEP != kRead)
-        delta_scans_kernel<TIO, DK, KEEP, CW><<<grid, 256, 0, s>>>(p, *o);
+        delta_scans_kernel<TIO, DK, KEEP, CW><<<grid, kScanThreads<TIO, DK, CW, true>, 0, s>>>(p, *o);
     return hipGetLastError();
 }
 
