@@ -47,6 +47,12 @@ struct Share {
     int local, segment, first;
 };
 
+// where a segment's first state lies: the end of the one before it; W0's copy in the last place
+__device__ __forceinline__ float* start_of(const DeltaPass& a, int local, int segment, int DK)
+{
+    return a.ends + ((size_t)local * a.cut.segments + (segment ? segment - 1 : a.cut.segments - 1)) * DK * a.dvp;
+}
+
 // Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
 template <typename TIO, int DK, int KEEP, int CW, bool BACK>
 struct Forward {
@@ -112,12 +118,14 @@ struct Forward {
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) W[m][e] = 16 * m + 4 * g + e == col ? 1.f : 0.f;
-        } else if (s.segment == 0) {
+        } else if (s.segment == 0 && (KEEP == kEnd || a.cut.segments == 1)) {
             if (a.f.W0)
 #pragma unroll
                 for (int m = 0; m < M; ++m) W[m] = load_state(a.f.W0 + state, col, 16 * m + 4 * g, dv, dk);
+            // the second run takes the first state from here: the last segment may write W_out at its place
+            if (KEEP == kEnd && works) store_plane(start_of(a, local, 0, DK), a.dvp, col, g, W);
         } else if (KEEP != kEnd && works) {
-            load_plane(a.ends + ((size_t)local * a.cut.segments + s.segment - 1) * DK * a.dvp, a.dvp, col, g, W);
+            load_plane(start_of(a, local, s.segment, DK), a.dvp, col, g, W);
         }
         if constexpr (!APART) put(next, begin);
         __syncthreads();

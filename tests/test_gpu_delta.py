@@ -277,3 +277,45 @@ def test_outputs_end_where_they_should(dev):
     ttt.delta_bwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW,
                   **dict(zip(("dK", "dQ", "dV", "deta", "dg", "dW0"), views)))
     assert all((o[t.numel():] == 7).all() for o, t in zip(outs, views))
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 4000, 64, 64), (1, 32, 1, 8192, 64, 64), (1, 2, 1, 3000, 128, 128)])
+def test_forward_in_place_in_segments(dev, shape):
+    """W_out at W0's place where the sequence's segments run at once: the first reads its state from
+    elsewhere."""
+    c = Case(dev, *shape, "bf16", seed=31)
+    Z, W = ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, c.W0)
+    for _ in range(3):
+        W1 = c.W0.clone()
+        Z1, _ = ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, W1, W_out=W1)
+        assert (Z == Z1).all() and (W == W1).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(10, 16, 1, 130, 64, 64), (5, 32, 2, 70, 32, 64), (10, 16, 1, 140, 128, 60),
+                                   (3, 32, 4, 100, 50, 83)])
+def test_many_heads(dev, shape, io):
+    """Enough heads for workgroups of 64 columns."""
+    c = Case(dev, *shape, io, seed=sum(shape), forget=(66,))
+    check_fwd(c, *ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, c.W0))
+    check_bwd(c, ttt.delta_bwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 32, 1, 8192, 64, 64), (1, 32, 1, 8200, 32, 50), (1, 24, 1, 12000, 128, 64)])
+def test_segments_of_many_heads(dev, shape, io):
+    """Sequences in segments with workgroups of 64 columns: as a few heads at a time."""
+    B, H, share, T, dk, dv = shape
+    c = Case(dev, *shape, io, seed=sum(shape), forget=(1000, 5000))
+    whole = ttt.delta_fwd(c.K, c.Q, c.V, c.eta, c.g, c.W0) + ttt.delta_bwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW)
+    rel = 2 * ref.delta_rel(T, dk, dv)
+    # (dg's parts cancel: about ten times its largest value goes into the sum)
+    more = {0: ref.HALF[io] * 2 + (2 * ref.Z_BF16 if io == "bf16" else 0), 2: 2 * ref.HALF[io], 3: 2 * ref.HALF[io],
+            4: 2 * ref.HALF[io], 6: 9 * rel}
+    for h in range(0, H, 4):
+        s = slice(h, h + 4)
+        part = [t[:, s].contiguous() for t in (c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW)]
+        alone = ttt.delta_fwd(*part[:6]) + ttt.delta_bwd(*part)
+        for i, (a, b) in enumerate(zip(whole, alone)):
+            err = (a[:, s].double() - b.double()).abs().max().item()
+            assert err <= (rel + more.get(i, 0)) * b.double().abs().max().item(), (h, i, err)
