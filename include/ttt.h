@@ -620,8 +620,8 @@ int ttt_groupnorm_fwd(const void* X, const float* weight, const float* bias, flo
                       void* Y, float* mean, float* rstd, long long N, long long S, int C, int G,
                       int io_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace ttt_groupnorm_fwd needs (0 for shapes it refuses and where S = 1 and a
- * group is small). */
+/* Bytes of workspace ttt_groupnorm_fwd needs (0 for shapes it refuses and where a group is
+ * small enough to be read once). */
 size_t ttt_groupnorm_workspace_bytes(long long N, long long S, int C, int G, int io_dtype);
 
 /* Backward pass of ttt_groupnorm_fwd.  With n = (x - mean) rstd, v = n weight + bias and

@@ -4,12 +4,18 @@
 // and its gradients:  dv = dy act'(v),  u = dv weight,
 //   dx = rstd (u - mean(u) - n mean(u n)),  dweight = sum of dv n,  dbias = sum of dv.
 //
-// Two forms.  With one place (S = 1: the norm of every head's output of every token) a group
-// is at most 64 lanes' vectors: it stays in registers, every input is read once, and a
-// thread keeps the same channels for all its rows, so weight and bias (and the backward
-// pass's sums) stay in registers too.  Otherwise the places are shared out over the
-// workgroups, each thread with channels of its own: sums per channel first, then a wave per
-// group joins them, then a second read writes the result.
+// Three forms, by the size of a group.
+//   rows    one place (S = 1: the norm of every head's output of every token) and at most 64 vectors
+//           a group: it stays in registers, every input is read once, and a thread keeps the same
+//           channels for all its rows, so weight and bias (and the backward pass's sums) stay in
+//           registers too.  HBM bounds it: 16384 x 2048 bf16 in 32 groups with SiLU 32 us forward
+//           (134 MB), 49 us backward (201 MB) and 5 us for the sums.
+//   blocks  up to 4096 vectors a group: 16 to 512 threads hold it in registers, read once as well
+//           (16384 x 4096 bf16 in one group 52 us forward; as a slab 769 us); the sums for weight
+//           and bias take a second read, channel by channel.
+//   slabs   larger ones: the places are shared out over the workgroups, each thread with channels
+//           of its own: sums per channel first, then a workgroup per group joins them, then a
+//           second read writes the result (8 x 4096 x 640 bf16 15, 8 and 21 us).
 //
 // Sums run in a fixed order: the same bits on every call.
 #include <algorithm>
@@ -42,6 +48,32 @@ __device__ __forceinline__ void store_vec(TIO* p, const float (&y)[V])
         else if constexpr (V == 4) *reinterpret_cast<u32x2*>(p) = pack_bf16x4(f32x4{y[0], y[1], y[2], y[3]});
         else if constexpr (V == 2) *reinterpret_cast<unsigned*>(p) = pack_bf16x2(y[0], y[1]);
         else *p = (uint16_t)(pack_bf16x2(y[0], 0.f) & 0xffffu);
+    }
+}
+
+// V neighbouring floats (aligned as one is), or a value for all where there are none
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef f32x2 f32x2_any __attribute__((aligned(4)));
+template <int V>
+__device__ __forceinline__ void floats(const float* p, long long at, float none, float (&x)[V])
+{
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = none;
+        return;
+    }
+    p += at;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4_any*>(p + i);
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+    } else if constexpr (V == 2) {
+        const f32x2 v = *reinterpret_cast<const f32x2_any*>(p);
+        x[0] = v.x; x[1] = v.y;
+    } else {
+        x[0] = *p;
     }
 }
 
@@ -524,6 +556,188 @@ __global__ void __launch_bounds__(256) group_dx_kernel(GroupBwdArgs a, int parts
     }
 }
 
+// ---- a group in the registers of TS threads ------------------------------------------------
+constexpr int kHeld = 8;       // vectors of a thread
+
+// sum over the TS threads of a slab, in each
+template <int TS>
+__device__ __forceinline__ float held_sum(float x, float* room)
+{
+    x = lane_sum<(TS < 64 ? TS : 64)>(x);
+    if constexpr (TS > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < TS / 64; ++i) x += room[i];
+    }
+    return x;
+}
+
+// this thread's place: slab, and the offsets of its vectors in it (a workgroup has 256 / TS slabs)
+template <int V, int TS>
+struct Held {
+    long long slab, base, at[kHeld];
+    int lane, ch[kHeld], first;      // channels, and the group's first
+    bool in[kHeld], live;
+    __device__ __forceinline__ Held(long long N, long long S, int C, int G)
+    {
+        const int per = C / G, pv = per / V, count = (int)(S * pv);
+        lane = threadIdx.x % TS;
+        slab = (long long)blockIdx.x * (blockDim.x / TS) + threadIdx.x / TS;
+        live = slab < N * G;
+        first = (int)(slab % G) * per;
+        base = slab / G * S * C + first;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int e = lane + TS * k;
+            in[k] = live && e < count;
+            ch[k] = e % pv * V;
+            at[k] = base + (long long)(e / pv) * C + ch[k];
+        }
+    }
+};
+
+template <typename TIO, int V, int ACT, int TS>
+__global__ void __launch_bounds__(TS > 256 ? TS : 256) group_block_fwd_kernel(GroupArgs a)
+{
+    __shared__ float room[16];
+    const Held<V, TS> p(a.N, a.S, a.C, a.G);
+    const TIO* X = (const TIO*)a.X;
+    float v[kHeld][V], s = 0.f;
+    const float inv = 1.f / (float)(a.S * (a.C / a.G));
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        Vec<TIO, V> x;
+        if (p.in[k]) x.load(X + p.at[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += v[k][i] = p.in[k] ? x.at(i) : 0.f;
+    }
+    const float mean = held_sum<TS>(s, room) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        if (p.in[k])
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k][i] -= mean;
+                s = fmaf(v[k][i], v[k][i], s);
+            }
+    const float rstd = __builtin_amdgcn_rsqf(fmaf(held_sum<TS>(s, room), inv, a.eps));
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        if (!p.in[k]) continue;
+        float w[V], b[V];
+        floats<V>(a.weight, p.first + p.ch[k], 1.f, w);
+        floats<V>(a.bias, p.first + p.ch[k], 0.f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = act<ACT>(fmaf(v[k][i] * rstd, w[i], b[i]));
+        store_vec<TIO, V>((TIO*)a.Y + p.at[k], v[k]);
+    }
+    if (p.live && p.lane == 0) {
+        a.mean[p.slab] = mean;
+        a.rstd[p.slab] = rstd;
+    }
+}
+
+template <typename TIO, int V, int ACT, int TS>
+__global__ void __launch_bounds__(TS > 256 ? TS : 256) group_block_bwd_kernel(GroupBwdArgs a)
+{
+    __shared__ float room[16];
+    const Held<V, TS> p(a.N, a.S, a.C, a.G);
+    float n[kHeld][V], u[kHeld][V], s1 = 0.f, s2 = 0.f;
+    const float inv = 1.f / (float)(a.S * (a.C / a.G));
+    const float mean = p.live ? a.mean[p.slab] : 0.f, rstd = p.live ? a.rstd[p.slab] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        if (!p.in[k]) continue;
+        Vec<TIO, V> x, dy;
+        x.load((const TIO*)a.X + p.at[k]);
+        dy.load((const TIO*)a.dY + p.at[k]);
+        float w[V], b[V];
+        floats<V>(a.weight, p.first + p.ch[k], 1.f, w);
+        floats<V>(a.bias, p.first + p.ch[k], 0.f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            n[k][i] = (x.at(i) - mean) * rstd;
+            u[k][i] = dy.at(i) * dact<ACT>(fmaf(n[k][i], w[i], b[i])) * w[i];
+            s1 += u[k][i];
+            s2 = fmaf(u[k][i], n[k][i], s2);
+        }
+    }
+    s1 = held_sum<TS>(s1, room) * inv;
+    s2 = held_sum<TS>(s2, room) * inv;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        if (!p.in[k]) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[k][i] = rstd * (u[k][i] - fmaf(n[k][i], s2, s1));
+        store_vec<TIO, V>((TIO*)a.dX + p.at[k], u[k]);
+    }
+}
+
+// sums of dv n and dv over the N S rows of C channels, to planes [2][C] of each block y: run before
+// the gradient is written, which may stand at X's or dY's place
+template <typename TIO, int V, int ACT>
+__global__ void __launch_bounds__(256) group_columns_kernel(GroupBwdArgs a, float* planes)
+{
+    const int vectors = a.C / V, per = a.C / a.G;
+    const Slab p(vectors, V, a.N * a.S, (int)gridDim.y);
+    const bool one = per % V == 0;      // (a vector's channels are of one group)
+    const int group = p.ch / per;
+    float s[V], q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+    if (p.in) {
+        float w[V], b[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            w[i] = a.weight ? a.weight[p.ch + i] : 1.f;
+            b[i] = a.bias ? a.bias[p.ch + i] : 0.f;
+        }
+#pragma unroll 2
+        for (long long t = p.first + p.slot; t < p.last; t += p.slots) {
+            Vec<TIO, V> x, dy;
+            x.load((const TIO*)a.X + t * a.C + p.ch);
+            dy.load((const TIO*)a.dY + t * a.C + p.ch);
+            const long long row = a.S == 1 ? t : t / a.S;
+            float mean[V], rstd[V];
+            if (one) {
+                const float m = a.mean[row * a.G + group], r = a.rstd[row * a.G + group];
+#pragma unroll
+                for (int i = 0; i < V; ++i) { mean[i] = m; rstd[i] = r; }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const long long g = row * a.G + (p.ch + i) / per;
+                    mean[i] = a.mean[g];
+                    rstd[i] = a.rstd[g];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float n = (x.at(i) - mean[i]) * rstd[i];
+                const float dv = dy.at(i) * dact<ACT>(fmaf(n, w[i], b[i]));
+                s[i] = fmaf(dv, n, s[i]);
+                q[i] += dv;
+            }
+        }
+    }
+    over_slots<V>(p, vectors, s, q, [&](int i, int, float sb, float qb) {
+        s[i] += sb;
+        q[i] += qb;
+    });
+    if (p.slot == 0 && p.in) {
+        float* to = planes + (size_t)blockIdx.y * 2 * a.C + p.ch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            to[i] = s[i];
+            to[a.C + i] = q[i];
+        }
+    }
+}
+
 // ---- launch shapes -----------------------------------------------------------------------
 constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -537,6 +751,8 @@ int vector_of(int n, bool bf16)
 
 struct Shape {
     bool rows;               // the form for one place
+    int held;                // threads that hold a group (0: they do not)
+    int wide;                // vector of a row of all channels
     int V, L, x, y, slots;   // vector, lanes of a group, grid, rows a workgroup holds at once
     int parts;               // workgroups along the places
     size_t planes;           // of 2 C floats
@@ -561,8 +777,19 @@ Shape shape_of(long long N, long long S, int C, int G, bool bf16)
         h.planes = (size_t)h.y * h.slots;
         return h;
     }
-    h.V = vector_of(C, bf16);
-    const int vectors = C / h.V;
+    h.wide = vector_of(C, bf16);
+    const int vectors = C / h.wide;
+    const long long count = per / v <= 4096 / S ? S * (per / v) : 4097;
+    if (count <= 512 * kHeld) {
+        h.V = v;
+        h.held = count <= 64 ? 16 : count <= 64 * kHeld ? 64 : count <= 256 * kHeld ? 256 : 512;
+        h.slots = vectors < 256 ? 256 / vectors : 1;
+        h.x = (vectors + 255) / 256;
+        h.y = (int)std::min<long long>((N * S + h.slots - 1) / h.slots, std::max(1, 1024 / h.x));
+        h.planes = (size_t)h.y;
+        return h;
+    }
+    h.V = h.wide;
     h.slots = vectors < 256 ? 256 / vectors : 1;
     h.x = (vectors + 255) / 256;
     const long long most = std::max<long long>(1, S / (16ll * h.slots));
@@ -606,11 +833,48 @@ void lanes_as(int L, DO d)
     }
 }
 
+template <typename TIO, int V, int ACT>
+void block_fwd(const GroupArgs& a, const Shape& h, hipStream_t s)
+{
+    const long long slabs = a.N * a.G;
+    if (h.held == 16)
+        group_block_fwd_kernel<TIO, V, ACT, 16><<<(unsigned)((slabs + 15) / 16), 256, 0, s>>>(a);
+    else if (h.held == 64) group_block_fwd_kernel<TIO, V, ACT, 64><<<(unsigned)((slabs + 3) / 4), 256, 0, s>>>(a);
+    else if (h.held == 256) group_block_fwd_kernel<TIO, V, ACT, 256><<<(unsigned)slabs, 256, 0, s>>>(a);
+    else group_block_fwd_kernel<TIO, V, ACT, 512><<<(unsigned)slabs, 512, 0, s>>>(a);
+}
+
+template <typename TIO, int V, int ACT>
+void block_bwd(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
+{
+    const long long slabs = a.N * a.G;
+    if (h.held == 16)
+        group_block_bwd_kernel<TIO, V, ACT, 16><<<(unsigned)((slabs + 15) / 16), 256, 0, s>>>(a);
+    else if (h.held == 64) group_block_bwd_kernel<TIO, V, ACT, 64><<<(unsigned)((slabs + 3) / 4), 256, 0, s>>>(a);
+    else if (h.held == 256) group_block_bwd_kernel<TIO, V, ACT, 256><<<(unsigned)slabs, 256, 0, s>>>(a);
+    else group_block_bwd_kernel<TIO, V, ACT, 512><<<(unsigned)slabs, 512, 0, s>>>(a);
+}
+
+template <typename TIO, int V>
+void columns(const GroupBwdArgs& a, const Shape& h, float* planes, hipStream_t s)
+{
+    const dim3 grid(h.x, h.y);
+    if (a.act == TTT_ACT_SILU) group_columns_kernel<TIO, V, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, planes);
+    else if (a.act == TTT_ACT_GELU) group_columns_kernel<TIO, V, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, planes);
+    else group_columns_kernel<TIO, V, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, planes);
+}
+
 template <typename TIO, int V>
 hipError_t fwd_as(const GroupArgs& a, const Shape& h, hipStream_t s)
 {
     if (h.rows) {
         lanes_as<TIO, V>(h.L, [&](auto L) { row_fwd<TIO, V, decltype(L)::value>(a, h, s); });
+        return hipGetLastError();
+    }
+    if (h.held) {
+        if (a.act == TTT_ACT_SILU) block_fwd<TIO, V, TTT_ACT_SILU>(a, h, s);
+        else if (a.act == TTT_ACT_GELU) block_fwd<TIO, V, TTT_ACT_GELU>(a, h, s);
+        else block_fwd<TIO, V, TTT_ACT_NONE>(a, h, s);
         return hipGetLastError();
     }
     float* planes = (float*)a.workspace;
@@ -640,6 +904,16 @@ hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
     if (h.rows) {
         float* to = sums ? planes : nullptr;
         lanes_as<TIO, V>(h.L, [&](auto L) { row_bwd<TIO, V, decltype(L)::value>(a, h, to, s); });
+    } else if (h.held) {
+        if (sums) {
+            if (h.wide == 8) { if constexpr (sizeof(TIO) == 2) columns<TIO, 8>(a, h, planes, s); }
+            else if (h.wide == 4) columns<TIO, 4>(a, h, planes, s);
+            else if (h.wide == 2) columns<TIO, 2>(a, h, planes, s);
+            else columns<TIO, 1>(a, h, planes, s);
+        }
+        if (a.act == TTT_ACT_SILU) block_bwd<TIO, V, TTT_ACT_SILU>(a, h, s);
+        else if (a.act == TTT_ACT_GELU) block_bwd<TIO, V, TTT_ACT_GELU>(a, h, s);
+        else block_bwd<TIO, V, TTT_ACT_NONE>(a, h, s);
     } else {
         float* means = (float*)((char*)a.workspace + up256(h.planes * 8 * a.C));
         if (a.act == TTT_ACT_SILU) slab_bwd<TIO, V, TTT_ACT_SILU>(a, h, planes, means, s);
@@ -657,13 +931,13 @@ hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
 size_t groupnorm_fwd_workspace(long long N, long long S, int C, int G, bool bf16)
 {
     const Shape h = shape_of(N, S, C, G, bf16);
-    return h.rows ? 0 : up256(h.planes * 8 * C);
+    return h.rows || h.held ? 0 : up256(h.planes * 8 * C);
 }
 
 size_t groupnorm_bwd_workspace(long long N, long long S, int C, int G, bool bf16)
 {
     const Shape h = shape_of(N, S, C, G, bf16);
-    return up256(h.planes * 8 * C) + (h.rows ? 0 : up256((size_t)N * G * 8));
+    return up256(h.planes * 8 * C) + (h.rows || h.held ? 0 : up256((size_t)N * G * 8));
 }
 
 hipError_t launch_groupnorm_fwd(const GroupArgs& a, hipStream_t s)

@@ -118,10 +118,12 @@ def test_groupnorm_of_nothing_does_nothing():
 
 
 def test_groupnorm_workspace_is_asked_for():
-    need = ttt.groupnorm_workspace_bytes(4, 100, 64, 8, 1)
+    need = ttt.groupnorm_workspace_bytes(4, 100000, 64, 8, 1)
     assert need > 0
-    assert group(ws=None) == ttt.ERR_WORKSPACE and group(wsb=need - 1) == ttt.ERR_WORKSPACE
-    assert ttt.groupnorm_workspace_bytes(4, 1, 64, 8, 1) == 0
+    assert group(S=100000, ws=None) == ttt.ERR_WORKSPACE
+    assert group(S=100000, wsb=need - 1) == ttt.ERR_WORKSPACE
+    for S in (1, 100):
+        assert ttt.groupnorm_workspace_bytes(4, S, 64, 8, 1) == 0
 
 
 def group_bwd(**kw):
@@ -142,7 +144,7 @@ def test_groupnorm_bwd_refuses(kw):
 
 
 def test_groupnorm_bwd_workspace_is_asked_for():
-    for S in (1, 100):
+    for S in (1, 100, 100000):
         need = ttt.groupnorm_bwd_workspace_bytes(4, S, 64, 8, 1)
         assert need > 0
         assert group_bwd(S=S, ws=None) == ttt.ERR_WORKSPACE

@@ -58,7 +58,8 @@ SHAPES = [
     # N, S, C, G
     (1, 1, 64, 1), (5, 1, 64, 8), (7, 1, 24, 8), (3, 1, 3, 1), (9, 1, 20, 1), (1000, 1, 96, 32), (4, 1, 2048, 32),
     (3, 1, 4096, 4), (2, 1, 640, 1), (600, 1, 160, 2), (2, 1, 5000, 1), (2, 49, 24, 8), (1, 100, 64, 4), (2, 1000, 640, 32),
-    (3, 2, 7, 7), (1, 5000, 5, 1), (2, 300, 4096, 32), (70, 9, 32, 4), (1, 33, 2051, 7),
+    (3, 2, 7, 7), (1, 5000, 5, 1), (40, 2, 512, 8), (30, 1, 4096, 1), (3, 1, 65536, 1), (2, 8, 8192, 2), (4, 3, 1200, 5),
+    (1, 40000, 6, 2), (2, 300, 4096, 32), (70, 9, 32, 4), (1, 33, 2051, 7),
 ]
 
 
