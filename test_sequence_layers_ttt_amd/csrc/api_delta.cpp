@@ -50,7 +50,9 @@ int delta_dims(int B, int H, int Hk, int T, int dk, int dv, int io_dtype)
     return TTT_OK;
 }
 
-// Few tokens go token by token: no preparing kernel, no workspace.
+// Few tokens go token by token: no preparing kernel, no workspace.  (us a call, by token and by
+// chunk: 8 x 12 heads of 64 features, 17 tokens 15.6 and 19.5, 24 tokens 20.0 and 19.6; 1 x 32 of
+// 128, 16 tokens 19.5 and 20.3, 24 tokens 27 and 20; 64 x 16 of 64, 17 tokens 35 and 50.)
 bool delta_by_token(int T) { return T <= 16; }
 
 struct DeltaSizes {

@@ -1,13 +1,14 @@
 // The gated delta rule's scans over the chunks: forward, and from the last chunk to the first.
 // (delta_common.h has the formulas.)
 //
-// One workgroup of four waves per head and 64 columns of values; a wave keeps W^T (or D^T) for
-// 16 of them in fp32 registers, since columns never meet: the result tiles of one product are,
-// as they lie in registers, operands of the next, and only what all waves need goes through
-// LDS.  All that the next chunk needs is loaded to registers while this one is worked on, and
-// then goes to the other LDS buffer: no product waits for memory, one barrier a chunk.  What
-// bounds a chunk (3.3 us with 64 features) is one wave's own instructions: some 650 of the
-// vector units, most of them splitting operands into parts, and 120 matrix products.
+// A wave keeps W^T (or D^T) for 16 columns of values in fp32 registers, since columns never meet:
+// the result tiles of one product are, as they lie in registers, operands of the next, and only
+// what all waves need goes through LDS.  A workgroup has 32 or 64 columns of a head.  A chunk's data
+// is loaded to registers one or two chunks ahead and goes to the other LDS buffer while this one is
+// worked on: one barrier a chunk.  What bounds a chunk (64 features: 2.5 us with 32 columns and the
+// card half empty, 4.0 us with 64 and the card full) is that each computing wave reads every operand
+// from LDS for its own 16 columns (56 KB), and its 650 vector instructions, most of which split
+// operands into parts, next to 120 matrix products of 16 cycles.
 //
 // The reverse scan needs nothing of the forward one, so in a backward pass both run at once.
 // Where there are too few heads for the card, each sequence is cut into segments.  First the
@@ -596,15 +597,15 @@ hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStre
 }
 
 // How a sequence is cut: into how many segments, and whether a workgroup takes 32 columns or 64.
-// A round of workgroups over the 256 compute units takes its chunks times (8 x 12 heads of 64
+// One filling of the 256 compute units takes its chunks times (8 x 12 heads of 64
 // features, us a chunk) 4.0 with 64 columns and 2.6 with 32, where the workgroup's waves meet less
 // in LDS; where only ends are found 2.3 and 1.8.  The ends and the second run cost 2 / segments of
 // the sequence where they fit at once, so segments pay from few heads on (1 x 32 heads of 64
-// features, 32768 tokens: 2.05 ms whole, 0.82 ms in 8 segments).
+// features, 32768 tokens: the whole call 2.05 ms, in 8 segments 0.68 ms).
 DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward)
 {
     const long long sides = backward ? 2 : 1, cus = 256;
-    auto rounds = [&](long long shares) { return (heads * shares + cus - 1) / cus; };
+    auto fillings = [&](long long shares) { return (heads * shares + cus - 1) / cus; };
     DeltaCut best = {1, chunks, false};
     long long least = -1;
     for (int narrow = 0; narrow < 2; ++narrow) {
@@ -615,10 +616,10 @@ DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward)
             if (n == 2) continue;                      // (the ends alone are half of it then)
             const int each = (chunks + n - 1) / n;
             if ((chunks + each - 1) / each != n) continue;   // (no empty segments)
-            long long cost = rounds(sides * n * parts) * (narrow ? 26 : 40) * each;
+            long long cost = fillings(sides * n * parts) * (narrow ? 26 : 40) * each;
             // the ends, and joins of about a chunk's time
             if (n > 1)
-                cost += rounds(sides * (n - 1) * parts + (n - 2) * wide) * (narrow ? 18 : 23) * each + 40 * n;
+                cost += fillings(sides * (n - 1) * parts + (n - 2) * wide) * (narrow ? 18 : 23) * each + 40 * n;
             if (least < 0 || cost < least) {
                 least = cost;
                 best = {n, each, narrow != 0};
