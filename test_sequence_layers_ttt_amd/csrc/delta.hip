@@ -45,8 +45,15 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaPass a)
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
     TileLoad<TIO, DK> lk, lq;
-    lk.load(Rows<const TIO>((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first), t0, T, dk, whole, tid);
-    lq.load(Rows<const TIO>((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first), t0, T, dk, whole, tid);
+    const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
+    if (whole && dk == DK && t0 + kChunk <= T) {
+        lk.load_inside(K, t0, tid);
+        lq.load_inside(Q, t0, tid);
+    } else {
+        lk.load(K, t0, T, dk, whole, tid);
+        lq.load(Q, t0, T, dk, whole, tid);
+    }
     const size_t unit = (size_t)local * a.chunks + chunk;
     Record& rec = a.records[unit];
     if (w == 0) {

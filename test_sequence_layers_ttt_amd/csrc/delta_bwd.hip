@@ -79,8 +79,13 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
         TileLoad<TIO, DK> lk, lq;
         const Rows<const TIO> K((const TIO*)a.f.K, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
         const Rows<const TIO> Q((const TIO*)a.f.Q, b, hk, a.f.Hk, T, dk, a.f.tokens_first);
-        lk.load(K, t0, T, dk, whole, tid);
-        lq.load(Q, t0, T, dk, whole, tid);
+        if (whole && dk == DK && t0 + kChunk <= T) {
+            lk.load_inside(K, t0, tid);
+            lq.load_inside(Q, t0, tid);
+        } else {
+            lk.load(K, t0, T, dk, whole, tid);
+            lq.load(Q, t0, T, dk, whole, tid);
+        }
         lk.put(tk, tid);
         lq.put(tq, tid);
     }

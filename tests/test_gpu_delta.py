@@ -302,7 +302,8 @@ def test_many_heads(dev, shape, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("shape", [(1, 32, 1, 8192, 64, 64), (1, 32, 1, 8200, 32, 50), (1, 24, 1, 12000, 128, 64)])
+@pytest.mark.parametrize("shape", [(1, 32, 1, 8192, 64, 64), (1, 32, 1, 8200, 32, 50), (1, 24, 1, 12000, 128, 64),
+                                   (1, 24, 1, 8192, 32, 64)])
 def test_segments_of_many_heads(dev, shape, io):
     """Sequences in segments with workgroups of 64 columns: as a few heads at a time."""
     B, H, share, T, dk, dv = shape
