@@ -320,3 +320,35 @@ def test_segments_of_many_heads(dev, shape, io):
         for i, (a, b) in enumerate(zip(whole, alone)):
             err = (a[:, s].double() - b.double()).abs().max().item()
             assert err <= (rel + more.get(i, 0)) * b.double().abs().max().item(), (h, i, err)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 3, 1, 40, 64, 64), (1, 2, 1, 33, 128, 1), (1, 2, 2, 90, 2, 256)])
+def test_step_of_many_tokens(dev, shape, io):
+    c = Case(dev, *shape, io, seed=44, forget=(20,))
+    W = c.W0.clone()
+    Z = ttt.delta_step(c.K, c.Q, c.V, c.eta, c.g, W)
+    check_fwd(c, Z, W)
+
+
+def test_one_tensor_for_keys_queries_and_values(dev):
+    c = Case(dev, 1, 2, 1, 100, 64, 64, "f32", ttt.LAYOUT_BTHD, seed=45)
+    c.Q = c.V = c.K
+    check_fwd(c, *ttt.delta_fwd(c.K, c.K, c.K, c.eta, c.g, c.W0, layout=c.layout))
+    check_bwd(c, ttt.delta_bwd(c.K, c.K, c.K, c.eta, c.g, c.W0, c.dZ, c.dW, layout=c.layout))
+
+
+def test_backward_leaves_out_what_is_not_asked_for(dev):
+    """deta, dg and dW0 are optional in the C call; a shared head's sums are not."""
+    import torch
+    c = Case(dev, 1, 4, 2, 100, 64, 64, "bf16", seed=46)
+    want = ttt.delta_bwd(c.K, c.Q, c.V, c.eta, c.g, c.W0, c.dZ, c.dW)
+    dK, dQ, dV = (torch.empty_like(t) for t in (c.K, c.Q, c.V))
+    n = ttt.delta_bwd_workspace_bytes(1, 4, 2, 100, 64, 64, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    rc = ttt.lib().ttt_delta_bwd(p(c.K), p(c.Q), p(c.V), p(c.eta), 0.0, p(c.g), p(c.W0), p(c.dZ), p(c.dW), p(dK), p(dQ),
+                                 p(dV), None, None, None, 1, 4, 2, 100, 64, 64, 0, 1, p(ws), n,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert rc == ttt.OK
+    assert all((a == b).all() for a, b in zip((dK, dQ, dV), want))

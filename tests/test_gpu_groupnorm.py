@@ -146,3 +146,32 @@ def test_outputs_end_where_they_should(dev):
         wide = [torch.full((C + 64,), 7.0, device=dev) for _ in range(2)]
         ttt.groupnorm_bwd(X, G, w, b, dY, mean, rstd, dX=room[:n].view(X.shape), dweight=wide[0][:C], dbias=wide[1][:C])
         assert (room[n:] == 7).all() and all((t[C:] == 7).all() for t in wide)
+
+
+@pytest.mark.parametrize("shape", [(70000, 1, 32, 4), (9, 3, 40, 5), (2, 9000, 40, 5)])
+def test_weight_or_bias_alone(dev, shape):
+    N, S, C, G = shape
+    X, w, b, dY = make(dev, N, S, C, "f32", 9)
+    for ww, bb in ((w, None), (None, b)):
+        Y, mean, rstd = ttt.groupnorm_fwd(X, G, ww, bb, EPS, ttt.ACT_SILU)
+        y, _, _, ey, _, _ = ref.groupnorm(np64(X), G, np64(ww), np64(bb), EPS, "silu")
+        assert ref.within(np64(Y), y, ey, "f32")[0]
+        dx, dw, db = ttt.groupnorm_bwd(X, G, ww, bb, dY, mean, rstd, ttt.ACT_SILU)
+        assert (dw is None) == (ww is None) and (db is None) == (bb is None)
+        want, bound = ref.groupnorm_bwd(np64(X), G, np64(ww), np64(bb), np64(dY), np64(mean), np64(rstd), "silu")
+        for got, v, e in zip((dx, dw, db), want, bound):
+            assert got is None or ref.within(np64(got), v, e, "f32")[0]
+
+
+def test_refuses_what_does_not_fit(dev):
+    import torch
+    X, w, b, dY = make(dev, 4, 10, 32, "f32", 10)
+    stats = torch.zeros(4, 8, device=dev)
+    for call in (lambda: ttt.groupnorm_fwd(X, 5), lambda: ttt.groupnorm_fwd(X, 0), lambda: ttt.groupnorm_fwd(X[0, 0], 4),
+                 lambda: ttt.groupnorm_fwd(X, 4, w[:16]), lambda: ttt.groupnorm_fwd(X, 4, w.double()),
+                 lambda: ttt.groupnorm_fwd(X.transpose(1, 2), 4), lambda: ttt.groupnorm_fwd(X, 4, mean=stats),
+                 lambda: ttt.groupnorm_bwd(X, 4, w, b, dY, stats, stats), lambda: ttt.groupnorm_fwd(X.cpu(), 4)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ttt.groupnorm_fwd(X.half(), 4)
