@@ -396,17 +396,37 @@ __global__ void __launch_bounds__(256) group_statistics_kernel(GroupArgs a, int 
     const float* from = planes + (size_t)row * parts * 2 * a.C + group * per;
     const int entries = parts * per;
     const double n = (double)a.S * per;
-    auto have = [&](int part) { return (double)max(0ll, min(each, a.S - each * part)); };
+    auto have = [&](int part) { return (float)max(0ll, min(each, a.S - each * part)); };
+    // (the first entries of a thread stay in registers)
+    constexpr int KEPT = 12;
+    float m[KEPT], q[KEPT], h[KEPT];
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) {
+        const int e = threadIdx.x + 256 * k;
+        m[k] = q[k] = h[k] = 0.f;
+        if (e < entries) {
+            const float* p = from + (size_t)(e / per) * 2 * a.C + e % per;
+            m[k] = p[0];
+            q[k] = p[a.C];
+            h[k] = have(e / per);
+        }
+    }
     double s = 0.0;
-    for (int e = threadIdx.x; e < entries; e += 256)
-        s += have(e / per) * from[(size_t)(e / per) * 2 * a.C + e % per];
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k)
+        if (h[k] > 0.f) s += (double)h[k] * m[k];
+    for (int e = threadIdx.x + 256 * KEPT; e < entries; e += 256)
+        s += (double)have(e / per) * from[(size_t)(e / per) * 2 * a.C + e % per];
     const double mean = block_sum(s, room) / n;
     s = 0.0;
-    for (int e = threadIdx.x; e < entries; e += 256) {
-        const double h = have(e / per);
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k)
+        if (h[k] > 0.f) s += q[k] + h[k] * (m[k] - mean) * (m[k] - mean);
+    for (int e = threadIdx.x + 256 * KEPT; e < entries; e += 256) {
+        const double g = have(e / per);
         const float* p = from + (size_t)(e / per) * 2 * a.C + e % per;
         const double d = p[0] - mean;
-        if (h > 0.0) s += p[a.C] + h * d * d;
+        if (g > 0.0) s += p[a.C] + g * d * d;
     }
     s = block_sum(s, room) / n;
     if (threadIdx.x == 0) {
