@@ -601,7 +601,7 @@ hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStre
 // features, us a chunk) 4.0 with 64 columns and 2.6 with 32, where the workgroup's waves meet less
 // in LDS; where only ends are found 2.3 and 1.8.  The ends and the second run cost 2 / segments of
 // the sequence where they fit at once, so segments pay from few heads on (1 x 32 heads of 64
-// features, 32768 tokens: the whole call 2.05 ms, in 8 segments 0.68 ms).
+// features, 32768 tokens: the whole call 2.05 ms, in 8 segments 0.69 ms).
 DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward)
 {
     const long long sides = backward ? 2 : 1, cus = 256;
