@@ -554,8 +554,9 @@ size_t ttt_clip_workspace_bytes(void);
  *             padding of a shorter sequence (whose keys and values have to be finite).
  *   W0      : [B, H, dv, dk] fp32 state before the first token, or NULL for zero.
  *   W_out   : [B, H, dv, dk] fp32 state after the last token (may be W0), or NULL.
- *   1 <= dk <= 128, 1 <= dv <= 256 (TTT_ERR_UNSUPPORTED past that), T >= 1; token tensors
- *   and states 16-byte aligned, eta and g 4-byte.
+ *   1 <= dk <= 128, 1 <= dv <= 256 (TTT_ERR_UNSUPPORTED past that), 1 <= T <= 2^30; B H
+ *   ceil(dv / 16) and (H / Hk) ceil(T / 64) below 2^24; token tensors and states 16-byte
+ *   aligned, eta and g 4-byte.
  *   workspace : at least ttt_delta_workspace_bytes(...) bytes, 256-byte aligned; one for
  *             each call that may overlap in time, graph replays included.
  * Sums, states and the products behind W_out are fp32 (operands that are not exact in bf16

@@ -42,10 +42,10 @@ int delta_dims(int B, int H, int Hk, int T, int dk, int dv, int io_dtype)
     if (B <= 0 || H <= 0 || Hk <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(io_dtype) || H % Hk)
         return TTT_ERR_INVALID_ARG;
     if (dk > kDeltaMostDk || dv > kDeltaMostDv) return TTT_ERR_UNSUPPORTED;
-    // token counts with room in an int; (head, chunk) pairs and 16-row blocks of states inside
-    // a grid
-    const long double heads = (long double)B * H;
-    if (T > 1 << 30 || heads * 16 >= 2147483648.0L || heads * ((T + 63) / 64) >= 2147483648.0L)
+    // token counts with room in an int; 16-row blocks of states, and the chunks of the heads that
+    // share keys, inside a grid (2^32 threads of 256 a workgroup)
+    const long double heads = (long double)B * H, most = 16777216.0L;
+    if (T > 1 << 30 || heads * ((dv + 15) / 16) >= most || (long double)(H / Hk) * ((T + 63) / 64) >= most)
         return TTT_ERR_INVALID_ARG;
     return TTT_OK;
 }

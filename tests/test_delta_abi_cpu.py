@@ -23,7 +23,7 @@ BAD_DELTA = [
     dict(W0=P[5] + 4), dict(eta=P[3] + 2), dict(g=P[4] + 1), dict(B=0), dict(H=0), dict(Hk=0), dict(Hk=3),
     dict(T=0), dict(dk=0), dict(dv=-1), dict(lay=2), dict(lay=-1), dict(io=2), dict(T=(1 << 30) + 1),
     dict(eta=None, es=math.nan), dict(eta=None, es=math.inf), dict(B=1 << 20, H=1 << 10, Hk=1),
-    dict(B=1 << 10, H=1 << 10, T=1 << 28),
+    dict(B=1 << 10, H=1 << 10, Hk=1, T=1 << 28), dict(B=1 << 22, H=1, Hk=1), dict(B=1, H=4, Hk=1, T=1 << 28),
 ]
 
 
