@@ -559,11 +559,10 @@ size_t ttt_clip_workspace_bytes(void);
  *   aligned, eta and g 4-byte.
  *   workspace : at least ttt_delta_workspace_bytes(...) bytes, 256-byte aligned; one for
  *             each call that may overlap in time, graph replays included.
- * Sums, states and the products behind W_out are fp32 (operands that are not exact in bf16
- * go to the matrix cores in three bf16 parts); of the products behind a bf16 Z what is
- * below 2^-16 of them is left out.  Magnitudes below 1e-33 lose their last digits, and those
- * above 3.38e38 turn NaN.  Non-finite values spread within their (batch, head) and may turn
- * NaN.  Every output is the same bits on every call. */
+ * Sums, states and products are fp32 (operands that are not exact in bf16 go to the matrix
+ * cores in three bf16 parts), and a bf16 Z is rounded once from them.  Magnitudes below 1e-33
+ * lose their last digits, and those above 3.38e38 turn NaN.  Non-finite values spread within
+ * their (batch, head) and may turn NaN.  Every output is the same bits on every call. */
 int ttt_delta_fwd(const void* K, const void* Q, const void* V, const float* eta, float eta_scalar,
                   const float* g, const float* W0, void* Z, float* W_out,
                   int B, int H, int Hk, int T, int dk, int dv, int layout, int io_dtype,

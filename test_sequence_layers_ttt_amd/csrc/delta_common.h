@@ -57,13 +57,12 @@ __device__ __forceinline__ Parts<N> split(f32x4 a, f32x4 b)
     return r;
 }
 
-// c + a b over 32 contraction slots, part products of order up to O (2: fp32's accuracy,
-// 1: about 2^-17), the smallest first
-template <int O = 2, int NA, int NB>
+// c + a b over 32 contraction slots, part products of order up to 2, the smallest first
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32x4 c)
 {
 #pragma unroll
-    for (int s = O; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             const int j = s - i;
@@ -73,8 +72,6 @@ __device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32
 }
 
 template <typename TIO> constexpr int kParts = sizeof(TIO) == 2 ? 1 : 3;
-// parts of P that the forward scan takes: behind a bf16 Z two are enough (2^-17)
-template <typename TIO> constexpr int kZParts = sizeof(TIO) == 2 ? 2 : 3;
 
 // ---- token tensors ---------------------------------------------------------
 // rows of one (batch, head) of [B, H, T, d] or [B, T, H, d]

@@ -57,7 +57,7 @@ __device__ __forceinline__ float* start_of(const DeltaPass& a, int local, int se
 // Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
 template <typename TIO, int DK, int KEEP, int CW, bool BACK>
 struct Forward {
-    static constexpr int NZ = KEEP == kRead ? kZParts<TIO> : 0;
+    static constexpr int NZ = KEEP == kRead ? 3 : 0;   // parts of P
     typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
     static constexpr bool APART = kApart<TIO, DK, CW, BACK>, PARTS = BACK && CW == 4;
@@ -66,7 +66,7 @@ struct Forward {
     // `unit`: V = 0 and a unit matrix for the start, columns are features
     static __device__ __forceinline__ void run(const DeltaPass& a, Tiles* tiles, Share s, bool unit)
     {
-        constexpr int M = DK / 16, J = DK / 32, OZ = kZParts<TIO> - 1;
+        constexpr int M = DK / 16, J = DK / 32;
         const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
         const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int local = s.local, head = a.head0 + local, first = s.first;
@@ -217,13 +217,13 @@ struct Forward {
 #pragma unroll
                     for (int j = 0; j < J; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z[i] = mma<OZ>(wp[j], qt[j][i], z[i]);
+                        for (int i = 0; i < 4; ++i) z[i] = mma(wp[j], qt[j][i], z[i]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) z[i] *= t.start[16 * i + c];
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int i = 2 * j; i < 4; ++i) z[i] = mma<OZ>(u[j], P[frag_lower(i, j)], z[i]);
+                        for (int i = 2 * j; i < 4; ++i) z[i] = mma(u[j], P[frag_lower(i, j)], z[i]);
                     const int token = n * kChunk + c;
                     if (fours && first + 16 * CW <= dv && (n + 1) * kChunk <= T) {
 #pragma unroll
