@@ -2,13 +2,19 @@
 //
 // The forward scan is run again and keeps every chunk's first state and U, while a second scan
 // carries the state's gradient D from the last chunk to the first; the gradients of keys, queries,
-// step sizes and decays then follow chunk by chunk, all chunks at once.  Every sum has a fixed order: the same bits on
-// every call.
+// step sizes and decays then follow chunk by chunk, all chunks at once.  Every sum has a fixed order:
+// the same bits on every call.
 //
 // The decay's gradient is the product of D and the state across the token, that is of all
-// that is read from token t on with all that was written before it.  Within a chunk, with
-// row t of dQ, of the part of dK that reads (from R) and of the part that writes,
-//   dg_t = sum over s >= t of (q_s.dQ_s + k_s.dKread_s - k_s.dKwrite_s) + <D, W'> at the end.
+// that is read from token t on with all that was written before it.  Within a chunk, with the
+// gradients dP and dL that are left of the pairs (s reads what r wrote) after their decays,
+//   dg_t = sum over s >= t > r of (dP_sr q_s.k_r + dL_sr k_s.k_r)        (pairs across t)
+//        + sum over s >= t of what s reads of the chunk's first state
+//        + sum over r < t of what is left of r's write at the chunk's end
+//        + start_C <D, W>.
+// Every term has the decay of t in it, so a strong one makes all of them small: the sum has its
+// own digits.  (A difference of sums over whole rows and columns of the pairs keeps only the
+// digits of what does not cross t: all that dg_t is after a decay of exp(-16).)
 #include <algorithm>
 
 #include "delta_common.h"
@@ -41,7 +47,10 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
     __shared__ __align__(16) quad fu[4 * 3 * 64], fv[4 * 3 * 64], fz[4 * NP * 64], fw[M * 3 * 64], fd[M * 3 * 64];
     __shared__ double across[4];
     __shared__ __align__(16) float hi[kChunk], lo[kChunk];
-    __shared__ float dG[kChunk];
+    // of dg: what a token reads of the first state, leaves at the end, reads of tiles before its
+    // own; pairs across it in its own tile; what the tiles after it read of it, a row for each
+    __shared__ float reads[kChunk], leaves[kChunk], rows[kChunk], inner[kChunk];
+    __shared__ __align__(16) float later[4][kChunk];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -176,15 +185,64 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
             }
         }
     }
-    float wrote = 0.f;
+    // pairs (rows r, column s = own) across a token: those that end at s in the tiles of r before
+    // its own (row sum), what each r has in this tile of s (column sums), and in the tile on the
+    // diagonal, for t = 4 g + e + 1, all r < t <= s
+    {
+        float row = 0.f;
+        if (lane < 16) inner[own] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i > w) continue;
+            f32x4 qk = zero, kk = zero;
+#pragma unroll
+            for (int j = 0; j < DK / 32; ++j) {
+                const Parts<NP> r = by_token(tk, i, j, lane);
+                qk = mma(r, by_token(tq, w, j, lane), qk);
+                kk = mma(r, by_token(tk, w, j, lane), kk);
+            }
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = 16 * i + 4 * g + e < own ? fmaf(pt[i][e], qk[e], lt[i][e] * kk[e]) : 0.f;
+            if (i < w) {
+                row += (x[0] + x[1]) + (x[2] + x[3]);
+                row_sum16_n(x);
+                if (c == 0) *reinterpret_cast<f32x4*>(later[w] + 16 * i + 4 * g) = f32x4{x[0], x[1], x[2], x[3]};
+            } else {
+#pragma unroll
+                for (int e = 1; e < 4; ++e) x[e] += x[e - 1];
+                float all4 = x[3];
+#pragma unroll
+                for (int o = 16; o < 64; o <<= 1) {
+                    const float y = __shfl_up(all4, o, 64);
+                    if (lane >= o) all4 += y;
+                }
+                const float before = __shfl_up(all4, 16, 64);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = 4 * g + e < c ? x[e] + (g ? before : 0.f) : 0.f;
+                row_sum16_n(x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c == 0 && 4 * g + e < 15) inner[16 * w + 4 * g + e + 1] = x[e];
+            }
+        }
+        row += __shfl_xor(row, 16, 64);
+        row += __shfl_xor(row, 32, 64);
+        if (g == 0) rows[own] = row;
+    }
+    float wrote = 0.f, read = 0.f;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         aw[m] *= so;
         av[m] *= -so;
         ad[m] *= no;
-        const f32x4 k4 = token4(tk, own, 16 * m + 4 * g);
+        const f32x4 k4 = token4(tk, own, 16 * m + 4 * g), q4 = token4(tq, own, 16 * m + 4 * g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) wrote = fmaf(k4[e], ad[m][e], wrote);
+        for (int e = 0; e < 4; ++e) {
+            wrote = fmaf(k4[e], ad[m][e], wrote);
+            read = fmaf(q4[e], aw[m][e], fmaf(k4[e], av[m][e], read));
+        }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -206,41 +264,58 @@ __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
             }
         }
     }
-    float sum = 0.f;
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const f32x4 k4 = token4(tk, own, 16 * m + 4 * g), q4 = token4(tq, own, 16 * m + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            sum = fmaf(q4[e], aw[m][e], fmaf(k4[e], av[m][e] - ad[m][e], sum));
-        av[m] += ad[m];
-    }
-    // <D, W'> = start_C <D, W> + sum of k_s.(written part of dK_s)
-    double cross = (double)kept * all + wrote;
+    for (int m = 0; m < M; ++m) av[m] += ad[m];
+    double cross = (double)kept * all;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) cross += __shfl_xor(cross, o, 64);
-    sum += __shfl_xor(sum, 16, 64);
-    sum += __shfl_xor(sum, 32, 64);
-    de += __shfl_xor(de, 16, 64);
-    de += __shfl_xor(de, 32, 64);
+    auto over_groups = [](float x) {
+        x += __shfl_xor(x, 16, 64);
+        return x + __shfl_xor(x, 32, 64);
+    };
+    wrote = over_groups(wrote);
+    read = over_groups(read);
+    de = over_groups(de);
     if (g == 0) {
-        dG[own] = sum;
+        reads[own] = read;
+        leaves[own] = wrote;
         const Rows<float> o(q_.a.deta, b, h, a.f.H, T, 1, a.f.tokens_first);
         if (q_.a.deta && inside) *o.at(t0 + own) = de;
     }
     if (lane == 0) across[w] = cross;
     __syncthreads();
     if (w == 0 && q_.a.dg) {
-        double y = dG[lane];
+        const int t = lane, tile = lane >> 4;
+        double r = reads[t], l = leaves[t];
+        float y = rows[t], x[4];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) x[i] = t < 16 * i ? later[i][t] : 0.f;
+#pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const double z = __shfl_down(y, o, 64);
-            if (lane + o < 64) y += z;
+            const double r1 = __shfl_down(r, o, 64), l1 = __shfl_up(l, o, 64);
+            if (t + o < 64) r += r1;
+            if (t >= o) l += l1;
+            const float y1 = __shfl_down(y, o, 64);
+            if (o < 16 && c + o < 16) y += y1;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                const float x1 = __shfl_up(x[i], o, 64);
+                if (t >= o) x[i] += x1;
+            }
         }
-        y += across[0] + across[1] + across[2] + across[3];
+        // (sums over r < t: those through t - 1)
+        l = __shfl_up(l, 1, 64);
+        double pairs = (double)y + inner[t];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const float x1 = __shfl_up(x[i], 1, 64);
+            if (t && i > tile) pairs += x1;
+        }
+        const double all_ = (across[0] + across[1]) + (across[2] + across[3]);
         const Rows<float> o(q_.a.dg, b, h, a.f.H, T, 1, a.f.tokens_first);
-        if (t0 + lane < T) *o.at(t0 + lane) = rec.forgets[lane] ? 0.f : (float)y;
+        if (t0 + t < T) *o.at(t0 + t) = rec.forgets[t] ? 0.f : (float)(pairs + r + (t ? l : 0.0) + all_);
     }
-if (q_.dK) {
+    if (q_.dK) {
         float* to = q_.dK + (unit * kChunk + own) * DK + 4 * g;
         float* tq_ = q_.dQ + (unit * kChunk + own) * DK + 4 * g;
 #pragma unroll
