@@ -613,8 +613,8 @@ size_t ttt_delta_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv
  *   weight, bias : [C] fp32, or NULL for ones and zeros.
  *   mean, rstd   : [N, G] fp32 (outputs: the mean and 1 / sqrt(var + eps)).
  *   act          : a ttt_act.  eps : > 0 and finite (no denormal number).
- *   N, S >= 0 (0 does nothing), C a multiple of G, C <= 2^20; X and Y 16-byte aligned,
- *   the others 4-byte.
+ *   N, S >= 0 (0 does nothing), C a multiple of G, C <= 2^20, N G and N ceil(C / 256) below
+ *   2^31; X and Y 16-byte aligned, the others 4-byte.
  *   workspace    : at least ttt_groupnorm_workspace_bytes(...) bytes, 256-byte aligned.
  * Arithmetic is fp32, sums in a fixed order: the same bits on every call. */
 int ttt_groupnorm_fwd(const void* X, const float* weight, const float* bias, float eps, int act,

@@ -103,7 +103,8 @@ int delta_outputs(DeltaArgs& a, const DeltaSizes& n, void* Z, float* W_out)
 bool group_dims_ok(long long N, long long S, int C, int G, int io_dtype)
 {
     if (N < 0 || S < 0 || C <= 0 || G <= 0 || C % G || C > 1 << 20 || !dtype_ok(io_dtype)) return false;
-    // every element index inside 2^59, a wave for each group of each row inside a grid
+    // every element index inside 2^59; groups of rows, and rows by 256 channels, in an int (the
+    // kernels' grids go on along further axes from 2^22 workgroups on)
     return (long double)N * S * C < 5.0e17L && (long double)N * G < 2147483648.0L &&
            (long double)N * ((C + 255) / 256) < 2147483648.0L;
 }

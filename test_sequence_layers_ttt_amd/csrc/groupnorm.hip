@@ -28,6 +28,15 @@
 namespace ttt {
 namespace {
 
+// A launch has fewer than 2^32 threads along an axis of its grid: workgroups past 2^22 go on along y.
+__device__ __forceinline__ long long workgroup() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+constexpr long long kMostX = 1 << 22;
+dim3 workgroups(long long n)
+{
+    const long long x = std::min(n, kMostX);
+    return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 // V elements of the I/O type as fp32
 template <typename TIO, int V> struct Vec {
     RawRow<TIO, V> raw;
@@ -269,22 +278,22 @@ __global__ void __launch_bounds__(1024) group_planes_kernel(const float* planes,
 }
 
 // ---- many places: channels in the threads, places over the workgroups --------------------
-// Workgroup (x: row by row 256 threads' worth of vectors of channels, y: places first .. last).
+// Workgroup (x and z: row by row 256 threads' worth of vectors of channels, y: places first .. last).
 struct Slab {
     long long row;
     int ch, slot, slots;      // channel, place within a step, places a step
     bool in;
     long long first, last;
-    __device__ __forceinline__ Slab(int vectors, int V, long long S, int parts)
+    __device__ __forceinline__ Slab(int vectors, int V, long long N, long long S, int parts)
     {
         const int wide = (vectors + 255) / 256;
-        row = blockIdx.x / wide;
+        row = (long long)blockIdx.z * (gridDim.x / wide) + blockIdx.x / wide;
         int t = threadIdx.x, x = (int)(blockIdx.x % wide) * 256;
         slots = vectors < 256 ? 256 / vectors : 1;
         slot = 0;
         if (vectors < 256) { slot = t / vectors; t -= slot * vectors; }
         ch = (x + t) * V;
-        in = x + t < vectors && slot < slots;
+        in = x + t < vectors && slot < slots && row < N;
         const long long each = (S + parts - 1) / parts;
         first = each * blockIdx.y;
         last = first + each < S ? first + each : S;
@@ -330,7 +339,7 @@ template <typename TIO, int V>
 __global__ void __launch_bounds__(256) group_moments_kernel(GroupArgs a, int parts, float* planes)
 {
     const int vectors = a.C / V;
-    const Slab p(vectors, V, a.S, parts);
+    const Slab p(vectors, V, a.N, a.S, parts);
     const TIO* X = (const TIO*)a.X + p.row * a.S * a.C;
     float shift[V], s[V], q[V];
 #pragma unroll
@@ -390,8 +399,9 @@ __device__ __forceinline__ double block_sum(double x, double* room)
 __global__ void __launch_bounds__(256) group_statistics_kernel(GroupArgs a, int parts, const float* planes)
 {
     __shared__ double room[4];
-    const long long row = blockIdx.x / a.G;
-    const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
+    const long long id = workgroup(), row = id / a.G;
+    const int group = (int)(id % a.G), per = a.C / a.G;
+    if (row >= a.N) return;
     const long long each = (a.S + parts - 1) / parts;
     const float* from = planes + (size_t)row * parts * 2 * a.C + group * per;
     const int entries = parts * per;
@@ -430,15 +440,15 @@ __global__ void __launch_bounds__(256) group_statistics_kernel(GroupArgs a, int 
     }
     s = block_sum(s, room) / n;
     if (threadIdx.x == 0) {
-        a.mean[blockIdx.x] = (float)mean;
-        a.rstd[blockIdx.x] = (float)(1.0 / sqrt(s + (double)a.eps));
+        a.mean[id] = (float)mean;
+        a.rstd[id] = (float)(1.0 / sqrt(s + (double)a.eps));
     }
 }
 
 template <typename TIO, int V, int ACT>
 __global__ void __launch_bounds__(256) group_apply_kernel(GroupArgs a, int parts)
 {
-    const Slab p(a.C / V, V, a.S, parts);
+    const Slab p(a.C / V, V, a.N, a.S, parts);
     if (!p.in) return;
     const long long row = p.row;
     const TIO* X = (const TIO*)a.X + row * a.S * a.C + p.ch;
@@ -469,7 +479,7 @@ template <typename TIO, int V, int ACT>
 __global__ void __launch_bounds__(256) group_sums_kernel(GroupBwdArgs a, int parts, float* planes)
 {
     const int vectors = a.C / V;
-    const Slab p(vectors, V, a.S, parts);
+    const Slab p(vectors, V, a.N, a.S, parts);
     const long long row = p.row;
     const TIO* X = (const TIO*)a.X + row * a.S * a.C + p.ch;
     const TIO* dY = (const TIO*)a.dY + row * a.S * a.C + p.ch;
@@ -520,8 +530,9 @@ __global__ void __launch_bounds__(256) group_means_kernel(GroupBwdArgs a, int pa
                                                           float* means)
 {
     __shared__ double room[4];
-    const long long row = blockIdx.x / a.G;
-    const int group = (int)(blockIdx.x % a.G), per = a.C / a.G;
+    const long long id = workgroup(), row = id / a.G;
+    const int group = (int)(id % a.G), per = a.C / a.G;
+    if (row >= a.N) return;
     const float* from = planes + (size_t)row * parts * 2 * a.C + group * per;
     double m1 = 0.0, m2 = 0.0;
     for (int e = threadIdx.x; e < parts * per; e += 256) {
@@ -534,15 +545,15 @@ __global__ void __launch_bounds__(256) group_means_kernel(GroupBwdArgs a, int pa
     m2 = block_sum(m2, room);
     if (threadIdx.x == 0) {
         const double n = (double)a.S * per;
-        means[2 * (size_t)blockIdx.x] = (float)(m1 / n);
-        means[2 * (size_t)blockIdx.x + 1] = (float)(m2 / n);
+        means[2 * id] = (float)(m1 / n);
+        means[2 * id + 1] = (float)(m2 / n);
     }
 }
 
 template <typename TIO, int V, int ACT>
 __global__ void __launch_bounds__(256) group_dx_kernel(GroupBwdArgs a, int parts, const float* means)
 {
-    const Slab p(a.C / V, V, a.S, parts);
+    const Slab p(a.C / V, V, a.N, a.S, parts);
     if (!p.in) return;
     const long long row = p.row, at = row * a.S * a.C + p.ch;
     const TIO* X = (const TIO*)a.X + at;
@@ -605,7 +616,7 @@ struct Held {
     {
         const int per = C / G, pv = per / V, count = (int)(S * pv);
         lane = threadIdx.x % TS;
-        slab = (long long)blockIdx.x * (blockDim.x / TS) + threadIdx.x / TS;
+        slab = workgroup() * (blockDim.x / TS) + threadIdx.x / TS;
         live = slab < N * G;
         first = (int)(slab % G) * per;
         base = slab / G * S * C + first;
@@ -703,7 +714,7 @@ template <typename TIO, int V, int ACT>
 __global__ void __launch_bounds__(256) group_columns_kernel(GroupBwdArgs a, float* planes)
 {
     const int vectors = a.C / V, per = a.C / a.G;
-    const Slab p(vectors, V, a.N * a.S, (int)gridDim.y);
+    const Slab p(vectors, V, 1, a.N * a.S, (int)gridDim.y);
     const bool one = per % V == 0;      // (a vector's channels are of one group)
     const int group = p.ch / per;
     float s[V], q[V];
@@ -857,22 +868,24 @@ template <typename TIO, int V, int ACT>
 void block_fwd(const GroupArgs& a, const Shape& h, hipStream_t s)
 {
     const long long slabs = a.N * a.G;
-    if (h.held == 16)
-        group_block_fwd_kernel<TIO, V, ACT, 16><<<(unsigned)((slabs + 15) / 16), 256, 0, s>>>(a);
-    else if (h.held == 64) group_block_fwd_kernel<TIO, V, ACT, 64><<<(unsigned)((slabs + 3) / 4), 256, 0, s>>>(a);
-    else if (h.held == 256) group_block_fwd_kernel<TIO, V, ACT, 256><<<(unsigned)slabs, 256, 0, s>>>(a);
-    else group_block_fwd_kernel<TIO, V, ACT, 512><<<(unsigned)slabs, 512, 0, s>>>(a);
+    const int each = h.held < 256 ? 256 / h.held : 1;
+    const dim3 grid = workgroups((slabs + each - 1) / each);
+    if (h.held == 16) group_block_fwd_kernel<TIO, V, ACT, 16><<<grid, 256, 0, s>>>(a);
+    else if (h.held == 64) group_block_fwd_kernel<TIO, V, ACT, 64><<<grid, 256, 0, s>>>(a);
+    else if (h.held == 256) group_block_fwd_kernel<TIO, V, ACT, 256><<<grid, 256, 0, s>>>(a);
+    else group_block_fwd_kernel<TIO, V, ACT, 512><<<grid, 512, 0, s>>>(a);
 }
 
 template <typename TIO, int V, int ACT>
 void block_bwd(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
 {
     const long long slabs = a.N * a.G;
-    if (h.held == 16)
-        group_block_bwd_kernel<TIO, V, ACT, 16><<<(unsigned)((slabs + 15) / 16), 256, 0, s>>>(a);
-    else if (h.held == 64) group_block_bwd_kernel<TIO, V, ACT, 64><<<(unsigned)((slabs + 3) / 4), 256, 0, s>>>(a);
-    else if (h.held == 256) group_block_bwd_kernel<TIO, V, ACT, 256><<<(unsigned)slabs, 256, 0, s>>>(a);
-    else group_block_bwd_kernel<TIO, V, ACT, 512><<<(unsigned)slabs, 512, 0, s>>>(a);
+    const int each = h.held < 256 ? 256 / h.held : 1;
+    const dim3 grid = workgroups((slabs + each - 1) / each);
+    if (h.held == 16) group_block_bwd_kernel<TIO, V, ACT, 16><<<grid, 256, 0, s>>>(a);
+    else if (h.held == 64) group_block_bwd_kernel<TIO, V, ACT, 64><<<grid, 256, 0, s>>>(a);
+    else if (h.held == 256) group_block_bwd_kernel<TIO, V, ACT, 256><<<grid, 256, 0, s>>>(a);
+    else group_block_bwd_kernel<TIO, V, ACT, 512><<<grid, 512, 0, s>>>(a);
 }
 
 template <typename TIO, int V>
@@ -882,6 +895,13 @@ void columns(const GroupBwdArgs& a, const Shape& h, float* planes, hipStream_t s
     if (a.act == TTT_ACT_SILU) group_columns_kernel<TIO, V, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, planes);
     else if (a.act == TTT_ACT_GELU) group_columns_kernel<TIO, V, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, planes);
     else group_columns_kernel<TIO, V, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, planes);
+}
+
+// the slabs' kernels: rows along x, past its threads along z
+dim3 slab_grid(const Shape& h, long long N)
+{
+    const long long rows = std::min(N, kMostX / h.x);
+    return dim3((unsigned)(h.x * rows), h.parts, (unsigned)((N + rows - 1) / rows));
 }
 
 template <typename TIO, int V>
@@ -898,9 +918,9 @@ hipError_t fwd_as(const GroupArgs& a, const Shape& h, hipStream_t s)
         return hipGetLastError();
     }
     float* planes = (float*)a.workspace;
-    const dim3 grid((unsigned)(h.x * a.N), h.parts);
+    const dim3 grid = slab_grid(h, a.N);
     group_moments_kernel<TIO, V><<<grid, 256, 0, s>>>(a, h.parts, planes);
-    group_statistics_kernel<<<(unsigned)(a.N * a.G), 256, 0, s>>>(a, h.parts, planes);
+    group_statistics_kernel<<<workgroups(a.N * a.G), 256, 0, s>>>(a, h.parts, planes);
     if (a.act == TTT_ACT_SILU) group_apply_kernel<TIO, V, TTT_ACT_SILU><<<grid, 256, 0, s>>>(a, h.parts);
     else if (a.act == TTT_ACT_GELU) group_apply_kernel<TIO, V, TTT_ACT_GELU><<<grid, 256, 0, s>>>(a, h.parts);
     else group_apply_kernel<TIO, V, TTT_ACT_NONE><<<grid, 256, 0, s>>>(a, h.parts);
@@ -910,9 +930,9 @@ hipError_t fwd_as(const GroupArgs& a, const Shape& h, hipStream_t s)
 template <typename TIO, int V, int ACT>
 void slab_bwd(const GroupBwdArgs& a, const Shape& h, float* planes, float* means, hipStream_t s)
 {
-    const dim3 grid((unsigned)(h.x * a.N), h.parts);
+    const dim3 grid = slab_grid(h, a.N);
     group_sums_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, planes);
-    group_means_kernel<<<(unsigned)(a.N * a.G), 256, 0, s>>>(a, h.parts, planes, means);
+    group_means_kernel<<<workgroups(a.N * a.G), 256, 0, s>>>(a, h.parts, planes, means);
     group_dx_kernel<TIO, V, ACT><<<grid, 256, 0, s>>>(a, h.parts, means);
 }
 
@@ -930,6 +950,8 @@ hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
             else if (h.wide == 4) columns<TIO, 4>(a, h, planes, s);
             else if (h.wide == 2) columns<TIO, 2>(a, h, planes, s);
             else columns<TIO, 1>(a, h, planes, s);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
         if (a.act == TTT_ACT_SILU) block_bwd<TIO, V, TTT_ACT_SILU>(a, h, s);
         else if (a.act == TTT_ACT_GELU) block_bwd<TIO, V, TTT_ACT_GELU>(a, h, s);
@@ -940,6 +962,8 @@ hipError_t bwd_as(const GroupBwdArgs& a, const Shape& h, hipStream_t s)
         else if (a.act == TTT_ACT_GELU) slab_bwd<TIO, V, TTT_ACT_GELU>(a, h, planes, means, s);
         else slab_bwd<TIO, V, TTT_ACT_NONE>(a, h, planes, means, s);
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (sums)
         group_planes_kernel<<<(unsigned)((2ll * a.C + 31) / 32), 1024, 0, s>>>(planes, (long long)h.planes, a.C,
                                                                             a.dweight, a.dbias);
