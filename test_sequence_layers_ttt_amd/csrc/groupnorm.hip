@@ -333,40 +333,68 @@ __device__ __forceinline__ void join_moments(float& na, float& mean, float& m2, 
     na = n;
 }
 
-// mean and squares about it of every channel over this workgroup's places; sums are taken of
-// the distance to the channel's first value, which keeps the digits of a far mean
+// mean and squares about it of every channel over this workgroup's places.  A thread takes its
+// places in runs of 16, sums of the distance to the mean of those before: with n the places so far,
+//   mean += s / n,   squares about it += q - s^2 / n.
+// That keeps the digits of a far mean, and of values behind a first one that is far from all others
+// (sums about that one over the whole run would not: n^2 / 2 roundings of its square).
 template <typename TIO, int V>
 __global__ void __launch_bounds__(256) group_moments_kernel(GroupArgs a, int parts, float* planes)
 {
+    constexpr int RUN = 16;
     const int vectors = a.C / V;
     const Slab p(vectors, V, a.N, a.S, parts);
     const TIO* X = (const TIO*)a.X + p.row * a.S * a.C;
-    float shift[V], s[V], q[V];
+    float s[V], q[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) shift[i] = s[i] = q[i] = 0.f;
+    for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+    const float mine = taken(p, p.slot);
     if (p.in && p.first + p.slot < p.last) {
+        const TIO* at = X + (p.first + p.slot) * a.C + p.ch;
+        const long long step = (long long)p.slots * a.C;
         Vec<TIO, V> x;
-        x.load(X + (p.first + p.slot) * a.C + p.ch);
+        x.load(at);
 #pragma unroll
-        for (int i = 0; i < V; ++i) shift[i] = x.at(i);
-#pragma unroll 4
-        for (long long t = p.first + p.slot + p.slots; t < p.last; t += p.slots) {
-            Vec<TIO, V> y;
-            y.load(X + t * a.C + p.ch);
+        for (int i = 0; i < V; ++i) s[i] = x.at(i);
+        const long long all = (p.last - p.first - p.slot + p.slots - 1) / p.slots;
+        for (long long done = 1; done < all;) {
+            const int run = (int)min((long long)RUN, all - done);
+            float d1[V], d2[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) d1[i] = d2[i] = 0.f;
+            auto take = [&](const Vec<TIO, V>& y) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = y.at(i) - s[i];
+                    d1[i] += d;
+                    d2[i] = fmaf(d, d, d2[i]);
+                }
+            };
+            if (run == RUN) {
+#pragma unroll
+                for (int k = 0; k < RUN; k += 4) {
+                    Vec<TIO, V> y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e].load(at += step);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) take(y[e]);
+                }
+            } else {
+                for (int k = 0; k < run; ++k) {
+                    Vec<TIO, V> y;
+                    y.load(at += step);
+                    take(y);
+                }
+            }
+            done += run;
+            const float inv = 1.f / (float)done;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float d = y.at(i) - shift[i];
+                const float d = d1[i] * inv;
+                q[i] += fmaxf(d2[i] - d1[i] * d, d2[i] * 0.f);   // (not below 0; NaN stays)
                 s[i] += d;
-                q[i] = fmaf(d, d, q[i]);
             }
         }
-    }
-    const float mine = taken(p, p.slot), inv = mine > 0.f ? 1.f / mine : 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float d = s[i] * inv;
-        q[i] = fmaxf(q[i] - s[i] * d, q[i] * 0.f);   // (not below 0; NaN stays)
-        s[i] = shift[i] + d;
     }
     float n[V];
 #pragma unroll
