@@ -7,6 +7,7 @@ the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -1033,7 +1034,8 @@ def groupnorm_fwd(X, groups: int, weight=None, bias=None, eps: float = 1e-5, act
     row's places (the axes between) and the C / groups neighbouring channels of a group,
     y = act((x - mean) / sqrt(var + eps) * weight + bias).  weight, bias: [C] fp32 or None;
     act: ACT_NONE, ACT_SILU or ACT_GELU.  [tokens, heads * d] with groups = heads norms every
-    head's output.  Returns (Y, mean, rstd): the statistics are [N, groups] fp32."""
+    head's output.  Returns (Y, mean, rstd): the statistics are [N, groups] fp32 (NaN where a
+    row has no places)."""
     import torch
     io, dev, N, S, C = _group_args(X, groups, weight, bias)
     on = _elsewhere(dev, stream)
@@ -1053,6 +1055,9 @@ def groupnorm_fwd(X, groups: int, weight=None, bias=None, eps: float = 1e-5, act
         rstd = torch.empty((N, groups), dtype=torch.float32, device=X.device)
     else:
         _match(rstd, "rstd", (N, groups), torch.float32, dev)
+    if S == 0:                 # (the library leaves the statistics of no values as they are)
+        mean.fill_(math.nan)
+        rstd.fill_(math.nan)
     L = lib()
     ws = _scratch(L.ttt_groupnorm_workspace_bytes(N, S, C, groups, io), X, workspace)
     rc = L.ttt_groupnorm_fwd(X.data_ptr(), _ptr(weight), _ptr(bias), eps, act, Y.data_ptr(),
