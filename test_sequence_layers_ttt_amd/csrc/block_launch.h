@@ -1,6 +1,6 @@
 // Internal launchers of the operators around the scan (gated recurrence, RMS norm,
-// gradient clipping, group norm, dropout).  The C ABI (api_block.cpp) validates every argument before calling
-// these; they only size grids and launch.
+// gradient clipping: validated by the C ABI in api_block.cpp; group norm, dropout: in
+// api_delta.cpp).  Arguments are valid here; these only size grids and launch.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>

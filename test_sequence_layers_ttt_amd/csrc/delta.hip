@@ -18,7 +18,7 @@ __device__ __forceinline__ double shift_up(double x, int by) { return __shfl_up(
 // of the products of keys and queries as they lie, with the operands' order chosen for it.
 // S = (I + L eta)^-1 L column tile by column tile: the four 16 x 16 diagonal blocks are
 // inverted by substitution, the tiles below follow from them in order, in fp32 throughout.
-// HBM and latency bound it: 16384 chunks of 64 features 164 us for 620 MB.
+// HBM and latency bound it: 16384 chunks of 64 features 140 us for 640 MB.
 // LDS decides how many workgroups a compute unit holds: S takes the place of the tiles, and
 // the inverted blocks stand in the tiles of L above its diagonal.
 template <typename TIO, int DK, bool BACKWARD>

@@ -30,13 +30,15 @@ struct BwdPass {
 
 // ---- gradients of a chunk ------------------------------------------------------------
 // One workgroup of four waves per chunk and head of values (where heads share keys, dQ and dK
-// go to fp32 planes that another kernel adds up).  Wave w has the gradients of tokens 16 w .. 16 w + 15, transposed: tokens
-// in the lanes, features down the result tiles.  The 64 x 64 products over the columns
-// (dZ u^T and dV u^T, both ways up) come out as operands of what follows, as they lie.
+// go to fp32 planes that another kernel adds up).  Wave w has the gradients of tokens
+// 16 w .. 16 w + 15, transposed: tokens in the lanes, features down the result tiles.  The 64 x 64
+// products over the columns (dZ u^T and dV u^T, both ways up) come out as operands of what
+// follows, as they lie.
 // The planes that the scans left (U, F, and the states and their gradients) are taken 32
 // columns at a time: each is loaded once, split into parts by the wave that loads it and
 // handed to the others as operands in LDS, while the next 32 columns are on their way (8 x 12 x
-// 2048 tokens of 64 features 130 us, 398 us when every wave read and split the planes by itself).
+// 2048 tokens of 64 features 124 us, 398 us when every wave read and split the planes by itself;
+// 134 us with the decays' gradients from the pairs across each token).
 template <typename TIO, int DK>
 __global__ void __launch_bounds__(256) delta_grads_kernel(BwdPass q_)
 {

@@ -321,7 +321,8 @@ __device__ __forceinline__ void zero_halves(quad* to, int tid, int threads)
 // A scan's workgroup: CW waves that compute, 16 columns of values each, and as many that load;
 // four waves that do both where registers do not allow eight, and in the backward pass (BACK), whose
 // triangular operands then come in parts from memory (both scans at 8 x 12 x 2048 tokens of 64
-// features 145 us so, 188 us with waves apart; forward 277 and 257 us a run at 1 x 32 x 32768).
+// features 133 us so, 188 us with waves apart; the whole forward call at 1 x 32 x 32768 694 us with
+// waves apart, 838 us with four that do both).
 template <typename TIO, int DK, int CW, bool BACK>
 constexpr bool kApart = CW == 2 || (!BACK && sizeof(TIO) == 2 && DK <= 64);
 template <typename TIO, int DK, int CW, bool BACK>

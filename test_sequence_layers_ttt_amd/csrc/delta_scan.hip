@@ -5,10 +5,10 @@
 // the result tiles of one product are, as they lie in registers, operands of the next, and only
 // what all waves need goes through LDS.  A workgroup has 32 or 64 columns of a head.  A chunk's data
 // is loaded to registers one or two chunks ahead and goes to the other LDS buffer while this one is
-// worked on: one barrier a chunk.  What bounds a chunk (64 features: 2.5 us with 32 columns and the
-// card half empty, 4.0 us with 64 and the card full) is that each computing wave reads every operand
-// from LDS for its own 16 columns (56 KB), and its 650 vector instructions, most of which split
-// operands into parts, next to 120 matrix products of 16 cycles.
+// worked on: one barrier a chunk.  What bounds a chunk (64 features: 2.7 us with 32 columns and the
+// card half empty, 4.1 us with 64 and the card full) is that each computing wave reads every operand
+// from LDS for its own 16 columns (62 KB), and its 500 vector instructions, most of which split
+// operands into parts, next to 144 matrix products of 16 cycles.
 //
 // The reverse scan needs nothing of the forward one, so in a backward pass both run at once.
 // Where there are too few heads for the card, each sequence is cut into segments.  First the
@@ -57,7 +57,8 @@ __device__ __forceinline__ float* start_of(const DeltaPass& a, int local, int se
 // Z comes out with its columns down the lanes (operands the other way round): 8-byte stores.
 template <typename TIO, int DK, int KEEP, int CW, bool BACK>
 struct Forward {
-    static constexpr int NZ = KEEP == kRead ? 3 : 0;   // parts of P
+    // parts of P: fp32 products behind a bf16 Z too (two parts: 111 us for 119 at 8 x 12 x 2048)
+    static constexpr int NZ = KEEP == kRead ? 3 : 0;
     typedef ChunkTiles<TIO, DK, NZ, KEEP == kRead, CW> Tiles;
     static constexpr int NB = kBuffers<Tiles>;
     static constexpr bool APART = kApart<TIO, DK, CW, BACK>, PARTS = BACK && CW == 4;
@@ -601,7 +602,7 @@ hipError_t launch_delta_scans(const DeltaPass& p, const DeltaBwdArgs* o, hipStre
 // features, us a chunk) 4.0 with 64 columns and 2.6 with 32, where the workgroup's waves meet less
 // in LDS; where only ends are found 2.3 and 1.8.  The ends and the second run cost 2 / segments of
 // the sequence where they fit at once, so segments pay from few heads on (1 x 32 heads of 64
-// features, 32768 tokens: the whole call 2.05 ms, in 8 segments 0.69 ms).
+// features, 32768 tokens: the whole call 2.05 ms, in 8 segments 0.70 ms).
 DeltaCut delta_cut(int heads, int chunks, int dv, int dk, bool backward)
 {
     const long long sides = backward ? 2 : 1, cus = 256;

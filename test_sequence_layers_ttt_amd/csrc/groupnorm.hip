@@ -8,14 +8,14 @@
 //   rows    one place (S = 1: the norm of every head's output of every token) and at most 64 vectors
 //           a group: it stays in registers, every input is read once, and a thread keeps the same
 //           channels for all its rows, so weight and bias (and the backward pass's sums) stay in
-//           registers too.  HBM bounds it: 16384 x 2048 bf16 in 32 groups with SiLU 32 us forward
+//           registers too.  HBM bounds it: 16384 x 2048 bf16 in 32 groups with SiLU 33 us forward
 //           (134 MB), 49 us backward (201 MB) and 5 us for the sums.
 //   blocks  up to 4096 vectors a group: 16 to 512 threads hold it in registers, read once as well
 //           (16384 x 4096 bf16 in one group 52 us forward; as a slab 769 us); the sums for weight
 //           and bias take a second read, channel by channel.
 //   slabs   larger ones: the places are shared out over the workgroups, each thread with channels
 //           of its own: sums per channel first, then a workgroup per group joins them, then a
-//           second read writes the result (8 x 4096 x 640 bf16 16, 5 and 21 us).
+//           second read writes the result (8 x 4096 x 640 bf16 17, 4 and 20 us).
 //
 // Sums run in a fixed order: the same bits on every call.
 #include <algorithm>
